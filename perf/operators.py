@@ -17,6 +17,7 @@ import torch
 own = False
 
 IGNORE = -100
+UNSCORED = 0.06  # share of positions without a target
 EPS = 1e-5
 DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
 
@@ -157,7 +158,7 @@ def prepare(case, seed):
         target = (torch.exp(u * math.log(vocab)) - 1).long().clamp_(0, vocab - 1)
         lean = 2.5 * torch.rand(rows, 1, device="cuda", generator=g)
         s["x"] = (randn(rows, d) + lean * s["W"][target].float()).bfloat16()
-        target[torch.rand(rows, device="cuda", generator=g) < 0.06] = IGNORE
+        target[torch.rand(rows, device="cuda", generator=g) < UNSCORED] = IGNORE
         s["target"] = target
         s["nll"] = torch.empty(rows, device="cuda")
         s["lse"] = torch.empty(rows, device="cuda")
@@ -219,7 +220,7 @@ def _plain_xent(s):
     top = z.amax(1, keepdim=True)
     e = torch.exp(z - top)
     total = e.sum(1, keepdim=True)
-    lse = (top + torch.log(total))[:, 0]
+    lse = torch.where(counted, (top + torch.log(total))[:, 0], 0.0)
     nll = torch.where(counted, lse - z.gather(1, at)[:, 0], 0.0)
     n = counted.sum().clamp(min=1).float()
     loss = (nll.sum() / n)[None]
@@ -283,10 +284,12 @@ def work(case):
         return {"bytes": n * d * (2 * sx + sy + (sx if case["res"] else 0)) + d * (sw + 8) + 8 * n, "flops": 14 * n * d}
     if case["op"] == "xent":
         n, d, v = case["rows"], case["d"], case["vocab"]
-        read = 2 * n * d + 2 * v * d + 8 * n
+        scored = (1 - UNSCORED) * n
+        read = 2 * scored * d + 2 * v * d + 8 * n
         if not case["grad"]:
-            return {"bytes": read + 8 * n, "flops": 2 * n * v * d}
-        return {"bytes": 2 * read, "flops": 6 * n * v * d}  # logits, dx and dW: one product each
+            return {"bytes": read + 8 * n, "flops": 2 * scored * v * d}
+        # logits, dx and dW: one product each
+        return {"bytes": read + 8 * n + 2 * n * d + 2 * v * d, "flops": 6 * scored * v * d}
     shapes = _shapes(case)
     each = sum(n * (2 if t == "bf16" else 4) for n, t in shapes)
     # read for the norm, then read and written scaled; what the second read finds in the cache is not taken off
@@ -316,8 +319,9 @@ def exact(case, seed):
     if case["op"] == "xent":
         x, W, target = s["x"].double(), s["W"].double(), s["target"]
         z = torch.mm(x, W.T)
-        lse = torch.logsumexp(z, dim=1)
         rows = torch.nonzero(target != IGNORE)[:, 0]
+        lse = torch.zeros(len(target), dtype=torch.float64, device="cuda")
+        lse[rows] = torch.logsumexp(z[rows], dim=1)
         nll = torch.zeros_like(lse)
         nll[rows] = lse[rows] - z[rows, target[rows]]
         n = max(1, len(rows))
