@@ -54,7 +54,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
 
+// 2^x by the special-function unit (about 2 ulp; results below 2^-126 are 0).
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // ------------------------------------------------------------ warp sums --
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
 
 // After this, lane u holds the sum over all 32 lanes of v[u] (in v[0]): a
 // butterfly where each step keeps the half of the values that belongs to the
@@ -301,6 +316,19 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
+}
+
+// One fp32 column of the accumulator for the warp's 32 TMEM lanes.
+__device__ __forceinline__ uint32_t tmem_ld1_wait(uint32_t taddr)
+{
+    uint32_t r;
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(r)
+        : "r"(taddr)
+        : "memory");
+    return r;
 }
 
 // ------------------------------------------------- CTA pairs (cta_group::2) --

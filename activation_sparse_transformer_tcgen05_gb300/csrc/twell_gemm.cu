@@ -19,6 +19,12 @@
 //                    (gate > 0) of the tile in ascending order.
 //   GEMM_DENSE       plain bf16 output (optional bias and ReLU): the dense
 //                    baseline layer.
+//   GEMM_SPLITK      fp32 partial products over parts of a long depth (CTA
+//                    pairs only), summed by the caller's next kernel.
+//   GEMM_XENT        A = hidden rows, B = the head's rows (one per word), CTA
+//                    pairs only: per (row, 256 words) the logits' maximum and
+//                    sum of exponentials, and 16-bit codes of the logits; the
+//                    logits themselves are never written.
 //
 // Warp roles (192 threads, one CTA per SM, persistent over tiles):
 //   warp 0     TMA producer: 128-byte-swizzled A/B tiles into a STAGES-deep ring
@@ -221,6 +227,101 @@ __device__ __forceinline__ void epi_dense_row(uint32_t tbase, int row, int rowsA
                 a.colsum[(size_t)rt * a.ldc + col] = ((s_col[c] + s_col[BN + c]) + s_col[2 * BN + c]) + s_col[3 * BN + c];
         }
     }
+}
+
+// Split-K epilogue of one accumulator row (one thread): the fp32 values as they are.
+template <int BN>
+__device__ __forceinline__ void epi_partial_row(uint32_t tbase, int row, int rowsA, int nb, const GemmArgs& a,
+                                                float* __restrict__ out)
+{
+    const bool row_ok = row < rowsA;
+#pragma unroll 1
+    for (int ch = 0; ch < BN / 32; ++ch) {
+        uint32_t v[32];
+        tmem_ld32_wait(tbase + ch * 32, v);
+        if (!row_ok) continue;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+            const int col = nb * BN + ch * 32 + g * 4;
+            if (col < a.rowsB)
+                *reinterpret_cast<uint4*>(out + (size_t)row * a.ldo + col) =
+                    make_uint4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
+        }
+    }
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Cross-entropy epilogue of one accumulator row (one thread) and 256 columns
+// (words). Two readings of the accumulator: the maximum m, then, with
+// m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0, the sum of 2^t and the
+// code round(-2048 t). A logit is kept as its distance to the maximum on a
+// logarithmic scale, in steps of 2^-11: the exponential rebuilt from a code is
+// off by at most 2^(2^-12) - 1 = 1.7e-4, a twentieth of its later rounding to
+// bf16 (up to 2^-8). Codes end 32 powers of two below the maximum; what is below
+// counts as zero in the gradient (not in the sum). Rounding to the integer is the
+// addition of 2^23, whose low mantissa bits are then the code.
+template <bool FULL>
+__device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row, int rowsA, int nb, int ncols,
+                                             const GemmArgs& a, int lane)
+{
+    const bool row_ok = row < rowsA;
+    if (!__any_sync(0xffffffffu, row_ok)) return;  // the warp's rows are all past the last one
+    constexpr int NCH = kXentTile / 32;
+    float m = -INFINITY;
+#pragma unroll 1
+    for (int ch = 0; ch < NCH; ++ch) {
+        if (!FULL && ch * 32 >= ncols) break;
+        uint32_t v[32];
+        tmem_ld32_wait(tbase + ch * 32, v);
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (FULL || ch * 32 + c < ncols) m = fmaxf(m, __uint_as_float(v[c]));
+    }
+    // no finite logit in the tile: the sum is 0 and every code the zero code
+    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kLog2e);
+    const float magic = 8388608.f;
+    float sum[2] = {0.f, 0.f};
+    uint16_t* out = a.codes ? a.codes + (size_t)(row_ok ? row : 0) * a.ldcode + (size_t)nb * kXentTile : nullptr;
+#pragma unroll 1
+    for (int ch = 0; ch < NCH; ++ch) {
+        if (!FULL && ch * 32 >= ncols) break;
+        uint32_t v[32];
+        tmem_ld32_wait(tbase + ch * 32, v);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            float t = fmaf(__uint_as_float(v[c]), kLog2e, -m2);
+            if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
+            sum[c & 1] += exp2_approx(t);
+            v[c] = __float_as_uint(fminf(fmaf(t, -kXentSteps, magic), magic + (float)kXentZero));
+        }
+        if (out && row_ok) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                uint4 o;
+                o.x = __byte_perm(v[g * 8 + 0], v[g * 8 + 1], 0x5410);
+                o.y = __byte_perm(v[g * 8 + 2], v[g * 8 + 3], 0x5410);
+                o.z = __byte_perm(v[g * 8 + 4], v[g * 8 + 5], 0x5410);
+                o.w = __byte_perm(v[g * 8 + 6], v[g * 8 + 7], 0x5410);
+                *reinterpret_cast<uint4*>(out + ch * 32 + g * 8) = o;
+            }
+        }
+    }
+    // the target's logit: one column read back for each lane whose target is in this tile
+    int tcol = -1;
+    if (row_ok) {
+        const int t = a.target[row] - nb * kXentTile;
+        if (t >= 0 && t < ncols) tcol = t;
+    }
+    uint32_t mine = __ballot_sync(0xffffffffu, tcol >= 0);
+    while (mine) {
+        const int l = __ffs(mine) - 1;
+        mine &= mine - 1;
+        const uint32_t z = tmem_ld1_wait(tbase + (uint32_t)__shfl_sync(0xffffffffu, tcol, l));
+        if (lane == l) a.ztarget[row] = __uint_as_float(z);
+    }
+    if (row_ok)
+        a.xstat[(size_t)row * a.NB + nb] = make_float2(m == -INFINITY ? -INFINITY : m2, sum[0] + sum[1]);
 }
 
 template <int BN, int MODE, int STAGES, int CAP = BN, int KSUB = 1>
@@ -564,8 +665,10 @@ template <int MODE, int STAGES, int CAP = PAIR_N, bool A_MN = false, bool B_MN =
 __global__ void __launch_bounds__(192, 1)
     k_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const GemmArgs a)
 {
-    static_assert(MODE == GEMM_TWELL_RELU || MODE == GEMM_DENSE, "row-wise epilogues only");
-    static_assert(MODE == GEMM_DENSE || (!A_MN && !B_MN), "MN-major operands: dense epilogue only");
+    static_assert(MODE != GEMM_GATE_SWAP, "row-wise epilogues only");
+    static_assert(MODE == GEMM_DENSE || MODE == GEMM_SPLITK || (!A_MN && !B_MN),
+                  "MN-major operands: dense epilogues only");
+    constexpr bool SPLIT = MODE == GEMM_SPLITK;
     using L = PairLayout<STAGES>;
     constexpr uint32_t IDESC =
         idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
@@ -627,7 +730,9 @@ __global__ void __launch_bounds__(192, 1)
     const int num_m = (rowsA + PAIR_M - 1) / PAIR_M;
     const int num_n = (a.rowsB + PAIR_N - 1) / PAIR_N;
     const int num_kb = (gemm_k(a) + BK - 1) / BK;  // same in both CTAs
-    const int num_tiles = num_kb > 0 ? num_m * num_n : 0;  // no k-block: nothing to add or store
+    const int mn_tiles = num_m * num_n;
+    // no k-block: nothing to add or store
+    const int num_tiles = num_kb > 0 ? (SPLIT ? mn_tiles * a.k_splits : mn_tiles) : 0;
     const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -640,8 +745,10 @@ __global__ void __launch_bounds__(192, 1)
             bool ok = true;
             for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
                 int mb, nb;
-                pair_tile_coords(tile, num_m, num_n, &mb, &nb);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                pair_tile_coords(SPLIT ? tile % mn_tiles : tile, num_m, num_n, &mb, &nb);
+                const int kb0 = SPLIT ? tile / mn_tiles * a.kb_per_split : 0;
+                const int kb1 = SPLIT ? min(kb0 + a.kb_per_split, num_kb) : num_kb;
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
@@ -693,7 +800,9 @@ __global__ void __launch_bounds__(192, 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PAIR_N);
-                for (int kb = 0; kb < num_kb; ++kb) {
+                const int kb0 = SPLIT ? tile / mn_tiles * a.kb_per_split : 0;
+                const int kb1 = SPLIT ? min(kb0 + a.kb_per_split, num_kb) : num_kb;
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&full[stage], phase, abort_flag)) {
                         ok = false;
                         break;
@@ -704,7 +813,7 @@ __global__ void __launch_bounds__(192, 1)
                     const uint64_t bdesc = operand_desc(B_MN, sa + L::A_BYTES);
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, (kb | k) != 0);
+                        umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, ((kb - kb0) | k) != 0);
                     umma_commit_pair(&empty[stage], 0x3);
                     if (++stage == STAGES) {
                         stage = 0;
@@ -729,9 +838,9 @@ __global__ void __launch_bounds__(192, 1)
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < num_tiles; tile += num_pairs) {
             int mb, nb;
-            pair_tile_coords(tile, num_m, num_n, &mb, &nb);
+            pair_tile_coords(SPLIT ? tile % mn_tiles : tile, num_m, num_n, &mb, &nb);
             named_bar_sync(1, kEpiThreads);  // previous tile's shared-memory reads are done
-            for (int c = et; c < PAIR_N; c += kEpiThreads) {
+            if constexpr (MODE != GEMM_XENT) for (int c = et; c < PAIR_N; c += kEpiThreads) {
                 const int col = nb * PAIR_N + c;
                 float bv;
                 if (MODE == GEMM_TWELL_RELU)
@@ -748,6 +857,15 @@ __global__ void __launch_bounds__(192, 1)
             const int row = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
             if constexpr (MODE == GEMM_TWELL_RELU)
                 epi_twell_row<PAIR_N, CAP>(tbase, row, rowsA, nb, a, bias_sm);
+            else if constexpr (MODE == GEMM_XENT) {
+                const int ncols = min(kXentTile, a.rowsB - nb * PAIR_N);
+                if (ncols == kXentTile)
+                    epi_xent_row<true>(tbase, row, rowsA, nb, ncols, a, lane);
+                else
+                    epi_xent_row<false>(tbase, row, rowsA, nb, ncols, a, lane);
+            } else if constexpr (SPLIT)
+                epi_partial_row<PAIR_N>(tbase, row, rowsA, nb, a,
+                                        a.out_f32 + (size_t)(tile / mn_tiles) * a.split_stride);
             else
                 epi_dense_row<PAIR_N>(tbase, row, rowsA, nb, a, bias_sm, s_col, 2 * mb + (int)rank, q, et);
             tc_fence_before();
@@ -791,12 +909,12 @@ EncodeTiledFn encode_fn()
 }
 
 // [rows, K] bf16 row-major, box = 64 (K) x box_rows, 128-byte swizzle, zero fill.
-bool make_map(CUtensorMap* m, const void* ptr, int rows, int K, int box_rows)
+bool make_map(CUtensorMap* m, const void* ptr, int rows, int K, int box_rows, int ld = 0)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : K) * 2};
     cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
@@ -822,12 +940,12 @@ cudaError_t run(const uint16_t* A, const uint16_t* B, const GemmArgs& a, int tok
 
 // Clusters of two that can be resident at once for this kernel (0 = none).
 // [K, mn] bf16 row-major (an MN-major operand), box = 64 (MN) x 64 (K), 128-byte swizzle, zero fill.
-bool make_map_mn(CUtensorMap* m, const void* ptr, int mn, int K)
+bool make_map_mn(CUtensorMap* m, const void* ptr, int mn, int K, int ld = 0)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)mn, (cuuint64_t)K};
-    cuuint64_t strides[1] = {(cuuint64_t)mn * 2};
+    cuuint64_t strides[1] = {(cuuint64_t)(ld ? ld : mn) * 2};
     cuuint32_t box[2] = {(cuuint32_t)kMnBox, (cuuint32_t)BK};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
@@ -879,10 +997,11 @@ cudaError_t run_pair(const uint16_t* A, const uint16_t* B, const GemmArgs& a, cu
     const int cap = pair_capacity<MODE, STAGES, CAP, A_MN, B_MN>(cfg);
     if (cap <= 0) return cudaSuccess;
     CUtensorMap ma, mb;
-    const bool ok_a = A_MN ? make_map_mn(&ma, A, a.rowsA, a.K) : make_map(&ma, A, a.rowsA, a.K, HALF);
+    const bool ok_a = A_MN ? make_map_mn(&ma, A, a.rowsA, a.K, a.lda) : make_map(&ma, A, a.rowsA, a.K, HALF, a.lda);
     const bool ok_b = B_MN ? make_map_mn(&mb, B, a.rowsB, a.K) : make_map(&mb, B, a.rowsB, a.K, HALF);
     if (!ok_a || !ok_b) return cudaErrorInvalidValue;
-    const int tiles = ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + PAIR_N - 1) / PAIR_N);
+    const int tiles = ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + PAIR_N - 1) / PAIR_N) *
+                      (MODE == GEMM_SPLITK ? a.k_splits : 1);
     cfg.gridDim = dim3(2 * (tiles < cap ? tiles : cap), 1, 1);
     count_launches(1);
     *launched = true;
@@ -934,6 +1053,15 @@ cudaError_t launch_gemm(int mode, const uint16_t* A, const uint16_t* B, const Ge
                 e = run_pair<GEMM_DENSE, 6, PAIR_N, false, true>(A, B, a, s, &launched);
             else
                 e = run_pair<GEMM_DENSE, 6, PAIR_N, true, false>(A, B, a, s, &launched);
+            if (e != cudaSuccess) return e;
+            return launched ? cudaSuccess : cudaErrorNotSupported;
+        }
+        case GEMM_SPLITK:
+        case GEMM_XENT: {
+            bool launched = false;
+            const cudaError_t e = mode == GEMM_XENT
+                                      ? run_pair<GEMM_XENT, 6>(A, B, a, s, &launched)
+                                      : run_pair<GEMM_SPLITK, 6, PAIR_N, false, true>(A, B, a, s, &launched);
             if (e != cudaSuccess) return e;
             return launched ? cudaSuccess : cudaErrorNotSupported;
         }

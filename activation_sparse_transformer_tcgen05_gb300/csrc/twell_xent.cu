@@ -1,0 +1,558 @@
+// twell_xent.cu — softmax cross entropy of a linear head over a large
+// vocabulary, with its gradient, without the logits.
+//
+//   z = x W^T          x [N, d] hidden rows, W [V, d] the head, one row per word
+//   lse_r = log sum_j exp z_rj,   nll_r = lse_r - z_r,target(r)
+//   dz_rj = g (exp(z_rj - lse_r) - [j = target(r)])
+//   dx = dz W,  dW = dz^T x
+//
+// Three products of 2 N V d operations bound it. The softmax needs a whole row
+// before its first gradient, so a gradient without stored logits either
+// computes the logits twice (a fourth product) or keeps something smaller. What
+// is kept here, for one chunk of rows at a time, are 16-bit codes of the
+// logits' distances to their (row, 256 words) maximum, written by the first
+// product's epilogue (twell_gemm.cu). One pass rewrites the codes in place as
+// bf16 dz, the operand of the two other products. Six bytes a logit cost
+// 0.9 ps at the memory's rate, a fourth product d * 1.03 fs: the codes cost
+// less from d = 860 on, and they round dz once, as any bf16 operand is.
+//
+// Rows that are not scored (target == ignore_index) take no part: the scored
+// rows are copied together first, so that a prompt or padding costs nothing in
+// the products and whatever stands there (NaN too) reaches no gradient.
+//
+//   k_xent_prep    orders the rows (scored first), counts them, checks the targets
+//   k_xent_gather  the scored rows of x together; zeros for the others
+//   GEMM_XENT      codes, per-(row, 256 words) maxima and sums, target logits
+//   k_xent_lse     one warp per row: lse, nll
+//   k_xent_dz      codes -> bf16 dz, in place
+//   GEMM_SPLITK    dx; with few output tiles the vocabulary (its depth) is split
+//                  over the GPU and k_xent_dx adds the parts in order
+//   GEMM_DENSE     dW (operands read MN-major, nothing is transposed)
+//   k_xent_loss    the sum or mean of the losses
+// Every sum is taken in a fixed order.
+#include "common.cuh"
+#include "launch.h"
+
+namespace twell {
+namespace {
+
+constexpr int kPrepThreads = 1024;
+constexpr int kPairsNominal = 76;  // CTA pairs the split of dx is planned for (152 SMs)
+constexpr int kMaxSplits = 32;
+
+struct XentWs {
+    int32_t* count;     // scored rows
+    float* gscale;      // gradient factor of a scored row
+    int32_t* rows_dev;  // [chunks] scored rows of each chunk
+    int32_t* k_dev;     // [chunks] the same as a depth of dW (at least 1 in chunk 0, so that dW is written)
+    int32_t* perm;      // [N] scored rows ascending, then the others
+    int32_t* target;    // [N] targets of the scored rows, in perm's order
+    uint16_t* xs;       // [N, d] scored rows of x, zeros in the 64 rows after them
+    float2* stat;       // [chunk, tiles] (maximum in log2 units, sum relative to it)
+    float* ztarget;     // [chunk]
+    float* lse2;        // [chunk] log2 of the sum of exponentials
+    float* nll;         // [chunk]
+    uint16_t* codes;    // [chunk, ldcode] codes, then bf16 dz
+    float* parts;       // [splits, chunk, d] partial dx
+    float* dw_acc;      // [V, d] when a bf16 dW is summed over several chunks
+};
+
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+
+// Row stride of the codes: whole 128-byte lines.
+size_t code_stride(int V) { return ((size_t)V + 63) & ~size_t(63); }
+
+// Parts of the depth V of dx = dz W: each (256 x 256 tile, part) is one unit of
+// work of a CTA pair; the time is the waves of units times a unit's k-blocks
+// plus its epilogue (about 8 k-blocks' worth), and what the parts' fp32 sums
+// cost to write and read again. One part writes dx directly.
+int plan_splits(int rows, int d, int V, int* kb_per)
+{
+    const long long tiles = (long long)((rows + 255) / 256) * ((d + 255) / 256);
+    const int num_kb = (V + 63) / 64;
+    int best = 1, best_per = num_kb;
+    double best_t = 1e30;
+    for (int s = 1; s <= kMaxSplits && s <= num_kb; ++s) {
+        const int per = (num_kb + s - 1) / s;
+        if ((num_kb + per - 1) / per != s) continue;  // an empty part
+        const long long waves = (tiles * s + kPairsNominal - 1) / kPairsNominal;
+        // 0.28 us a k-block; the parts move 8 bytes an element at ~5 TB/s
+        double t = (double)waves * (per + 8) * 0.28;
+        if (s > 1) t += (double)s * rows * d * 8 / 5e6 + 3.0;
+        if (t < best_t) {
+            best_t = t;
+            best = s;
+            best_per = per;
+        }
+    }
+    *kb_per = best_per;
+    return best;
+}
+
+size_t parts_rows(int rows, int d, int V)
+{
+    int per;
+    const int splits = rows > 0 ? plan_splits(rows, d, V, &per) : 1;
+    return splits > 1 ? (size_t)splits * rows : 0;
+}
+
+size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, XentWs* out)
+{
+    char* base = static_cast<char*>(ws);
+    size_t used = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base ? base + used : nullptr;
+        used += round256(bytes);
+        return p;
+    };
+    const size_t tiles = (size_t)(V + kXentTile - 1) / kXentTile;
+    const size_t chunks = chunk > 0 ? ((size_t)N + chunk - 1) / chunk : 0;
+    XentWs w{};
+    w.count = reinterpret_cast<int32_t*>(take(4));
+    w.gscale = reinterpret_cast<float*>(take(4));
+    w.rows_dev = reinterpret_cast<int32_t*>(take(chunks * 4));
+    w.k_dev = reinterpret_cast<int32_t*>(take(chunks * 4));
+    w.perm = reinterpret_cast<int32_t*>(take((size_t)N * 4));
+    w.target = reinterpret_cast<int32_t*>(take((size_t)N * 4));
+    w.xs = reinterpret_cast<uint16_t*>(take((size_t)N * d * 2));
+    w.stat = reinterpret_cast<float2*>(take((size_t)chunk * tiles * 8));
+    w.ztarget = reinterpret_cast<float*>(take((size_t)chunk * 4));
+    w.lse2 = reinterpret_cast<float*>(take((size_t)chunk * 4));
+    w.nll = reinterpret_cast<float*>(take((size_t)chunk * 4));
+    if (grad) {
+        w.codes = reinterpret_cast<uint16_t*>(take((size_t)chunk * code_stride(V) * 2));
+        // full chunks and the last, shorter one are each planned on their own
+        const size_t full = parts_rows(chunk, d, V), last = parts_rows(chunk > 0 ? N % chunk : 0, d, V);
+        w.parts = reinterpret_cast<float*>(take((full > last ? full : last) * d * 4));
+        if (acc) w.dw_acc = reinterpret_cast<float*>(take((size_t)V * d * 4));
+    }
+    if (out) *out = w;
+    return used;
+}
+
+// Inclusive sum over the lanes of a warp.
+__device__ __forceinline__ int warp_scan(int v, int lane)
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += u;
+    }
+    return v;
+}
+
+// Order of the rows: scored ones ascending, then the others. One block, each
+// thread a run of consecutive rows: their counts are scanned, then each thread
+// places its rows.
+__global__ void __launch_bounds__(kPrepThreads)
+    k_xent_prep(const int64_t* __restrict__ target, int N, int V, int64_t ignore_index, int chunk, int mean,
+                float grad_scale, XentWs w, int32_t* status)
+{
+    const int run = (N + kPrepThreads - 1) / kPrepThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long first = (long long)threadIdx.x * run;
+    const int i0 = (int)(first < N ? first : N), i1 = (int)(first + run < N ? first + run : N);
+    int n = 0;
+    bool bad = false;
+    for (int i = i0; i < i1; ++i) {
+        const int64_t t = target[i];
+        if (t == ignore_index) continue;
+        ++n;
+        bad |= t < 0 || t >= V;
+    }
+    if (bad) set_error(status, TWELL_ERR_INVALID_ARG);
+    const int incl = warp_scan(n, lane);
+    __shared__ int part[kPrepThreads / 32], before[kPrepThreads / 32], total_s;
+    if (lane == 31) part[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const int p = part[lane];
+        const int pi = warp_scan(p, lane);
+        before[lane] = pi - p;
+        if (lane == 31) total_s = pi;
+    }
+    __syncthreads();
+    const int total = total_s;
+    int at = before[warp] + incl - n;   // scored rows before this run
+    int other = total + (i0 - at);      // place of the run's first unscored row
+    for (int i = i0; i < i1; ++i) {
+        const int64_t t = target[i];
+        if (t == ignore_index) {
+            w.perm[other++] = i;
+        } else {
+            w.target[at] = (int32_t)t;
+            w.perm[at++] = i;
+        }
+    }
+    for (long long c = threadIdx.x; c * chunk < N; c += kPrepThreads) {
+        const long long left = (long long)total - c * chunk;
+        const int rows = (int)(left < 0 ? 0 : left < chunk ? left : chunk);
+        w.rows_dev[c] = rows;
+        w.k_dev[c] = rows == 0 && c == 0 ? 1 : rows;
+    }
+    if (threadIdx.x == 0) {
+        *w.count = total;
+        *w.gscale = mean ? grad_scale / (float)(total > 0 ? total : 1) : grad_scale;
+    }
+}
+
+// Row i of the order, one warp per row: scored rows of x together, zeros in the
+// 64 rows after them (the depth of dW is read in steps of 64), and zero results
+// for the rows that are not scored.
+__global__ void __launch_bounds__(256)
+    k_xent_gather(const uint16_t* __restrict__ x, int N, int d, XentWs w, float* __restrict__ nll,
+                  float* __restrict__ lse, uint16_t* __restrict__ dx, const int32_t* status)
+{
+    if (has_error(status)) return;
+    const int lane = threadIdx.x & 31, d8 = d / 8;
+    const int count = *w.count;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (long long i = blockIdx.x * 8 + (threadIdx.x >> 5); i < N; i += gridDim.x * 8) {
+        const int row = w.perm[i];
+        uint4* to = reinterpret_cast<uint4*>(w.xs + (size_t)i * d);
+        if (i < count) {
+            const uint4* from = reinterpret_cast<const uint4*>(x + (size_t)row * d);
+            for (int c = lane; c < d8; c += 32) to[c] = from[c];
+            continue;
+        }
+        if (i < (long long)count + 64)
+            for (int c = lane; c < d8; c += 32) to[c] = zero;
+        if (dx)
+            for (int c = lane; c < d8; c += 32) reinterpret_cast<uint4*>(dx + (size_t)row * d)[c] = zero;
+        if (lane == 0) {
+            nll[row] = 0.f;
+            lse[row] = 0.f;
+        }
+    }
+}
+
+// One warp per scored row: the tiles' (maximum, sum) pairs joined, in the order
+// of the lanes' strides and then a butterfly.
+__global__ void __launch_bounds__(256)
+    k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ perm,
+               float* __restrict__ nll, float* __restrict__ lse, const int32_t* status)
+{
+    if (has_error(status)) return;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= *rows_dev) return;
+    float m = -INFINITY;
+    const float2* st = w.stat + (size_t)row * tiles;
+    for (int t = lane; t < tiles; t += 32) m = fmaxf(m, st[t].x);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    // every logit -inf: the sum stays 0 and lse is -inf; a maximum of +inf or a
+    // NaN logit leaves a NaN sum, and with it a NaN loss and gradient row
+    float s = 0.f;
+    for (int t = lane; t < tiles; t += 32) {
+        const float2 v = st[t];
+        if (v.x != -INFINITY || v.y != 0.f) s += v.y * exp2_approx(v.x - m);
+    }
+    s = warp_sum(s);
+    if (lane != 0) return;
+    const double l = s == 0.f ? -INFINITY : (double)m * 0.69314718055994530942 + (double)logf(s);
+    const float loss = (float)(l - (double)w.ztarget[row]);
+    lse[perm[row]] = (float)l;
+    nll[perm[row]] = loss;
+    w.nll[row] = loss;
+    w.lse2[row] = (float)(l * 1.4426950408889634074);
+}
+
+// Codes to bf16 dz in place, one warp per (row, 256 words):
+// dz = g 2^(m2 - q / 2048 - lse2). The target's entry is g (p - 1) =
+// g expm1(-nll), which stays exact where p is close to 1. A row without a
+// finite lse is NaN throughout.
+__global__ void __launch_bounds__(256)
+    k_xent_dz(XentWs w, size_t ldcode, int tiles, const int32_t* __restrict__ target,
+              const int32_t* __restrict__ rows_dev, int max_rows, const int32_t* status)
+{
+    if (has_error(status)) return;
+    const int lane = threadIdx.x & 31;
+    const int rows = *rows_dev;
+    const int padded = min(max_rows, max((rows + 63) / 64 * 64, 64));  // zeros up to the depth dW reads
+    const float g = *w.gscale;
+    const size_t total = (size_t)padded * tiles;
+    for (size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (size_t)gridDim.x * 8) {
+        const int row = (int)(i / tiles), nb = (int)(i % tiles);
+        const int col = nb * kXentTile + lane * 8;
+        if ((size_t)col >= ldcode) continue;
+        uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + col);
+        if (row >= rows) {
+            *p = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 q = *p;
+        const float l2 = w.lse2[row];
+        const float shift = w.stat[i].x - l2;
+        const float gg = isfinite(l2) ? g : NAN;
+        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t c = (e & 1) ? qw[e >> 1] >> 16 : qw[e >> 1] & 0xffffu;
+            f[e] = c == kXentZero ? 0.f : exp2_approx(fmaf((float)c, -1.f / kXentSteps, shift));
+            f[e] *= gg;
+        }
+        const int t = target[row] - col;
+        if (t >= 0 && t < 8) {
+            const float ft = gg * expm1f(-w.nll[row]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e == t) f[e] = ft;
+        }
+        *p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                        pack_bf16x2(f[6], f[7]));
+    }
+}
+
+// dx = bf16 of the parts added in order, each scored row at its place.
+__global__ void __launch_bounds__(256)
+    k_xent_dx(const float* __restrict__ parts, int splits, size_t stride, const int32_t* __restrict__ rows_dev, int d,
+              const int32_t* __restrict__ perm, uint16_t* __restrict__ dx, const int32_t* status)
+{
+    if (has_error(status)) return;
+    const int d4 = d / 4;
+    const size_t n4 = (size_t)*rows_dev * d4;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
+        float4 a = reinterpret_cast<const float4*>(parts)[i];
+        for (int p = 1; p < splits; ++p) {
+            const float4 b = reinterpret_cast<const float4*>(parts + p * stride)[i];
+            a.x += b.x;
+            a.y += b.y;
+            a.z += b.z;
+            a.w += b.w;
+        }
+        const size_t row = i / d4, c = i % d4;
+        reinterpret_cast<uint2*>(dx + (size_t)perm[row] * d)[c] =
+            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    }
+}
+
+// dW in bf16 from the sum over chunks; n4 groups of four elements.
+__global__ void __launch_bounds__(256)
+    k_xent_round(const float* __restrict__ acc, size_t n4, uint16_t* __restrict__ out, const int32_t* status)
+{
+    if (has_error(status)) return;
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
+        const float4 a = reinterpret_cast<const float4*>(acc)[i];
+        reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    }
+}
+
+// Sum or mean of the losses, one block, fixed order, in 64 bits.
+__global__ void __launch_bounds__(kPrepThreads)
+    k_xent_loss(const float* __restrict__ nll, int N, const int32_t* __restrict__ count, int mean, float* loss,
+                const int32_t* status)
+{
+    if (has_error(status)) return;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < N; i += kPrepThreads) s += (double)nll[i];
+    __shared__ double part[kPrepThreads];
+    part[threadIdx.x] = s;
+    for (int half = kPrepThreads / 2; half >= 1; half >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < half) part[threadIdx.x] += part[threadIdx.x + half];
+    }
+    if (threadIdx.x == 0) {
+        const int n = *count;
+        *loss = n == 0 ? 0.f : (float)(mean ? part[0] / (double)n : part[0]);
+    }
+}
+
+int sms_current()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return n;
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool dims_ok(int N, int d, int V) { return N >= 0 && d > 0 && V > 0 && d % 8 == 0; }
+
+unsigned blocks_for(size_t work, size_t per_block, int sms)
+{
+    const size_t b = (work + per_block - 1) / per_block, most = (size_t)sms * 16;
+    return (unsigned)(b < 1 ? 1 : b < most ? b : most);
+}
+
+struct Grads {
+    float scale;
+    uint16_t* dx;
+    void* dW;  // null: losses only
+    int dw_type, accumulate;
+};
+
+// One chunk's gradients, after its losses: dz, dx, and its share of dW.
+cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int rows, int d, int V, const Grads& g,
+                        int sms, int32_t* status, cudaStream_t s)
+{
+    const int tiles = (V + kXentTile - 1) / kXentTile;
+    const size_t ldcode = code_stride(V);
+    count_launches(1);
+    k_xent_dz<<<blocks_for((size_t)rows * tiles, 8, sms), 256, 0, s>>>(w, ldcode, tiles, w.target + r0, w.rows_dev + c,
+                                                                       rows, status);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+
+    int per = 0;
+    const int splits = plan_splits(rows, d, V, &per);
+    GemmArgs g2{};
+    g2.rowsA = rows;
+    g2.rowsA_dev = w.rows_dev + c;
+    g2.rowsB = d;
+    g2.K = V;
+    g2.lda = (int)ldcode;
+    g2.b_mn = 1;
+    g2.ldo = d;
+    g2.status = status;
+    if (splits == 1) {
+        g2.out = g.dx;
+        g2.row_map = w.perm + r0;
+        e = launch_gemm(GEMM_DENSE, w.codes, W, g2, sms, s);
+    } else {
+        g2.k_splits = splits;
+        g2.kb_per_split = per;
+        g2.split_stride = (size_t)rows * d;
+        g2.out_f32 = w.parts;
+        e = launch_gemm(GEMM_SPLITK, w.codes, W, g2, sms, s);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+        k_xent_dx<<<blocks_for((size_t)rows * d / 4, 256, sms), 256, 0, s>>>(
+            w.parts, splits, g2.split_stride, w.rows_dev + c, d, w.perm + r0, g.dx, status);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+
+    GemmArgs g3{};
+    g3.rowsA = V;
+    g3.rowsB = d;
+    g3.K = rows;
+    g3.K_dev = w.k_dev + c;
+    g3.lda = (int)ldcode;
+    g3.a_mn = 1;
+    g3.b_mn = 1;
+    g3.ldo = d;
+    g3.status = status;
+    if (w.dw_acc || g.dw_type == TWELL_F32) {
+        g3.out_f32 = w.dw_acc ? w.dw_acc : static_cast<float*>(g.dW);
+        g3.accumulate = r0 > 0 || (!w.dw_acc && g.accumulate);
+    } else {
+        g3.out = static_cast<uint16_t*>(g.dW);
+    }
+    return launch_gemm(GEMM_DENSE, w.codes, w.xs + (size_t)r0 * d, g3, sms, s);
+}
+
+// Both entry points: losses, and with g.dW the gradients.
+cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target, int N, int d, int V,
+                     int64_t ignore_index, int mean, int chunk, float* nll, float* lse, float* loss, const Grads& g,
+                     void* ws, int32_t* status, cudaStream_t s)
+{
+    const int sms = sms_current();
+    if (sms <= 0) return cudaErrorInvalidDevice;
+    const bool grad = g.dW != nullptr;
+    XentWs w{};
+    carve(ws, N, chunk, d, V, grad, grad && g.dw_type == TWELL_BF16 && chunk < N, &w);
+    const int tiles = (V + kXentTile - 1) / kXentTile;
+    count_launches(1);
+    k_xent_prep<<<1, kPrepThreads, 0, s>>>(target, N, V, ignore_index, chunk > 0 ? chunk : 1, mean, g.scale, w, status);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (N > 0) {
+        count_launches(1);
+        k_xent_gather<<<blocks_for((size_t)N, 8, sms), 256, 0, s>>>(x, N, d, w, nll, lse, g.dx, status);
+        e = cudaGetLastError();
+    } else if (grad && !g.accumulate) {
+        e = cudaMemsetAsync(g.dW, 0, (size_t)V * d * (g.dw_type == TWELL_F32 ? 4 : 2), s);
+    }
+    for (int r0 = 0, c = 0; r0 < N && e == cudaSuccess; r0 += chunk, ++c) {
+        const int rows = N - r0 < chunk ? N - r0 : chunk;
+        GemmArgs g1{};
+        g1.rowsA = rows;
+        g1.rowsA_dev = w.rows_dev + c;
+        g1.rowsB = V;
+        g1.K = d;
+        g1.NB = tiles;
+        g1.codes = w.codes;
+        g1.ldcode = code_stride(V);
+        g1.xstat = w.stat;
+        g1.target = w.target + r0;
+        g1.ztarget = w.ztarget;
+        g1.status = status;
+        e = launch_gemm(GEMM_XENT, w.xs + (size_t)r0 * d, W, g1, sms, s);
+        if (e != cudaSuccess) return e;
+        count_launches(1);
+        k_xent_lse<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(w, tiles, w.rows_dev + c, w.perm + r0, nll, lse, status);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && grad) e = chunk_grads(w, W, r0, c, rows, d, V, g, sms, status, s);
+        if (rows < chunk) break;  // the last chunk; r0 + chunk may pass the range of int
+    }
+    if (e == cudaSuccess && w.dw_acc) {
+        const size_t n4 = (size_t)V * d / 4;
+        count_launches(1);
+        k_xent_round<<<blocks_for(n4, 256, sms), 256, 0, s>>>(w.dw_acc, n4, static_cast<uint16_t*>(g.dW), status);
+        e = cudaGetLastError();
+    }
+    if (e == cudaSuccess) {
+        count_launches(1);
+        k_xent_loss<<<1, kPrepThreads, 0, s>>>(nll, N, w.count, mean, loss, status);
+        e = cudaGetLastError();
+    }
+    return e;
+}
+
+int chunk_of(int N, int chunk_rows) { return chunk_rows == 0 || chunk_rows > N ? N : chunk_rows; }
+
+bool type_ok(int t) { return t == TWELL_BF16 || t == TWELL_F32; }
+
+}  // namespace
+}  // namespace twell
+
+using namespace twell;
+
+extern "C" size_t twell_xent_fwd_workspace_bytes(int N, int d, int V)
+{
+    if (!dims_ok(N, d, V)) return 0;
+    return carve(nullptr, N, N, d, V, false, false, nullptr);
+}
+
+extern "C" size_t twell_xent_bwd_workspace_bytes(int N, int d, int V, int chunk_rows, int dw_type)
+{
+    if (!dims_ok(N, d, V) || chunk_rows < 0 || !type_ok(dw_type)) return 0;
+    const int chunk = chunk_of(N, chunk_rows);
+    return carve(nullptr, N, chunk, d, V, true, dw_type == TWELL_BF16 && chunk < N, nullptr);
+}
+
+extern "C" twell_status twell_xent_fwd(const uint16_t* x, const uint16_t* W, const int64_t* target, int N, int d,
+                                       int V, int64_t ignore_index, int mean, float* nll, float* lse, float* loss,
+                                       void* ws, size_t ws_bytes, int32_t* status, void* stream)
+{
+    if (!dims_ok(N, d, V) || !W || !loss || !status || (N > 0 && (!x || !target || !nll || !lse)))
+        return TWELL_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(target, 8)) return TWELL_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < twell_xent_fwd_workspace_bytes(N, d, V)) return TWELL_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return TWELL_ERR_INVALID_ARG;
+    const cudaError_t e = run_xent(x, W, target, N, d, V, ignore_index, mean, N, nll, lse, loss, Grads{}, ws, status,
+                                   static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+extern "C" twell_status twell_xent_fwd_bwd(const uint16_t* x, const uint16_t* W, const int64_t* target, int N, int d,
+                                           int V, int64_t ignore_index, int mean, float grad_scale, int chunk_rows,
+                                           float* nll, float* lse, float* loss, uint16_t* dx, void* dW, int dw_type,
+                                           int accumulate, void* ws, size_t ws_bytes, int32_t* status, void* stream)
+{
+    if (!dims_ok(N, d, V) || chunk_rows < 0 || !type_ok(dw_type) || (accumulate && dw_type != TWELL_F32))
+        return TWELL_ERR_INVALID_ARG;
+    if (!W || !loss || !status || !dW || (N > 0 && (!x || !target || !nll || !lse || !dx)))
+        return TWELL_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(W, 16) || !aligned(target, 8) || !aligned(dx, 16) || !aligned(dW, 16))
+        return TWELL_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < twell_xent_bwd_workspace_bytes(N, d, V, chunk_rows, dw_type)) return TWELL_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return TWELL_ERR_INVALID_ARG;
+    const Grads g{grad_scale, dx, dW, dw_type, accumulate};
+    const cudaError_t e = run_xent(x, W, target, N, d, V, ignore_index, mean, chunk_of(N, chunk_rows), nll, lse, loss,
+                                   g, ws, status, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}

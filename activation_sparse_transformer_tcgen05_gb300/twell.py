@@ -27,7 +27,13 @@ EXPORTED_SYMBOLS = (
     "twell_set_kernel_timer", "twell_hybrid_up_pack", "twell_hybrid_spmm_down",
     "twell_hybrid_ffn_fwd", "twell_fwd_workspace_bytes", "twell_hybrid_bwd_workspace_bytes", "twell_hybrid_ffn_bwd",
     "twell_wait_selftest", "twell_spmm_down_tc_workspace_bytes", "twell_spmm_down_tc",
+    "twell_layernorm_fwd", "twell_layernorm_bwd", "twell_layernorm_bwd_workspace_bytes",
+    "twell_xent_fwd", "twell_xent_fwd_bwd", "twell_xent_fwd_workspace_bytes", "twell_xent_bwd_workspace_bytes",
+    "twell_grad_clip", "twell_grad_clip_workspace_bytes",
 )
+
+# Element type codes (twell_dtype).
+DTYPE_BF16, DTYPE_F32 = 0, 1
 
 # Call sites of twell_set_kernel_timer.
 (SITE_NONE, SITE_UP_GEMM, SITE_SPMM_DOWN, SITE_SDDMM, SITE_DX, SITE_CSC, SITE_WGRAD, SITE_DECODE_TAIL,
@@ -55,10 +61,16 @@ class _TwellOverflow(ctypes.Structure):
                 ("rows", ctypes.c_void_p), ("dense", ctypes.c_void_p)]
 
 
+class _TwellTensorList(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("inp", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("numel", ctypes.c_void_p), ("type", ctypes.c_void_p)]
+
+
 _lib = None
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 BUFP = ctypes.POINTER(_TwellBuf)
 OVP = ctypes.POINTER(_TwellOverflow)
+TLP = ctypes.POINTER(_TwellTensorList)
 
 
 def load_library(path: str | None = None):
@@ -117,6 +129,24 @@ def load_library(path: str | None = None):
     lib.twell_hybrid_ffn_bwd.argtypes = [P, P, P, P, BUFP, OVP, P, I32, F32, P, P, P, P, P, SZ, P, P]
     lib.twell_wait_selftest.restype = I32
     lib.twell_wait_selftest.argtypes = [I32, P, P, P]
+    lib.twell_layernorm_fwd.restype = I32
+    lib.twell_layernorm_fwd.argtypes = [P, I64, P, I64, P, P, I64, I32, F32, I32, I32, I32, P, I64, P, I64, P, P, P]
+    lib.twell_layernorm_bwd_workspace_bytes.restype = SZ
+    lib.twell_layernorm_bwd_workspace_bytes.argtypes = [I64, I32]
+    lib.twell_layernorm_bwd.restype = I32
+    lib.twell_layernorm_bwd.argtypes = [P, I64, P, I64, P, P, P, P, I64, I64, I32, I32, I32, I32, P, I64, P, P, P, SZ, P]
+    lib.twell_xent_fwd_workspace_bytes.restype = SZ
+    lib.twell_xent_fwd_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.twell_xent_bwd_workspace_bytes.restype = SZ
+    lib.twell_xent_bwd_workspace_bytes.argtypes = [I32, I32, I32, I32, I32]
+    lib.twell_xent_fwd.restype = I32
+    lib.twell_xent_fwd.argtypes = [P, P, P, I32, I32, I32, I64, I32, P, P, P, P, SZ, P, P]
+    lib.twell_xent_fwd_bwd.restype = I32
+    lib.twell_xent_fwd_bwd.argtypes = [P, P, P, I32, I32, I32, I64, I32, F32, I32, P, P, P, P, P, I32, I32, P, SZ, P, P]
+    lib.twell_grad_clip_workspace_bytes.restype = SZ
+    lib.twell_grad_clip_workspace_bytes.argtypes = []
+    lib.twell_grad_clip.restype = I32
+    lib.twell_grad_clip.argtypes = [TLP, F32, P, P, SZ, P]
     lib.twell_check.restype = I32
     lib.twell_check.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
     _lib = lib
@@ -389,6 +419,155 @@ def twell_dense_ffn_bwd(x, W_up, W_down, h_dense, dy, l1: float, dx, dW_up, dW_d
         _ptr(dW_up, "dW_up", bytes_per_elem=4, numel=F * d), _ptr(dW_down, "dW_down", bytes_per_elem=4, numel=F * d),
         _ptr(db, "db", bytes_per_elem=4, numel=F), _ptr(ws, "ws"), ws.numel() * ws.element_size(),
         _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_dense_ffn_bwd")
+
+
+def _dtype(t: torch.Tensor, name: str) -> int:
+    if t.dtype is torch.bfloat16 or t.dtype is torch.int16:
+        return DTYPE_BF16
+    if t.dtype is torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"{name} must be bfloat16 (or its int16 bits) or float32, got {t.dtype}")
+
+
+def _rows(t: torch.Tensor | None, name: str, N: int, d: int, dtype: int):
+    """(pointer, row stride) of an [N, d] matrix with unit column stride."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or t.shape[0] != N or t.shape[1] != d or (d > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a [{N}, {d}] matrix with unit column stride")
+    if _dtype(t, name) != dtype:
+        raise ValueError(f"{name} has another element type ({t.dtype}) than the tensors it goes with")
+    return t.data_ptr(), t.stride(0) if N > 1 else d
+
+
+def _vec(t: torch.Tensor | None, name: str, n: int, dtype: int):
+    """Pointer of a contiguous vector of n elements."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must have {n} contiguous elements")
+    if _dtype(t, name) != dtype:
+        raise ValueError(f"{name} has the wrong element type ({t.dtype})")
+    return t.data_ptr()
+
+
+def twell_layernorm_fwd(x, res, w, b, eps: float, sum_out, y, mean, rstd, stream=None):
+    """y = LN(x + res) w + b; sum_out = x + res (res and sum_out: both or neither). w, b, mean, rstd may be None."""
+    if x.dim() != 2 or y.dim() != 2:
+        raise ValueError("x and y must be matrices")
+    N, d = x.shape
+    tx, ty = _dtype(x, "x"), _dtype(y, "y")
+    tw = _dtype(w, "w") if w is not None else _dtype(b, "b") if b is not None else DTYPE_F32
+    px, ldx = _rows(x, "x", N, d, tx)
+    pr, ldr = _rows(res, "res", N, d, tx)
+    ps, lds = _rows(sum_out, "sum_out", N, d, tx)
+    py, ldy = _rows(y, "y", N, d, ty)
+    _check(load_library().twell_layernorm_fwd(
+        px, ldx, pr, ldr, _vec(w, "w", d, tw), _vec(b, "b", d, tw), N, d, eps, tx, ty, tw, ps, lds, py, ldy,
+        _vec(mean, "mean", N, DTYPE_F32), _vec(rstd, "rstd", N, DTYPE_F32), _stream(stream)), "twell_layernorm_fwd")
+
+
+def twell_layernorm_bwd_workspace_bytes(N: int, d: int) -> int:
+    return int(load_library().twell_layernorm_bwd_workspace_bytes(N, d))
+
+
+def twell_layernorm_bwd(dy, x, w, mean, rstd, dres, dx, dw, db, ws, stream=None):
+    """Backward of twell_layernorm_fwd; x is the normalised sum. dres (the residual's gradient, added to dx), w, and
+    dw with db may be None."""
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    N, d = x.shape
+    tx, ty = _dtype(x, "x"), _dtype(dy, "dy")
+    tw = _dtype(w, "w") if w is not None else DTYPE_F32
+    pg, ldg = _rows(dy, "dy", N, d, ty)
+    px, ldx = _rows(x, "x", N, d, tx)
+    pr, ldr = _rows(dres, "dres", N, d, tx)
+    pd, ldd = _rows(dx, "dx", N, d, tx)
+    _check(load_library().twell_layernorm_bwd(
+        pg, ldg, px, ldx, _vec(w, "w", d, tw), _vec(mean, "mean", N, DTYPE_F32), _vec(rstd, "rstd", N, DTYPE_F32), pr, ldr,
+        N, d, tx, ty, tw, pd, ldd, _vec(dw, "dw", d, DTYPE_F32), _vec(db, "db", d, DTYPE_F32), _ptr(ws, "ws"),
+        ws.numel() * ws.element_size(), _stream(stream)), "twell_layernorm_bwd")
+
+
+def twell_xent_fwd_workspace_bytes(N: int, d: int, V: int) -> int:
+    return int(load_library().twell_xent_fwd_workspace_bytes(N, d, V))
+
+
+def twell_xent_bwd_workspace_bytes(N: int, d: int, V: int, chunk_rows: int, dw_type: int) -> int:
+    return int(load_library().twell_xent_bwd_workspace_bytes(N, d, V, chunk_rows, dw_type))
+
+
+def _xent_inputs(x, W, target, nll, lse, loss):
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError("x [N, d] and W [V, d] must be matrices of the same width")
+    N, d = x.shape
+    V = W.shape[0]
+    if target.dtype is not torch.int64:
+        raise ValueError(f"target must be int64, got {target.dtype}")
+    return (N, d, V, _vec(x, "x", N * d, DTYPE_BF16), _vec(W, "W", V * d, DTYPE_BF16),
+            _ptr(target, "target", bytes_per_elem=8, numel=N), _vec(nll, "nll", N, DTYPE_F32),
+            _vec(lse, "lse", N, DTYPE_F32), _vec(loss, "loss", 1, DTYPE_F32))
+
+
+def twell_xent_fwd(x, W, target, ignore_index: int, mean: bool, nll, lse, loss, ws, status, stream=None):
+    """Cross entropy of the head x W^T: nll and lse per row, loss their sum or mean over the scored rows."""
+    N, d, V, px, pw, pt, pn, pl, po = _xent_inputs(x, W, target, nll, lse, loss)
+    _check(load_library().twell_xent_fwd(px, pw, pt, N, d, V, ignore_index, int(mean), pn, pl, po, _ptr(ws, "ws"),
+                                         ws.numel() * ws.element_size(), _ptr(status, "status", bytes_per_elem=4),
+                                         _stream(stream)), "twell_xent_fwd")
+
+
+def twell_xent_fwd_bwd(x, W, target, ignore_index: int, mean: bool, grad_scale: float, chunk_rows: int, nll, lse, loss,
+                       dx, dW, accumulate: bool, ws, status, stream=None):
+    """twell_xent_fwd and the gradients dx (bf16) and dW (bf16 or fp32) of grad_scale * loss."""
+    N, d, V, px, pw, pt, pn, pl, po = _xent_inputs(x, W, target, nll, lse, loss)
+    tw = _dtype(dW, "dW")
+    _check(load_library().twell_xent_fwd_bwd(
+        px, pw, pt, N, d, V, ignore_index, int(mean), grad_scale, chunk_rows, pn, pl, po,
+        _vec(dx, "dx", N * d, DTYPE_BF16), _vec(dW, "dW", V * d, tw), tw, int(accumulate), _ptr(ws, "ws"),
+        ws.numel() * ws.element_size(), _ptr(status, "status", bytes_per_elem=4), _stream(stream)),
+        "twell_xent_fwd_bwd")
+
+
+class TwellTensorList:
+    """Device tensors of bf16 or fp32 (contiguous) with the C struct naming them, for twell_grad_clip; outs: the tensors
+    the results go to (default: the same ones). Keeps the tensors alive; their memory must stay where it is."""
+
+    def __init__(self, tensors, outs=None):
+        self.tensors = list(tensors)
+        self.outs = self.tensors if outs is None else list(outs)
+        n = len(self.tensors)
+        if len(self.outs) != n:
+            raise ValueError(f"{n} tensors but {len(self.outs)} outs")
+        for i, (t, o) in enumerate(zip(self.tensors, self.outs)):
+            if not (t.is_cuda and o.is_cuda and t.is_contiguous() and o.is_contiguous()):
+                raise ValueError(f"tensor {i} and its out must be contiguous CUDA tensors")
+            if _dtype(t, f"tensor {i}") != _dtype(o, f"out {i}") or t.numel() != o.numel():
+                raise ValueError(f"out {i} must have its tensor's type and number of elements")
+        self._in = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.tensors])
+        self._out = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.outs])
+        self._numel = (ctypes.c_int64 * n)(*[t.numel() for t in self.tensors])
+        self._type = (ctypes.c_int32 * n)(*[_dtype(t, "tensor") for t in self.tensors])
+        self.struct = _TwellTensorList(n, ctypes.addressof(self._in), ctypes.addressof(self._out),
+                                       ctypes.addressof(self._numel), ctypes.addressof(self._type))
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def twell_grad_clip_workspace_bytes() -> int:
+    return int(load_library().twell_grad_clip_workspace_bytes())
+
+
+def twell_grad_clip(tensors: TwellTensorList, max_norm: float, norm, ws, stream=None):
+    """norm = the L2 norm over all tensors; outs = tensors * min(1, max_norm / norm)."""
+    _check(load_library().twell_grad_clip(tensors.ref, max_norm, _vec(norm, "norm", 1, DTYPE_F32), _ptr(ws, "ws"),
+                                          ws.numel() * ws.element_size(), _stream(stream)), "twell_grad_clip")
 
 
 def twell_check(status: torch.Tensor, stream=None) -> int:

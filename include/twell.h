@@ -80,6 +80,9 @@ typedef struct twell_buf {
     uint16_t* val;
 } twell_buf;
 
+/* Element types of the tensors that take more than one. */
+typedef enum twell_dtype { TWELL_BF16 = 0, TWELL_F32 = 1 } twell_dtype;
+
 /* Operation codes for twell_workspace_bytes. */
 enum { TWELL_OP_PACK = 0, TWELL_OP_SPMM_DOWN = 1, TWELL_OP_FFN_FWD = 2,
        TWELL_OP_FFN_BWD = 3, TWELL_OP_GATED_FWD = 4, TWELL_OP_HYBRID_FWD = 5 };
@@ -359,6 +362,102 @@ twell_status twell_dense_ffn_bwd(const uint16_t* x, const uint16_t* W_up, const 
 twell_status twell_ffn_fwd_static_ws(const uint16_t* x, const uint16_t* W_up, const uint16_t* W_gate,
                                      const float* b, const uint16_t* W_down, int M, int d, int F, int T,
                                      const twell_buf* h_out, uint16_t* y, int32_t* status, void* stream);
+
+/*
+ * Layer norm around the feed-forward layer. Rows of d elements; row strides
+ * (ld*) in elements, >= d, of any alignment (aligned rows whose d is a multiple
+ * of 8 are read in 16-byte pieces). x_type is the type of the residual stream
+ * (x, res, sum, dres, dx), y_type that of y and dy, w_type that of w and b; each
+ * TWELL_BF16 or TWELL_F32. w or b may be NULL (1 and 0). N >= 0, d >= 1.
+ * Statistics and sums are fp32; outputs are rounded once. Outputs must not
+ * overlap inputs (the call rejects equal pointers).
+ *
+ * twell_layernorm_fwd
+ *   s    = x + res, rounded to x_type and written to sum (res and sum both NULL: s = x)
+ *   mean = mean of the row of s, rstd = 1 / sqrt(variance + eps) (biased variance)
+ *   y    = (s - mean) rstd w + b
+ *   mean, rstd [N] fp32 (the backward's inputs); both may be NULL.
+ */
+twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const void* res, int64_t ldres, const void* w,
+                                 const void* b, int64_t N, int d, float eps, int x_type, int y_type, int w_type,
+                                 void* sum, int64_t ldsum, void* y, int64_t ldy, float* mean, float* rstd,
+                                 void* stream);
+
+/*
+ * twell_layernorm_bwd — with hat = (x - mean) rstd and v = w dy:
+ *   dx = rstd (v - mean(v) - hat mean(v hat)) + dres   (dres NULL: 0)
+ *   dw = sum over rows of dy hat, db = sum over rows of dy   [d] fp32
+ *   x: the forward's normalised rows (its sum, if there was a residual); mean,
+ *   rstd: the forward's. dw and db may both be NULL. The rows are summed in a
+ *   fixed order (no atomics).
+ *   ws: at least twell_layernorm_bwd_workspace_bytes(N, d) bytes, 256-byte aligned.
+ */
+size_t twell_layernorm_bwd_workspace_bytes(int64_t N, int d);
+twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w,
+                                 const float* mean, const float* rstd, const void* dres, int64_t lddres, int64_t N,
+                                 int d, int x_type, int y_type, int w_type, void* dx, int64_t lddx, float* dw,
+                                 float* db, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Softmax cross entropy of a linear head over a vocabulary of V words:
+ *   z = x W^T, lse_r = log sum_j exp z_rj, nll_r = lse_r - z_r,target(r),
+ *   loss = sum of nll over the scored rows, or with mean != 0 their mean.
+ * Rows whose target is ignore_index are not scored: their nll, lse and dx are 0
+ * and they take no part in dW, whatever x holds there. No scored row: loss 0,
+ * zero gradients. A target outside [0, V) that is not ignore_index sets
+ * *status = TWELL_ERR_INVALID_ARG and the outputs are then unspecified.
+ *   x [N, d] bf16, W [V, d] bf16 (one row per word), target [N] int64;
+ *   nll, lse [N] fp32, loss [1] fp32. N >= 0, V >= 1, d % 8 == 0.
+ * The logits are never stored: twell_xent_fwd keeps a maximum and a sum for
+ * every (row, 256 words).
+ *
+ * twell_xent_fwd_bwd also gives the gradients of grad_scale * loss:
+ *   dz_rj = g (exp(z_rj - lse_r) - [j = target(r)]), g = grad_scale (/ scored rows)
+ *   dx = dz W [N, d] bf16; dW = dz^T x [V, d], bf16 or fp32 (dw_type); with
+ *   accumulate != 0 (fp32 only) dW += dz^T x.
+ * dz enters the products as a bf16 operand (like any operand of the tensor
+ * cores); sums are fp32. The rows are worked through chunk_rows at a time (0: all
+ * at once); a chunk keeps 2 bytes per (row, word) in the workspace, and a bf16
+ * dW over several chunks 4 bytes per (word, d).
+ *   ws: at least twell_xent_fwd_workspace_bytes(N, d, V), or
+ *   twell_xent_bwd_workspace_bytes(N, d, V, chunk_rows, dw_type), 256-byte
+ *   aligned. Runs on CTA pairs (TWELL_ERR_CUDA if a cluster of two cannot be
+ *   launched).
+ */
+size_t twell_xent_fwd_workspace_bytes(int N, int d, int V);
+size_t twell_xent_bwd_workspace_bytes(int N, int d, int V, int chunk_rows, int dw_type);
+twell_status twell_xent_fwd(const uint16_t* x, const uint16_t* W, const int64_t* target, int N, int d, int V,
+                            int64_t ignore_index, int mean, float* nll, float* lse, float* loss, void* ws,
+                            size_t ws_bytes, int32_t* status, void* stream);
+twell_status twell_xent_fwd_bwd(const uint16_t* x, const uint16_t* W, const int64_t* target, int N, int d, int V,
+                                int64_t ignore_index, int mean, float grad_scale, int chunk_rows, float* nll,
+                                float* lse, float* loss, uint16_t* dx, void* dW, int dw_type, int accumulate,
+                                void* ws, size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * twell_grad_clip — L2 norm over many tensors, and the tensors scaled so that it
+ * is at most max_norm:
+ *   norm = sqrt(sum of g^2 over all elements), c = min(1, max_norm / norm),
+ *   out = c g, rounded once to the tensor's type.
+ * out[i] may be in[i] (then nothing is written while c = 1) or a tensor that
+ * overlaps no input. max_norm >= 0; INFINITY gives the norm alone (in place). A NaN
+ * norm makes every written element NaN; an infinite one makes finite elements 0.
+ *   list: host struct of host arrays (read during the call): n tensors, device
+ *   addresses, element counts (>= 0) and twell_dtype codes; tensors are
+ *   contiguous and aligned to their element size. norm [1] fp32 device.
+ *   ws: at least twell_grad_clip_workspace_bytes() bytes, 256-byte aligned.
+ *   Limit of this build: 32768 tensors (TWELL_ERR_UNSUPPORTED).
+ */
+typedef struct twell_tensor_list {
+    int32_t n;
+    const void* const* in;
+    void* const* out;
+    const int64_t* numel;
+    const int32_t* type;
+} twell_tensor_list;
+size_t twell_grad_clip_workspace_bytes(void);
+twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                             void* stream);
 
 /*
  * twell_set_kernel_timer — measurement hook. While set, every launch of the
