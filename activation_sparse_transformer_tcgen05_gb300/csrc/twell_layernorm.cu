@@ -4,6 +4,8 @@
 //   forward   s = x + res, hat = (s - mean) rstd, y = hat w + b
 //   backward  v = w dy, dx = rstd (v - mean(v) - hat mean(v hat)) + dres,
 //             dw = sum_r dy hat, db = sum_r dy
+#include <string.h>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -28,6 +30,7 @@ struct FwdArgs {
     int d;
     float eps;
     float *mean, *rstd;
+    bool w_f32;
 };
 
 struct BwdArgs {
@@ -38,10 +41,18 @@ struct BwdArgs {
     const float *mean, *rstd;
     float* part;  // [parts, 2, d] partial sums of dw and db; null: not wanted
     int parts;
+    bool w_f32;
 };
 
 constexpr int kRowThreads = 256;
 constexpr int kMaxParts = 304;
+
+// Element i of a weight vector of either type; `none` where there is no vector.
+__device__ __forceinline__ float weight(const void* p, int i, bool f32, float none)
+{
+    if (!p) return none;
+    return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
+}
 
 // Sums of a and b over the block; every thread gets them.
 __device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf)
@@ -60,12 +71,10 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* buf)
 }
 
 // One block per row, the row read three times (from L2 after the first).
-template <class TX, class TY, class TW>
+template <class TX, class TY>
 __global__ void __launch_bounds__(kRowThreads) k_ln_fwd_long(const FwdArgs a)
 {
     __shared__ float2 buf[kRowThreads / 32];
-    const typename TW::type* w = static_cast<const typename TW::type*>(a.w);
-    const typename TW::type* b = static_cast<const typename TW::type*>(a.b);
     for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
         const typename TX::type* x = static_cast<const typename TX::type*>(a.x) + r * a.ldx;
         const typename TX::type* res = a.res ? static_cast<const typename TX::type*>(a.res) + r * a.ldres : nullptr;
@@ -90,7 +99,7 @@ __global__ void __launch_bounds__(kRowThreads) k_ln_fwd_long(const FwdArgs a)
         const float rstd = 1.f / sqrtf(block_sum2(q, 0.f, buf).x / (float)a.d + a.eps);
         for (int i = threadIdx.x; i < a.d; i += kRowThreads) {
             const float hat = (TX::load(from + i) - mean) * rstd;
-            TY::store(y + i, fmaf(hat, w ? TW::load(w + i) : 1.f, b ? TW::load(b + i) : 0.f));
+            TY::store(y + i, fmaf(hat, weight(a.w, i, a.w_f32, 1.f), weight(a.b, i, a.w_f32, 0.f)));
         }
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = mean;
@@ -100,11 +109,10 @@ __global__ void __launch_bounds__(kRowThreads) k_ln_fwd_long(const FwdArgs a)
 }
 
 // dx, one block per row, the row read twice.
-template <class TX, class TY, class TW>
+template <class TX, class TY>
 __global__ void __launch_bounds__(kRowThreads) k_ln_bwd_long(const BwdArgs a)
 {
     __shared__ float2 buf[kRowThreads / 32];
-    const typename TW::type* w = static_cast<const typename TW::type*>(a.w);
     for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
         const typename TX::type* x = static_cast<const typename TX::type*>(a.x) + r * a.ldx;
         const typename TX::type* dres = a.dres ? static_cast<const typename TX::type*>(a.dres) + r * a.lddres : nullptr;
@@ -114,7 +122,7 @@ __global__ void __launch_bounds__(kRowThreads) k_ln_bwd_long(const BwdArgs a)
         float s1 = 0.f, s2 = 0.f;
         for (int i = threadIdx.x; i < a.d; i += kRowThreads) {
             const float hat = (TX::load(x + i) - mean) * rstd;
-            const float v = TY::load(dy + i) * (w ? TW::load(w + i) : 1.f);
+            const float v = TY::load(dy + i) * weight(a.w, i, a.w_f32, 1.f);
             s1 += v;
             s2 += v * hat;
         }
@@ -122,7 +130,7 @@ __global__ void __launch_bounds__(kRowThreads) k_ln_bwd_long(const BwdArgs a)
         const float c1 = s.x / (float)a.d, c2 = s.y / (float)a.d;
         for (int i = threadIdx.x; i < a.d; i += kRowThreads) {
             const float hat = (TX::load(x + i) - mean) * rstd;
-            const float v = TY::load(dy + i) * (w ? TW::load(w + i) : 1.f);
+            const float v = TY::load(dy + i) * weight(a.w, i, a.w_f32, 1.f);
             float g = rstd * (v - c1 - hat * c2);
             if (dres) g += TX::load(dres + i);
             TX::store(dx + i, g);
@@ -159,20 +167,20 @@ __global__ void __launch_bounds__(256) k_ln_cols_long(const BwdArgs a)
     }
 }
 
-// dw and db: the parts of 32 columns added by eight warps (every eighth part
-// each, ascending), then the eight sums in order.
-__global__ void __launch_bounds__(256)
+// dw and db: the parts of 32 columns added by 32 warps (every 32nd part each,
+// ascending), then the 32 sums in order.
+__global__ void __launch_bounds__(1024)
     k_ln_reduce(const float* __restrict__ part, int parts, int d, float* __restrict__ dw, float* __restrict__ db)
 {
     const int i = blockIdx.x * 32 + threadIdx.x, ty = threadIdx.y;  // column of [dw | db]
     float s = 0.f;
     if (i < 2 * d)
-        for (int p = ty; p < parts; p += 8) s += part[(size_t)p * 2 * d + i];
-    __shared__ float buf[8][32];
+        for (int p = ty; p < parts; p += 32) s += part[(size_t)p * 2 * d + i];
+    __shared__ float buf[32][32];
     buf[ty][threadIdx.x] = s;
     __syncthreads();
     if (ty == 0 && i < 2 * d) {
-        for (int j = 1; j < 8; ++j) s += buf[j][threadIdx.x];
+        for (int j = 1; j < 32; ++j) s += buf[j][threadIdx.x];
         if (i < d)
             dw[i] = s;
         else
@@ -180,7 +188,496 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-int parts_for(int64_t N) { return N < kMaxParts * 8 ? (int)((N + 7) / 8) : kMaxParts; }
+// ---------------------------------------------- rows held by their threads --
+//
+// A row is held by G threads (a warp to 512 threads, 8 or 16 elements each), so
+// that it is read from memory once. Blocks stay and walk over the rows: w, b and
+// the column sums live in registers. Where rows are aligned, each thread copies
+// its 16-byte pieces of the next rows asynchronously into shared memory, where
+// only it reads them: bytes in flight without registers and without barriers.
+// Other rows are read element by element when their turn comes. The mean is
+// summed first and the variance from the centred values, which holds for rows
+// whose mean is far larger than their deviation.
+
+constexpr int kMaxGroup = 512;  // threads of a row at most: rows up to 512 * 16 = 8192 elements
+
+// VEC consecutive elements of type T as they are in memory.
+template <class T, int VEC>
+struct Piece;
+template <int VEC>
+struct Piece<bf16_t, VEC> {
+    static_assert(VEC == 8, "");
+    uint4 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+        return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+    }
+    __device__ __forceinline__ void set(const float* f)
+    {
+        v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+    }
+    __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+};
+template <>
+struct Piece<bf16_t, 1> {
+    uint16_t v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ float get(int) const { return bf16_to_f32(v); }
+    __device__ __forceinline__ void set(const float* f) { v = f32_to_bf16_bits(f[0]); }
+    __device__ __forceinline__ void store(uint16_t* p) const { *p = v; }
+};
+template <int VEC>
+struct Piece<f32_t, VEC> {
+    static_assert(VEC == 8, "");
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
+    }
+    __device__ __forceinline__ void set(const float* f)
+    {
+        a = make_float4(f[0], f[1], f[2], f[3]);
+        b = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void store(float* p) const
+    {
+        reinterpret_cast<float4*>(p)[0] = a;
+        reinterpret_cast<float4*>(p)[1] = b;
+    }
+};
+template <>
+struct Piece<f32_t, 1> {
+    float v;
+    __device__ __forceinline__ void load(const float* p) { v = *p; }
+    __device__ __forceinline__ void zero() { v = 0.f; }
+    __device__ __forceinline__ float get(int) const { return v; }
+    __device__ __forceinline__ void set(const float* f) { v = f[0]; }
+    __device__ __forceinline__ void store(float* p) const { *p = v; }
+};
+
+// Sum over the G threads of a row, the same bits in all of them: a butterfly in
+// each warp, then the warps' sums in order. `buf` alternates between two halves
+// from one sum to the next, so one barrier each is enough.
+struct RowSum {
+    float2* buf;  // [2][16]
+    int warp0, warps, bar, turn = 0;
+    __device__ RowSum(float2* b, int G) : buf(b)
+    {
+        warps = G >> 5;
+        warp0 = (threadIdx.x / G) * warps;
+        bar = 1 + threadIdx.x / G;
+    }
+    __device__ __forceinline__ float2 sum2(float x, float y)
+    {
+        x = warp_sum(x);
+        y = warp_sum(y);
+        if (warps == 1) return make_float2(x, y);
+        float2* b = buf + turn * 16;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = make_float2(x, y);
+        named_bar_sync(bar, warps * 32);
+        float2 s = b[warp0];
+        for (int i = 1; i < warps; ++i) {
+            const float2 o = b[warp0 + i];
+            s.x += o.x;
+            s.y += o.y;
+        }
+        return s;
+    }
+    __device__ __forceinline__ float sum(float x)
+    {
+        x = warp_sum(x);
+        if (warps == 1) return x;
+        float2* b = buf + turn * 16;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5].x = x;
+        named_bar_sync(bar, warps * 32);
+        float s = b[warp0].x;
+        for (int i = 1; i < warps; ++i) s += b[warp0 + i].x;
+        return s;
+    }
+};
+
+template <class T>
+__device__ __forceinline__ const typename T::type* row_of(const void* p, int64_t r, int64_t ld)
+{
+    return static_cast<const typename T::type*>(p) + r * ld;
+}
+template <class T>
+__device__ __forceinline__ typename T::type* row_of(void* p, int64_t r, int64_t ld)
+{
+    return static_cast<typename T::type*>(p) + r * ld;
+}
+
+// VEC weights as floats; `f32`: their type.
+template <int VEC>
+__device__ __forceinline__ void load_weights(const void* p, int i, bool f32, float* out)
+{
+    if (f32) {
+        Piece<f32_t, VEC> w;
+        w.load(static_cast<const float*>(p) + i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = w.get(e);
+    } else {
+        Piece<bf16_t, VEC> w;
+        w.load(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = w.get(e);
+    }
+}
+
+__device__ __forceinline__ void copy_async16(void* smem, const void* global)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copies_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// Rows on their way: STAGES rows of every stream (x; res or dy; dres), each
+// thread's own pieces side by side (16-byte words, one word of all threads after
+// the other, so that a warp's accesses fall into different banks).
+template <int STAGES, int WORDS>
+struct Ring {
+    uint4* mine;
+    int stride, stage = 0;
+    __device__ Ring(void* smem) : mine(static_cast<uint4*>(smem) + threadIdx.x), stride(blockDim.x) {}
+    static size_t bytes(int threads) { return (size_t)STAGES * WORDS * threads * 16; }
+    __device__ __forceinline__ uint4* word(int st, int k) { return mine + (size_t)(st * WORDS + k) * stride; }
+};
+
+// 16-byte words of one piece of eight elements.
+template <class T>
+constexpr int words()
+{
+    return (int)sizeof(typename T::type) / 2;
+}
+
+// Piece v of this thread as it arrived in the ring.
+template <class T, class R>
+__device__ __forceinline__ void from_ring(R& ring, int st, int k, Piece<T, 8>& p)
+{
+    uint4 w[words<T>()];
+#pragma unroll
+    for (int i = 0; i < words<T>(); ++i) w[i] = *ring.word(st, k + i);
+    memcpy(&p, w, sizeof(p));
+}
+
+template <class T, class R>
+__device__ __forceinline__ void to_ring(R& ring, int st, int k, const typename T::type* from)
+{
+#pragma unroll
+    for (int i = 0; i < words<T>(); ++i) copy_async16(ring.word(st, k + i), reinterpret_cast<const uint4*>(from) + i);
+}
+
+// Stages of the ring: rows in flight for at most 98 KB with 512 threads of 8
+// elements, so that two blocks fit an SM (16 elements of three fp32 streams:
+// 196 KB, one block).
+constexpr int stages_for(int words) { return words <= 3 ? 4 : words <= 4 ? 3 : 2; }
+
+// Blocks of 512 threads that share an SM (64 registers a thread) with 8 elements
+// a thread; with 16, one.
+constexpr int blocks_per_sm(int per) { return per == 8 ? 2 : 1; }
+
+template <class TX, int PER, bool RES>
+constexpr int fwd_words()
+{
+    return PER / 8 * words<TX>() * (RES ? 2 : 1);
+}
+
+template <class TX, class TY, int VEC, int PER, bool RES>
+__global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const FwdArgs a, int G)
+{
+    constexpr int NV = PER / VEC, WORDS = fwd_words<TX, PER, RES>(), STAGES = stages_for(WORDS);
+    extern __shared__ uint4 dyn[];
+    __shared__ float2 buf[32];
+    RowSum rs(buf, G);
+    Ring<STAGES, WORDS> ring(dyn);
+    const int t = threadIdx.x % G;
+    const float inv_d = 1.f / (float)a.d;
+    float w[PER], b[PER];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = (v * G + t) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            w[v * VEC + e] = 1.f;
+            b[v * VEC + e] = 0.f;
+        }
+        if (i < a.d && a.w) load_weights<VEC>(a.w, i, a.w_f32, w + v * VEC);
+        if (i < a.d && a.b) load_weights<VEC>(a.b, i, a.w_f32, b + v * VEC);
+    }
+    const int64_t step = (int64_t)gridDim.x * (blockDim.x / G);
+    int64_t r = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
+    auto request = [&](int st, int64_t row) {
+        if constexpr (VEC == 8) {
+            if (row < a.N) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int i = (v * G + t) * 8;
+                    if (i < a.d) {
+                        to_ring<TX>(ring, st, v * words<TX>(), row_of<TX>(a.x, row, a.ldx) + i);
+                        if (RES) to_ring<TX>(ring, st, (NV + v) * words<TX>(), row_of<TX>(a.res, row, a.ldres) + i);
+                    }
+                }
+            }
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) request(st, r + st * step);
+    int st = 0;
+    for (; r < a.N; r += step) {
+        float f[PER];
+        float s = 0.f;
+        if (VEC == 8) copies_wait<STAGES - 1>();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+            Piece<TX, VEC> x, q;
+            x.zero();
+            q.zero();
+            if (i < a.d) {
+                if constexpr (VEC == 8) {
+                    from_ring<TX>(ring, st, v * words<TX>(), x);
+                    if (RES) from_ring<TX>(ring, st, (NV + v) * words<TX>(), q);
+                } else {
+                    x.load(row_of<TX>(a.x, r, a.ldx) + i);
+                    if (RES) q.load(row_of<TX>(a.res, r, a.ldres) + i);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) f[v * VEC + e] = x.get(e);
+            if (RES) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[v * VEC + e] += q.get(e);
+                x.set(f + v * VEC);
+                if (i < a.d) x.store(row_of<TX>(a.sum, r, a.ldsum) + i);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[v * VEC + e] = x.get(e);
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s += f[v * VEC + e];
+        }
+        request(st, r + STAGES * step);
+        st = st + 1 == STAGES ? 0 : st + 1;
+        const float mean = rs.sum(s) * inv_d;
+        float c2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool in = (v * G + t) * VEC < a.d;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                f[v * VEC + e] -= mean;
+                if (in) c2 = fmaf(f[v * VEC + e], f[v * VEC + e], c2);
+            }
+        }
+        const float rstd = 1.f / sqrtf(rs.sum(c2) * inv_d + a.eps);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                f[v * VEC + e] = fmaf(f[v * VEC + e] * rstd, w[v * VEC + e], b[v * VEC + e]);
+            Piece<TY, VEC> o;
+            o.set(f + v * VEC);
+            if (i < a.d) o.store(row_of<TY>(a.y, r, a.ldy) + i);
+        }
+        if (t == 0) {
+            if (a.mean) a.mean[r] = mean;
+            if (a.rstd) a.rstd[r] = rstd;
+        }
+    }
+    if (VEC == 8) copies_wait<0>();
+}
+
+template <class TX, class TY, int PER, bool RES>
+constexpr int bwd_words()
+{
+    return PER / 8 * (words<TX>() * (RES ? 2 : 1) + words<TY>());
+}
+
+// The normalised values and w dy are formed twice from what was read (before
+// and after the row's sums): two products cost less than the registers.
+template <class TX, class TY, int VEC, int PER, bool RES>
+__global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const BwdArgs a, int G)
+{
+    constexpr int NV = PER / VEC, WORDS = bwd_words<TX, TY, PER, RES>(), STAGES = stages_for(WORDS);
+    constexpr int G0 = NV * words<TX>(), Q0 = G0 + NV * words<TY>();  // first words of dy and dres
+    extern __shared__ uint4 dyn[];
+    __shared__ float2 buf[32];
+    RowSum rs(buf, G);
+    Ring<STAGES, WORDS> ring(dyn);
+    const int t = threadIdx.x % G, groups = blockDim.x / G;
+    const float inv_d = 1.f / (float)a.d;
+    float w[PER], dw[PER], db[PER];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int i = (v * G + t) * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            w[v * VEC + e] = 1.f;
+            dw[v * VEC + e] = db[v * VEC + e] = 0.f;
+        }
+        if (i < a.d && a.w) load_weights<VEC>(a.w, i, a.w_f32, w + v * VEC);
+    }
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / G;
+    auto request = [&](int st, int64_t row) {
+        if constexpr (VEC == 8) {
+            if (row < a.N) {
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const int i = (v * G + t) * 8;
+                    if (i < a.d) {
+                        to_ring<TX>(ring, st, v * words<TX>(), row_of<TX>(a.x, row, a.ldx) + i);
+                        to_ring<TY>(ring, st, G0 + v * words<TY>(), row_of<TY>(a.dy, row, a.lddy) + i);
+                        if (RES) to_ring<TX>(ring, st, Q0 + v * words<TX>(), row_of<TX>(a.dres, row, a.lddres) + i);
+                    }
+                }
+            }
+            copies_commit();
+        }
+    };
+#pragma unroll
+    for (int st = 0; st < STAGES; ++st) request(st, r + st * step);
+    int st = 0;
+    float next_mean = r < a.N ? a.mean[r] : 0.f, next_rstd = r < a.N ? a.rstd[r] : 0.f;
+    for (; r < a.N; r += step) {
+        const float mean = next_mean, rstd = next_rstd;
+        if (r + step < a.N) {
+            next_mean = a.mean[r + step];
+            next_rstd = a.rstd[r + step];
+        }
+        Piece<TX, VEC> x[NV];
+        Piece<TY, VEC> g[NV];
+        if (VEC == 8) copies_wait<STAGES - 1>();
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+            const bool in = i < a.d;
+            x[v].zero();
+            g[v].zero();
+            if (in) {
+                if constexpr (VEC == 8) {
+                    from_ring<TX>(ring, st, v * words<TX>(), x[v]);
+                    from_ring<TY>(ring, st, G0 + v * words<TY>(), g[v]);
+                } else {
+                    x[v].load(row_of<TX>(a.x, r, a.ldx) + i);
+                    g[v].load(row_of<TY>(a.dy, r, a.lddy) + i);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int k = v * VEC + e;
+                const float dy = g[v].get(e);
+                const float hat = in ? (x[v].get(e) - mean) * rstd : 0.f;
+                dw[k] = fmaf(dy, hat, dw[k]);
+                db[k] += dy;
+                const float dv = dy * w[k];
+                s1 += dv;
+                s2 = fmaf(dv, hat, s2);
+            }
+        }
+        const float2 c = rs.sum2(s1, s2);
+        const float c1 = c.x * inv_d, c2 = c.y * inv_d;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+            if (i >= a.d) continue;
+            Piece<TX, VEC> q;
+            if constexpr (RES) {
+                if constexpr (VEC == 8)
+                    from_ring<TX>(ring, st, Q0 + v * words<TX>(), q);
+                else
+                    q.load(row_of<TX>(a.dres, r, a.lddres) + i);
+            }
+            float f[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const float hat = (x[v].get(e) - mean) * rstd;
+                f[e] = rstd * (g[v].get(e) * w[v * VEC + e] - c1 - hat * c2);
+                if constexpr (RES) f[e] += q.get(e);
+            }
+            q.set(f);
+            q.store(row_of<TX>(a.dx, r, a.lddx) + i);
+        }
+        request(st, r + STAGES * step);
+        st = st + 1 == STAGES ? 0 : st + 1;
+    }
+    if (VEC == 8) copies_wait<0>();
+    if (!a.part) return;
+    float* part = a.part + (size_t)blockIdx.x * 2 * a.d;
+    if (groups == 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+            if (i < a.d) {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    part[i + e] = dw[v * VEC + e];
+                    part[a.d + i + e] = db[v * VEC + e];
+                }
+            }
+        }
+        return;
+    }
+    // several rows at a time in the block: their sums added in order, over the ring
+    float* sums = reinterpret_cast<float*>(dyn);
+    __syncthreads();
+    for (int k = 0; k < groups; ++k) {
+        if ((int)threadIdx.x / G == k) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int i = (v * G + t) * VEC;
+                if (i < a.d) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        sums[i + e] = (k ? sums[i + e] : 0.f) + dw[v * VEC + e];
+                        sums[a.d + i + e] = (k ? sums[a.d + i + e] : 0.f) + db[v * VEC + e];
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) part[i] = sums[i];
+}
+
+// Threads of a row: the fewest that hold it; 0 where kMaxGroup do not.
+int group_of(int d)
+{
+    int G = 32;
+    while (G < kMaxGroup && G * 8 < d) G *= 2;
+    return G * 16 >= d ? G : 0;
+}
+
+int rows_per_block(int G) { return G < 256 ? 256 / G : 1; }
+
+// Blocks of the backward, each with its own partial sums: as many as the rows
+// need, at most two on each of 152 SMs (long rows: as many parts of eight rows).
+int parts_for(int64_t N, int d)
+{
+    const int G = group_of(d);
+    const int64_t rows = G ? rows_per_block(G) : 8;
+    const int64_t n = (N + rows - 1) / rows;
+    return n < kMaxParts ? (int)n : kMaxParts;
+}
 
 bool type_ok(int t) { return t == TWELL_BF16 || t == TWELL_F32; }
 
@@ -189,38 +686,98 @@ bool elem_aligned(const void* p, int type)
     return (reinterpret_cast<uintptr_t>(p) & (type == TWELL_F32 ? 3u : 1u)) == 0;
 }
 
-template <class TX, class TY, class TW>
-cudaError_t fwd(const FwdArgs& a, cudaStream_t s)
+// 16-byte pieces: every row of p starts on a 16-byte boundary.
+bool vec_rows(const void* p, int64_t ld, int64_t N, int type)
 {
-    const unsigned grid = (unsigned)(a.N < 65536 ? a.N : 65536);
-    count_launches(1);
-    k_ln_fwd_long<TX, TY, TW><<<grid, kRowThreads, 0, s>>>(a);
+    const int64_t size = type == TWELL_F32 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (N <= 1 || ld * size % 16 == 0);
+}
+
+// Launches a kernel that may want more than 48 KB of shared memory (its static part included).
+template <class Args>
+cudaError_t launch_rows(void (*kern)(Args, int), const Args& a, int G, unsigned blocks, unsigned threads, size_t smem,
+                        cudaStream_t s)
+{
+    if (smem > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<blocks, threads, smem, s>>>(a, G);
     return cudaGetLastError();
 }
 
-template <class TX, class TY, class TW>
-cudaError_t bwd(const BwdArgs& a, float* dw, float* db, cudaStream_t s)
+template <class TX, class TY, int PER, bool RES>
+cudaError_t launch_fwd(const FwdArgs& a, int G, bool vec, unsigned blocks, unsigned threads, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)(a.N < 65536 ? a.N : 65536);
+    constexpr int W = fwd_words<TX, PER, RES>();
+    if (!vec) return launch_rows(k_ln_fwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, 0, s);
+    return launch_rows(k_ln_fwd<TX, TY, 8, PER, RES>, a, G, blocks, threads, Ring<stages_for(W), W>::bytes(threads), s);
+}
+
+template <class TX, class TY>
+cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t s)
+{
+    const int G = group_of(a.d);
     count_launches(1);
-    k_ln_bwd_long<TX, TY, TW><<<grid, kRowThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    if (G) {
+        const int64_t n = (a.N + rows_per_block(G) - 1) / rows_per_block(G);
+        const int64_t most = (int64_t)kMaxParts * (G <= 256 ? 2 : 1);
+        const unsigned blocks = (unsigned)(n < most ? n : most), threads = G < 256 ? 256 : G;
+        if (G * 8 >= a.d)
+            return a.res ? launch_fwd<TX, TY, 8, true>(a, G, vec, blocks, threads, s)
+                         : launch_fwd<TX, TY, 8, false>(a, G, vec, blocks, threads, s);
+        return a.res ? launch_fwd<TX, TY, 16, true>(a, G, vec, blocks, threads, s)
+                     : launch_fwd<TX, TY, 16, false>(a, G, vec, blocks, threads, s);
+    }
+    k_ln_fwd_long<TX, TY><<<(unsigned)(a.N < 65536 ? a.N : 65536), kRowThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <class TX, class TY, int PER, bool RES>
+cudaError_t launch_bwd(const BwdArgs& a, int G, bool vec, unsigned threads, cudaStream_t s)
+{
+    constexpr int W = bwd_words<TX, TY, PER, RES>();
+    // the block's column sums, when it holds several rows at a time (over the ring where there is one)
+    const size_t sums = G < 256 ? (size_t)2 * a.d * sizeof(float) : 0;
+    if (!vec) return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, sums, s);
+    const size_t ring = Ring<stages_for(W), W>::bytes(threads);
+    return launch_rows(k_ln_bwd<TX, TY, 8, PER, RES>, a, G, a.parts, threads, ring > sums ? ring : sums, s);
+}
+
+template <class TX, class TY>
+cudaError_t bwd(const BwdArgs& a, bool vec, float* dw, float* db, cudaStream_t s)
+{
+    const int G = group_of(a.d);
+    cudaError_t e;
+    count_launches(1);
+    if (G) {
+        const unsigned threads = G < 256 ? 256 : G;
+        if (G * 8 >= a.d)
+            e = a.dres ? launch_bwd<TX, TY, 8, true>(a, G, vec, threads, s)
+                       : launch_bwd<TX, TY, 8, false>(a, G, vec, threads, s);
+        else
+            e = a.dres ? launch_bwd<TX, TY, 16, true>(a, G, vec, threads, s)
+                       : launch_bwd<TX, TY, 16, false>(a, G, vec, threads, s);
+    } else {
+        k_ln_bwd_long<TX, TY><<<(unsigned)(a.N < 65536 ? a.N : 65536), kRowThreads, 0, s>>>(a);
+        if (dw) {
+            count_launches(1);
+            k_ln_cols_long<TX, TY><<<dim3((unsigned)((a.d + 31) / 32), (unsigned)a.parts), dim3(32, 8), 0, s>>>(a);
+        }
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess || !dw) return e;
-    count_launches(2);
-    k_ln_cols_long<TX, TY><<<dim3((unsigned)((a.d + 31) / 32), (unsigned)a.parts), dim3(32, 8), 0, s>>>(a);
-    k_ln_reduce<<<(unsigned)((2 * (int64_t)a.d + 31) / 32), dim3(32, 8), 0, s>>>(a.part, a.parts, a.d, dw, db);
+    count_launches(1);
+    k_ln_reduce<<<(unsigned)((2 * (int64_t)a.d + 31) / 32), dim3(32, 32), 0, s>>>(a.part, a.parts, a.d, dw, db);
     return cudaGetLastError();
 }
 
-// f with the tags of the three types.
+// f with the tags of the two types.
 template <class F>
-cudaError_t by_types(int x, int y, int w, F f)
+cudaError_t by_types(int x, int y, F f)
 {
-    auto with_w = [&](auto tx, auto ty) {
-        return w == TWELL_F32 ? f(tx, ty, f32_t{}) : f(tx, ty, bf16_t{});
-    };
-    auto with_y = [&](auto tx) { return y == TWELL_F32 ? with_w(tx, f32_t{}) : with_w(tx, bf16_t{}); };
-    return x == TWELL_F32 ? with_y(f32_t{}) : with_y(bf16_t{});
+    if (x == TWELL_F32) return y == TWELL_F32 ? f(f32_t{}, f32_t{}) : f(f32_t{}, bf16_t{});
+    return y == TWELL_F32 ? f(bf16_t{}, f32_t{}) : f(bf16_t{}, bf16_t{});
 }
 
 }  // namespace
@@ -243,9 +800,13 @@ extern "C" twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const vo
         !elem_aligned(y, y_type) || !elem_aligned(w, w_type) || !elem_aligned(b, w_type) ||
         !elem_aligned(mean, TWELL_F32) || !elem_aligned(rstd, TWELL_F32))
         return TWELL_ERR_INVALID_ARG;
-    const FwdArgs a{x, res, w, b, sum, y, ldx, ldres, ldsum, ldy, N, d, eps, mean, rstd};
-    const cudaError_t e = by_types(x_type, y_type, w_type, [&](auto tx, auto ty, auto tw) {
-        return fwd<decltype(tx), decltype(ty), decltype(tw)>(a, static_cast<cudaStream_t>(stream));
+    const bool vec = d % 8 == 0 && vec_rows(x, ldx, N, x_type) && vec_rows(res, ldres, N, x_type) &&
+                     vec_rows(sum, ldsum, N, x_type) && vec_rows(y, ldy, N, y_type) && vec_rows(w, 0, 1, w_type) &&
+                     vec_rows(b, 0, 1, w_type);
+    const FwdArgs a{x, res, w, b, sum, y, ldx, ldres, ldsum, ldy, N, d, eps, mean, rstd,
+                    w_type == TWELL_F32};
+    const cudaError_t e = by_types(x_type, y_type, [&](auto tx, auto ty) {
+        return fwd<decltype(tx), decltype(ty)>(a, vec, static_cast<cudaStream_t>(stream));
     });
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
@@ -253,7 +814,7 @@ extern "C" twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const vo
 extern "C" size_t twell_layernorm_bwd_workspace_bytes(int64_t N, int d)
 {
     if (N < 0 || d < 1) return 0;
-    const size_t n = (size_t)parts_for(N) * 2 * d * sizeof(float);
+    const size_t n = (size_t)parts_for(N, d) * 2 * d * sizeof(float);
     return n > 256 ? n : 256;
 }
 
@@ -282,10 +843,12 @@ extern "C" twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const 
         return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_layernorm_bwd_workspace_bytes(N, d)) return TWELL_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return TWELL_ERR_INVALID_ARG;
+    const bool vec = d % 8 == 0 && vec_rows(dy, lddy, N, y_type) && vec_rows(x, ldx, N, x_type) &&
+                     vec_rows(dres, lddres, N, x_type) && vec_rows(dx, lddx, N, x_type) && vec_rows(w, 0, 1, w_type);
     const BwdArgs a{dy, x, w, dres, dx, lddy, ldx, lddres, lddx, N, d, mean, rstd,
-                    dw ? static_cast<float*>(ws) : nullptr, parts_for(N)};
-    const cudaError_t e = by_types(x_type, y_type, w_type, [&](auto tx, auto ty, auto tw) {
-        return bwd<decltype(tx), decltype(ty), decltype(tw)>(a, dw, db, s);
+                    dw ? static_cast<float*>(ws) : nullptr, parts_for(N, d), w_type == TWELL_F32};
+    const cudaError_t e = by_types(x_type, y_type, [&](auto tx, auto ty) {
+        return bwd<decltype(tx), decltype(ty)>(a, vec, dw, db, s);
     });
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }
