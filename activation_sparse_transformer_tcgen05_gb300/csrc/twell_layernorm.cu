@@ -45,7 +45,7 @@ struct BwdArgs {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kMaxParts = 304;
+constexpr int kMaxLongParts = 304;
 
 // Element i of a weight vector of either type; `none` where there is no vector.
 __device__ __forceinline__ float weight(const void* p, int i, bool f32, float none)
@@ -217,10 +217,14 @@ struct Piece<bf16_t, VEC> {
     }
     __device__ __forceinline__ void set(const float* f)
     {
-        v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                       pack_bf16x2(f[6], f[7]));
+        v = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
     }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
+    static __device__ __forceinline__ uint32_t pair(float lo, float hi)
+    {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return (uint32_t)__bfloat16_as_ushort(b.x) | (uint32_t)__bfloat16_as_ushort(b.y) << 16;
+    }
 };
 template <>
 struct Piece<bf16_t, 1> {
@@ -266,32 +270,32 @@ struct Piece<f32_t, 1> {
     __device__ __forceinline__ void store(float* p) const { *p = v; }
 };
 
-// Sum over the G threads of a row, the same bits in all of them: a butterfly in
-// each warp, then the warps' sums in order. `buf` alternates between two halves
+// Sums over the G threads of a row, the same bits in all of them: a butterfly in
+// each warp, then one over the warps' sums. `buf` alternates between two halves
 // from one sum to the next, so one barrier each is enough.
 struct RowSum {
     float2* buf;  // [2][16]
-    int warp0, warps, bar, turn = 0;
+    int mine, from, warps, bar;
     __device__ RowSum(float2* b, int G) : buf(b)
     {
+        const int group = threadIdx.x / G;
         warps = G >> 5;
-        warp0 = (threadIdx.x / G) * warps;
-        bar = 1 + threadIdx.x / G;
+        mine = threadIdx.x >> 5;
+        from = group * warps + (threadIdx.x & (warps - 1));
+        bar = 1 + group;
     }
     __device__ __forceinline__ float2 sum2(float x, float y)
     {
         x = warp_sum(x);
         y = warp_sum(y);
         if (warps == 1) return make_float2(x, y);
-        float2* b = buf + turn * 16;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = make_float2(x, y);
+        if ((threadIdx.x & 31) == 0) buf[mine] = make_float2(x, y);
         named_bar_sync(bar, warps * 32);
-        float2 s = b[warp0];
-        for (int i = 1; i < warps; ++i) {
-            const float2 o = b[warp0 + i];
-            s.x += o.x;
-            s.y += o.y;
+        float2 s = buf[from];
+        turn();
+        for (int off = warps >> 1; off >= 1; off >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, off);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, off);
         }
         return s;
     }
@@ -299,13 +303,17 @@ struct RowSum {
     {
         x = warp_sum(x);
         if (warps == 1) return x;
-        float2* b = buf + turn * 16;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5].x = x;
+        if ((threadIdx.x & 31) == 0) buf[mine].x = x;
         named_bar_sync(bar, warps * 32);
-        float s = b[warp0].x;
-        for (int i = 1; i < warps; ++i) s += b[warp0 + i].x;
+        float s = buf[from].x;
+        turn();
+        for (int off = warps >> 1; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
         return s;
+    }
+    __device__ __forceinline__ void turn()
+    {
+        mine ^= 16;
+        from ^= 16;
     }
 };
 
@@ -384,13 +392,12 @@ __device__ __forceinline__ void to_ring(R& ring, int st, int k, const typename T
     for (int i = 0; i < words<T>(); ++i) copy_async16(ring.word(st, k + i), reinterpret_cast<const uint4*>(from) + i);
 }
 
-// Stages of the ring: rows in flight for at most 98 KB with 512 threads of 8
-// elements, so that two blocks fit an SM (16 elements of three fp32 streams:
-// 196 KB, one block).
-constexpr int stages_for(int words) { return words <= 3 ? 4 : words <= 4 ? 3 : 2; }
+// Stages of the ring: rows in flight for at most 98 KB with 256 threads of 16
+// elements, so that two blocks fit an SM.
+constexpr int stages_for(int words) { return words <= 6 ? 4 : words <= 8 ? 3 : 2; }
 
-// Blocks of 512 threads that share an SM (64 registers a thread) with 8 elements
-// a thread; with 16, one.
+// Blocks of 512 threads that share an SM: two (64 registers a thread) with 8
+// elements a thread, one with 16.
 constexpr int blocks_per_sm(int per) { return per == 8 ? 2 : 1; }
 
 template <class TX, int PER, bool RES>
@@ -423,23 +430,29 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
     }
     const int64_t step = (int64_t)gridDim.x * (blockDim.x / G);
     int64_t r = (int64_t)blockIdx.x * (blockDim.x / G) + threadIdx.x / G;
-    auto request = [&](int st, int64_t row) {
+    // this thread's first element in the row asked for next
+    int64_t asked = r;
+    const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
+    const typename TX::type* aq = RES ? row_of<TX>(a.res, r, a.ldres) + t * VEC : nullptr;
+    auto request = [&](int st) {
         if constexpr (VEC == 8) {
-            if (row < a.N) {
+            if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int i = (v * G + t) * 8;
-                    if (i < a.d) {
-                        to_ring<TX>(ring, st, v * words<TX>(), row_of<TX>(a.x, row, a.ldx) + i);
-                        if (RES) to_ring<TX>(ring, st, (NV + v) * words<TX>(), row_of<TX>(a.res, row, a.ldres) + i);
+                    if ((v * G + t) * 8 < a.d) {
+                        to_ring<TX>(ring, st, v * words<TX>(), ax + v * G * 8);
+                        if (RES) to_ring<TX>(ring, st, (NV + v) * words<TX>(), aq + v * G * 8);
                     }
                 }
             }
             copies_commit();
+            asked += step;
+            ax += step * a.ldx;
+            if (RES) aq += step * a.ldres;
         }
     };
 #pragma unroll
-    for (int st = 0; st < STAGES; ++st) request(st, r + st * step);
+    for (int st = 0; st < STAGES; ++st) request(st);
     int st = 0;
     for (; r < a.N; r += step) {
         float f[PER];
@@ -473,7 +486,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s += f[v * VEC + e];
         }
-        request(st, r + STAGES * step);
+        request(st);
         st = st + 1 == STAGES ? 0 : st + 1;
         const float mean = rs.sum(s) * inv_d;
         float c2 = 0.f;
@@ -486,7 +499,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
                 if (in) c2 = fmaf(f[v * VEC + e], f[v * VEC + e], c2);
             }
         }
-        const float rstd = 1.f / sqrtf(rs.sum(c2) * inv_d + a.eps);
+        const float rstd = rsqrtf(rs.sum(c2) * inv_d + a.eps);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int i = (v * G + t) * VEC;
@@ -537,24 +550,31 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
     }
     const int64_t step = (int64_t)gridDim.x * groups;
     int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / G;
-    auto request = [&](int st, int64_t row) {
+    int64_t asked = r;
+    const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
+    const typename TY::type* ag = row_of<TY>(a.dy, r, a.lddy) + t * VEC;
+    const typename TX::type* aq = RES ? row_of<TX>(a.dres, r, a.lddres) + t * VEC : nullptr;
+    auto request = [&](int st) {
         if constexpr (VEC == 8) {
-            if (row < a.N) {
+            if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    const int i = (v * G + t) * 8;
-                    if (i < a.d) {
-                        to_ring<TX>(ring, st, v * words<TX>(), row_of<TX>(a.x, row, a.ldx) + i);
-                        to_ring<TY>(ring, st, G0 + v * words<TY>(), row_of<TY>(a.dy, row, a.lddy) + i);
-                        if (RES) to_ring<TX>(ring, st, Q0 + v * words<TX>(), row_of<TX>(a.dres, row, a.lddres) + i);
+                    if ((v * G + t) * 8 < a.d) {
+                        to_ring<TX>(ring, st, v * words<TX>(), ax + v * G * 8);
+                        to_ring<TY>(ring, st, G0 + v * words<TY>(), ag + v * G * 8);
+                        if (RES) to_ring<TX>(ring, st, Q0 + v * words<TX>(), aq + v * G * 8);
                     }
                 }
             }
             copies_commit();
+            asked += step;
+            ax += step * a.ldx;
+            ag += step * a.lddy;
+            if (RES) aq += step * a.lddres;
         }
     };
 #pragma unroll
-    for (int st = 0; st < STAGES; ++st) request(st, r + st * step);
+    for (int st = 0; st < STAGES; ++st) request(st);
     int st = 0;
     float next_mean = r < a.N ? a.mean[r] : 0.f, next_rstd = r < a.N ? a.rstd[r] : 0.f;
     for (; r < a.N; r += step) {
@@ -617,7 +637,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             q.set(f);
             q.store(row_of<TX>(a.dx, r, a.lddx) + i);
         }
-        request(st, r + STAGES * step);
+        request(st);
         st = st + 1 == STAGES ? 0 : st + 1;
     }
     if (VEC == 8) copies_wait<0>();
@@ -659,24 +679,33 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
     for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) part[i] = sums[i];
 }
 
+// Elements of a row per thread. What a warp does once a row (sums over lanes and
+// warps, addresses) weighs more than the bytes with 8 elements a lane (16384 x 4096
+// bf16 with residual: forward 117 us with 8, issue slots 74 % busy); rows that a
+// warp holds with 8 take 8.
+int per_thread(int d) { return d <= 256 ? 8 : 16; }
+
 // Threads of a row: the fewest that hold it; 0 where kMaxGroup do not.
 int group_of(int d)
 {
     int G = 32;
-    while (G < kMaxGroup && G * 8 < d) G *= 2;
-    return G * 16 >= d ? G : 0;
+    while (G * per_thread(d) < d) G *= 2;
+    return G <= kMaxGroup ? G : 0;
 }
 
 int rows_per_block(int G) { return G < 256 ? 256 / G : 1; }
 
-// Blocks of the backward, each with its own partial sums: as many as the rows
-// need, at most two on each of 152 SMs (long rows: as many parts of eight rows).
+// Blocks on 152 SMs at once: 128 registers a thread with 16 elements, 64 with 8.
+int resident_blocks(int G, int d) { return 152 * (G > 256 ? 1 : per_thread(d) == 16 ? 2 : 4); }
+
+// Blocks of the backward, each with its own partial sums (long rows: parts of
+// eight rows at a time).
 int parts_for(int64_t N, int d)
 {
     const int G = group_of(d);
     const int64_t rows = G ? rows_per_block(G) : 8;
-    const int64_t n = (N + rows - 1) / rows;
-    return n < kMaxParts ? (int)n : kMaxParts;
+    const int64_t n = (N + rows - 1) / rows, most = G ? resident_blocks(G, d) : kMaxLongParts;
+    return (int)(n < most ? n : most);
 }
 
 bool type_ok(int t) { return t == TWELL_BF16 || t == TWELL_F32; }
@@ -721,9 +750,9 @@ cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t s)
     count_launches(1);
     if (G) {
         const int64_t n = (a.N + rows_per_block(G) - 1) / rows_per_block(G);
-        const int64_t most = (int64_t)kMaxParts * (G <= 256 ? 2 : 1);
+        const int64_t most = resident_blocks(G, a.d);
         const unsigned blocks = (unsigned)(n < most ? n : most), threads = G < 256 ? 256 : G;
-        if (G * 8 >= a.d)
+        if (per_thread(a.d) == 8)
             return a.res ? launch_fwd<TX, TY, 8, true>(a, G, vec, blocks, threads, s)
                          : launch_fwd<TX, TY, 8, false>(a, G, vec, blocks, threads, s);
         return a.res ? launch_fwd<TX, TY, 16, true>(a, G, vec, blocks, threads, s)
@@ -752,7 +781,7 @@ cudaError_t bwd(const BwdArgs& a, bool vec, float* dw, float* db, cudaStream_t s
     count_launches(1);
     if (G) {
         const unsigned threads = G < 256 ? 256 : G;
-        if (G * 8 >= a.d)
+        if (per_thread(a.d) == 8)
             e = a.dres ? launch_bwd<TX, TY, 8, true>(a, G, vec, threads, s)
                        : launch_bwd<TX, TY, 8, false>(a, G, vec, threads, s);
         else
