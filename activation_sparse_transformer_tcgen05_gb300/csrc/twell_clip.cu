@@ -6,12 +6,13 @@
 //
 // Bound by memory: every element is read for the norm, and read and written
 // again scaled (12 bytes in fp32). The tensors' addresses travel in the
-// launch's parameters (up to kTable of them a launch), so nothing is copied to
-// the device first.
+// launch's parameters (up to 512 of them a launch), so nothing is copied to the
+// device first.
 //
-//   k_sumsq       every block sums the squares of its share of the elements
+//   k_sumsq       every block sums the squares of a run of consecutive units
 //   k_clip_scale  every block adds the blocks' sums in the same fixed order and
-//                 scales its share
+//                 scales the same run, last unit first: what the first kernel
+//                 read last is still in L2
 #include "common.cuh"
 #include "launch.h"
 
@@ -19,22 +20,106 @@ namespace twell {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTable = 512;         // tensors of one launch
-constexpr int kChunk = 8192;        // elements of one unit of work
-constexpr int kMaxBlocks = 608;     // four blocks on each of 152 SMs; partial sums of one launch
-constexpr int kMaxLaunches = 64;    // 32768 tensors
+constexpr int kBlocksPerSm = 4;
+constexpr int kUnit = 8192;                     // elements of one unit of work: 32 a thread
+constexpr int kPer = kUnit / kThreads;
+constexpr int kMaxBlocks = 152 * kBlocksPerSm;  // of one launch, each with one partial sum
+constexpr int kTable = 512, kSmallTable = 32;   // tensors of one launch: two sizes of its parameters
+constexpr int kMaxLaunches = 64;                // 32768 tensors
 
+template <int CAP>
 struct Table {
-    const void* in[kTable];
-    void* out[kTable];
-    int64_t numel[kTable];
-    int32_t first[kTable + 1];  // first unit of each tensor
-    uint8_t f32[kTable];
-    int n;
+    const void* in[CAP];
+    void* out[CAP];
+    int64_t numel[CAP];
+    int32_t first[CAP + 1];  // first unit of each tensor
+    uint8_t f32[CAP];
+    uint8_t vec[CAP];        // 16-byte accesses: both addresses allow them
+    int32_t n;
+
+    // Units of block b: a run of them, no run more than one longer than another.
+    __device__ __forceinline__ int from(int b) const { return (int)((int64_t)first[n] * b / gridDim.x); }
 };
 
+// One thread's elements of a unit as floats: 16-byte loads where the tensor
+// allows them, else element by element, neighbours in neighbouring threads.
+// at(k) is the place of element k in the unit.
+template <bool F32, bool VEC>
+struct Slice {
+    static constexpr int W = VEC ? (F32 ? 4 : 8) : 1;
+    static __device__ __forceinline__ int at(int k) { return (k / W * kThreads + (int)threadIdx.x) * W + k % W; }
+
+    static __device__ __forceinline__ void load(const void* p, int64_t i0, int left, float (&v)[kPer])
+    {
+#pragma unroll
+        for (int k = 0; k < kPer; k += W) {
+            const int i = at(k);
+            if (VEC && i + W <= left) {
+                if constexpr (F32) {
+                    const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i0 + i);
+                    v[k] = q.x, v[k + 1 < kPer ? k + 1 : k] = q.y, v[k + 2 < kPer ? k + 2 : k] = q.z,
+                    v[k + 3 < kPer ? k + 3 : k] = q.w;
+                } else if constexpr (VEC) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i0 + i);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < W; ++e) v[k + e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+                }
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                float x = 0.f;
+                if (i + e < left)
+                    x = F32 ? static_cast<const float*>(p)[i0 + i + e]
+                            : bf16_to_f32(static_cast<const uint16_t*>(p)[i0 + i + e]);
+                v[k + e] = x;
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void store(void* p, int64_t i0, int left, const float (&v)[kPer])
+    {
+#pragma unroll
+        for (int k = 0; k < kPer; k += W) {
+            const int i = at(k);
+            if (VEC && i + W <= left) {
+                if constexpr (F32) {
+                    *reinterpret_cast<float4*>(static_cast<float*>(p) + i0 + i) =
+                        make_float4(v[k], v[k + 1 < kPer ? k + 1 : k], v[k + 2 < kPer ? k + 2 : k],
+                                    v[k + 3 < kPer ? k + 3 : k]);
+                } else if constexpr (VEC) {
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i0 + i) =
+                        make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
+                                   pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+                }
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e) {
+                if (i + e >= left) continue;
+                if (F32)
+                    static_cast<float*>(p)[i0 + i + e] = v[k + e];
+                else
+                    static_cast<uint16_t*>(p)[i0 + i + e] = f32_to_bf16_bits(v[k + e]);
+            }
+        }
+    }
+};
+
+// f(tag) with the Slice for a tensor's type and alignment.
+template <class F>
+__device__ __forceinline__ void by_slice(bool f32, bool vec, F f)
+{
+    if (f32)
+        vec ? f(Slice<true, true>{}) : f(Slice<true, false>{});
+    else
+        vec ? f(Slice<false, true>{}) : f(Slice<false, false>{});
+}
+
 // The tensor that unit u belongs to.
-__device__ __forceinline__ int find_tensor(const Table& t, int u)
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const Table<CAP>& t, int u)
 {
     int lo = 0, hi = t.n - 1;
     while (lo < hi) {
@@ -47,17 +132,11 @@ __device__ __forceinline__ int find_tensor(const Table& t, int u)
     return lo;
 }
 
-__device__ __forceinline__ float load1(const void* p, bool f32, int64_t i)
-{
-    return f32 ? static_cast<const float*>(p)[i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
-}
-
 __device__ double block_sum(double v)
 {
     __shared__ double part[kThreads / 32];
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
     __syncthreads();
     double s = 0.0;
@@ -66,26 +145,52 @@ __device__ double block_sum(double v)
     return s;
 }
 
-__global__ void __launch_bounds__(kThreads) k_sumsq(const __grid_constant__ Table t, double* __restrict__ partial)
+// Sum of the squares of one thread's 32 elements. In fp32, unless the largest is
+// so large that its square overflows or so small that squares are lost below
+// fp32's range: then in 64 bits from the same registers.
+__device__ __forceinline__ double sum_squares(const float (&v)[kPer])
+{
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, m = 0.f;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        s[k & 3] = fmaf(v[k], v[k], s[k & 3]);
+        m = fmaxf(m, fabsf(v[k]));
+    }
+    if (m > 0x1p+60f || (m < 0x1p-40f && m > 0.f)) {
+        double d = 0.0;
+#pragma unroll 1
+        for (int k = 0; k < kPer; ++k) d = fma((double)v[k], (double)v[k], d);
+        return d;
+    }
+    return (double)((s[0] + s[1]) + (s[2] + s[3]));
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    k_sumsq(const __grid_constant__ Table<CAP> t, double* __restrict__ partial)
 {
     double s = 0.0;
-    for (int u = blockIdx.x; u < t.first[t.n]; u += gridDim.x) {
-        const int k = find_tensor(t, u);
-        const int64_t i0 = (int64_t)(u - t.first[k]) * kChunk;
-        const int64_t i1 = i0 + kChunk < t.numel[k] ? i0 + kChunk : t.numel[k];
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const double g = (double)load1(t.in[k], t.f32[k], i);
-            s += g * g;
-        }
+    const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
+    int k = u0 < u1 ? find_tensor(t, u0) : 0;
+    for (int u = u0; u < u1; ++u) {
+        while (u >= t.first[k + 1]) ++k;
+        const int64_t i0 = (int64_t)(u - t.first[k]) * kUnit;
+        const int left = (int)min((int64_t)kUnit, t.numel[k] - i0);
+        by_slice(t.f32[k], t.vec[k], [&](auto slice) {
+            float v[kPer];
+            slice.load(t.in[k], i0, left, v);
+            s += sum_squares(v);
+        });
     }
     s = block_sum(s);
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
 // n_partial sums were written; this launch scales the tensors of its table.
-__global__ void __launch_bounds__(kThreads)
-    k_clip_scale(const __grid_constant__ Table t, const double* __restrict__ partial, int n_partial, float max_norm,
-                 float* __restrict__ norm_out)
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    k_clip_scale(const __grid_constant__ Table<CAP> t, const double* __restrict__ partial, int n_partial,
+                 float max_norm, float* __restrict__ norm_out)
 {
     double s = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
@@ -94,19 +199,69 @@ __global__ void __launch_bounds__(kThreads)
     // a norm that is NaN keeps a NaN factor; an infinite one gives 0 (NaN where g is infinite)
     const float r = max_norm / norm;
     const float c = r >= 1.f ? 1.f : r;
-    for (int u = blockIdx.x; u < t.first[t.n]; u += gridDim.x) {
-        const int k = find_tensor(t, u);
+    const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
+    int k = u0 < u1 ? find_tensor(t, u1 - 1) : 0;
+    for (int u = u1 - 1; u >= u0; --u) {
+        while (u < t.first[k]) --k;
         if (c == 1.f && t.in[k] == t.out[k]) continue;
-        const int64_t i0 = (int64_t)(u - t.first[k]) * kChunk;
-        const int64_t i1 = i0 + kChunk < t.numel[k] ? i0 + kChunk : t.numel[k];
-        for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-            const float g = load1(t.in[k], t.f32[k], i) * c;
-            if (t.f32[k])
-                static_cast<float*>(t.out[k])[i] = g;
-            else
-                static_cast<uint16_t*>(t.out[k])[i] = f32_to_bf16_bits(g);
-        }
+        const int64_t i0 = (int64_t)(u - t.first[k]) * kUnit;
+        const int left = (int)min((int64_t)kUnit, t.numel[k] - i0);
+        by_slice(t.f32[k], t.vec[k], [&](auto slice) {
+            float v[kPer];
+            slice.load(t.in[k], i0, left, v);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) v[e] *= c;
+            slice.store(t.out[k], i0, left, v);
+        });
     }
+}
+
+// Both passes over the tensors, CAP of them a launch.
+template <int CAP>
+twell_status run_clip(const twell_tensor_list* list, float max_norm, float* norm, double* partial, cudaStream_t s)
+{
+    int n_partial = 0;
+    Table<CAP> t;
+    for (int pass = 0; pass < 2; ++pass) {
+        int next = 0;
+        do {
+            if (pass == 0 || list->n > CAP) {  // a list of one table: pass 1 takes pass 0's
+                t.n = 0;
+                int64_t units = 0;
+                while (next < list->n && t.n < CAP) {
+                    const int64_t n = list->numel[next];
+                    const int64_t more = (n + kUnit - 1) / kUnit;
+                    if (units + more > INT32_MAX / 2 && t.n > 0) break;
+                    if (n > 0) {
+                        t.in[t.n] = list->in[next];
+                        t.out[t.n] = list->out[next];
+                        t.numel[t.n] = n;
+                        t.first[t.n] = (int32_t)units;
+                        t.f32[t.n] = list->type[next] == TWELL_F32;
+                        t.vec[t.n] = ((reinterpret_cast<uintptr_t>(list->in[next]) |
+                                       reinterpret_cast<uintptr_t>(list->out[next])) & 15u) == 0;
+                        units += more;
+                        ++t.n;
+                    }
+                    ++next;
+                }
+                t.first[t.n] = (int32_t)units;
+                if (list->n <= CAP && next < list->n) return TWELL_ERR_UNSUPPORTED;  // more units than a table counts
+            }
+            const int units = t.first[t.n];
+            const int blocks = units < 1 ? 1 : units < kMaxBlocks ? units : kMaxBlocks;
+            if (pass == 0 && n_partial + blocks > kMaxBlocks * kMaxLaunches) return TWELL_ERR_UNSUPPORTED;
+            count_launches(1);
+            if (pass == 0) {
+                k_sumsq<CAP><<<blocks, kThreads, 0, s>>>(t, partial + n_partial);
+                n_partial += blocks;
+            } else {
+                k_clip_scale<CAP><<<blocks, kThreads, 0, s>>>(t, partial, n_partial, max_norm, norm);
+            }
+            if (cudaGetLastError() != cudaSuccess) return TWELL_ERR_CUDA;
+        } while (next < list->n && list->n > CAP);
+    }
+    return TWELL_OK;
 }
 
 }  // namespace
@@ -130,46 +285,12 @@ extern "C" twell_status twell_grad_clip(const twell_tensor_list* list, float max
         if (n > 0 && (!list->in[i] || !list->out[i] || (reinterpret_cast<uintptr_t>(list->in[i]) & mask) ||
                       (reinterpret_cast<uintptr_t>(list->out[i]) & mask)))
             return TWELL_ERR_INVALID_ARG;
-        if (n > (int64_t)kChunk * (INT32_MAX / 2)) return TWELL_ERR_UNSUPPORTED;
+        if (n > (int64_t)kUnit * (INT32_MAX / 2)) return TWELL_ERR_UNSUPPORTED;
     }
     if (!ws || ws_bytes < twell_grad_clip_workspace_bytes()) return TWELL_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return TWELL_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     double* partial = static_cast<double*>(ws);
-    int n_partial = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        int next = 0;
-        do {
-            Table t;
-            t.n = 0;
-            int64_t units = 0;
-            while (next < list->n && t.n < kTable) {
-                const int64_t n = list->numel[next];
-                const int64_t more = (n + kChunk - 1) / kChunk;
-                if (units + more > INT32_MAX / 2 && t.n > 0) break;
-                if (n > 0) {
-                    t.in[t.n] = list->in[next];
-                    t.out[t.n] = list->out[next];
-                    t.numel[t.n] = n;
-                    t.first[t.n] = (int32_t)units;
-                    t.f32[t.n] = list->type[next] == TWELL_F32;
-                    units += more;
-                    ++t.n;
-                }
-                ++next;
-            }
-            t.first[t.n] = (int32_t)units;
-            const int blocks = units < 1 ? 1 : units < kMaxBlocks ? (int)units : kMaxBlocks;
-            if (pass == 0 && n_partial + blocks > kMaxBlocks * kMaxLaunches) return TWELL_ERR_UNSUPPORTED;
-            count_launches(1);
-            if (pass == 0) {
-                k_sumsq<<<blocks, kThreads, 0, s>>>(t, partial + n_partial);
-                n_partial += blocks;
-            } else {
-                k_clip_scale<<<blocks, kThreads, 0, s>>>(t, partial, n_partial, max_norm, norm);
-            }
-            if (cudaGetLastError() != cudaSuccess) return TWELL_ERR_CUDA;
-        } while (next < list->n);
-    }
-    return TWELL_OK;
+    return list->n <= kSmallTable ? run_clip<kSmallTable>(list, max_norm, norm, partial, s)
+                                  : run_clip<kTable>(list, max_norm, norm, partial, s);
 }
