@@ -114,7 +114,8 @@ cudaError_t launch_wgrad(const TwellView& tw, const CscWork& w, const float* dpr
                          cudaStream_t s);
 
 // ---- tcgen05 GEMM (twell_gemm.cu)
-enum GemmMode { GEMM_TWELL_RELU = 0, GEMM_GATE_SWAP = 1, GEMM_DENSE = 2, GEMM_SPLITK = 3, GEMM_XENT = 4 };
+enum GemmMode { GEMM_TWELL_RELU = 0, GEMM_GATE_SWAP = 1, GEMM_DENSE = 2, GEMM_SPLITK = 3, GEMM_XENT = 4,
+                GEMM_SCALED = 5 };
 // ---- gated decode tail (twell_sparse.cu): layout, fill, gated up and
 // down-projection in one cooperative launch; y == nullptr skips the
 // down-projection. `counter` must be 0 when it starts (grid barrier).
@@ -152,13 +153,14 @@ struct GemmArgs {
     const uint16_t* mask;  //   if set, [rowsA, ldm] bf16: result kept only where mask is nonzero
     int ldm;
     float add_scalar;      //   added to every result before the mask (fp32 and bf16 outputs)
-    int lda;               // DENSE / SPLITK: row stride of A's array in elements (0: packed)
+    int lda;               // SPLITK / SCALED: row stride of A's array in elements (0: packed)
     int k_splits;          // SPLITK: the depth in this many parts of kb_per_split 64-deep k-blocks (the last one
-    int kb_per_split;      //   may be shorter, none empty); part p goes to out_f32 + p * split_stride
-    size_t split_stride;
+    int kb_per_split;      //   may be shorter, none empty); out_f32 is [k_splits, rowsA, ldo]
+    const float* scale;    // SCALED: device scalar that multiplies the product (out, with row_map if set, or
+                           //   out_f32, with accumulate)
     uint16_t* codes;       // XENT: logit codes [rowsA, ldcode], or null: statistics only
     size_t ldcode;
-    float2* xstat;         // XENT: [rowsA, column tiles] (maximum in log2 units, sum of 2^(z - maximum))
+    float2* xstat;         // XENT: [rowsA, NB] (maximum in log2 units, sum of 2^(z - maximum)), NB tiles of kXentTile
     const int32_t* target; // XENT: [rowsA] column whose logit goes to ztarget
     float* ztarget;        // XENT: [rowsA]
     float* colsum;         // DENSE, bf16 output only: if set, column sums of the (masked) fp32 results per
@@ -182,12 +184,12 @@ cudaError_t launch_spmm_union(const TwellView& tw, const uint16_t* W, int d, con
                               int32_t* status, cudaStream_t s);
 
 // Logit codes of the cross entropy (GEMM_XENT's epilogue writes them, the
-// gradient pass reads them): code q of a logit z in a (row, 256-column) tile
+// gradient pass reads them): code q of a logit z in a (row, 128-column) tile
 // with maximum m2 (log2 units) stands for z log2(e) = m2 - q / 2048; the
 // largest code stands for a probability of zero.
 constexpr float kXentSteps = 2048.f;
 constexpr uint32_t kXentZero = 65535u;
-constexpr int kXentTile = 256;
+constexpr int kXentTile = 128;
 
 // Returns the column-block width BN the GEMM uses for this mode/shape.
 int gemm_block_n(int mode, int rowsB);

@@ -21,8 +21,10 @@
 //                    baseline layer.
 //   GEMM_SPLITK      fp32 partial products over parts of a long depth (CTA
 //                    pairs only), summed by the caller's next kernel.
+//   GEMM_SCALED      the product times a device scalar, in bf16 or fp32 (CTA
+//                    pairs only).
 //   GEMM_XENT        A = hidden rows, B = the head's rows (one per word), CTA
-//                    pairs only: per (row, 256 words) the logits' maximum and
+//                    pairs only: per (row, 128 words) the logits' maximum and
 //                    sum of exponentials, and 16-bit codes of the logits; the
 //                    logits themselves are never written.
 //
@@ -229,44 +231,56 @@ __device__ __forceinline__ void epi_dense_row(uint32_t tbase, int row, int rowsA
     }
 }
 
-// Split-K epilogue of one accumulator row (one thread): the fp32 values as they are.
-template <int BN>
-__device__ __forceinline__ void epi_partial_row(uint32_t tbase, int row, int rowsA, int nb, const GemmArgs& a,
-                                                float* __restrict__ out)
-{
-    const bool row_ok = row < rowsA;
-#pragma unroll 1
-    for (int ch = 0; ch < BN / 32; ++ch) {
-        uint32_t v[32];
-        tmem_ld32_wait(tbase + ch * 32, v);
-        if (!row_ok) continue;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) {
-            const int col = nb * BN + ch * 32 + g * 4;
-            if (col < a.rowsB)
-                *reinterpret_cast<uint4*>(out + (size_t)row * a.ldo + col) =
-                    make_uint4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]);
-        }
-    }
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Cross-entropy epilogue of one accumulator row (one thread) and 256 columns
+// --- Epilogues of eight warps, 32 rows x 128 columns of the tile each. Results go
+// through 4 KB of a warp's own shared memory, so that it stores whole 128-byte
+// pieces of rows: threads that store their own rows touch 32 lines with every
+// instruction. With short depths the epilogue holds the MMAs back (777 x 1000 x
+// 50001, logits and dW: four warps with direct stores 94 and 88 us). Loops over 32
+// columns stay loops: holding 128 in registers, unrolled, made the code so long
+// that fetching it took longer than running it (82 and 80 us); bulk stores from
+// shared memory waited on their fences (73 and 74 us).
+
+// 32 rows of 128 bytes, the lane's own row written as 16-byte pieces c (0 to 7),
+// then all rows read back with eight lanes to a row. Pieces are permuted within a
+// row so that both fall into different banks.
+struct Outbox {
+    uint8_t* box;
+    int lane;
+    __device__ __forceinline__ void put(int c, const uint4& v)
+    {
+        *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
+    }
+    // f(row, piece, value) for the 256 pieces, eight in turn for each lane
+    template <class F>
+    __device__ __forceinline__ void drain(F f)
+    {
+        __syncwarp();
+        const int c = lane & 7;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            f(r, c, *reinterpret_cast<const uint4*>(box + r * 128 + ((c ^ (r & 7)) << 4)));
+        }
+        __syncwarp();
+    }
+};
+
+// Cross-entropy epilogue of one accumulator row (one thread) and 128 columns
 // (words). Two readings of the accumulator: the maximum m, then, with
 // m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0, the sum of 2^t and the
 // code round(-2048 t). A logit is kept as its distance to the maximum on a
-// logarithmic scale, in steps of 2^-11: the exponential rebuilt from a code is
-// off by at most 2^(2^-12) - 1 = 1.7e-4, a twentieth of its later rounding to
-// bf16 (up to 2^-8). Codes end 32 powers of two below the maximum; what is below
-// counts as zero in the gradient (not in the sum). Rounding to the integer is the
-// addition of 2^23, whose low mantissa bits are then the code.
+// logarithmic scale, in steps of 2^-11: the exponential rebuilt from a code is off
+// by at most 2^(2^-12) - 1 = 1.7e-4, a twentieth of its later rounding to bf16 (up
+// to 2^-8). Codes end 32 powers of two below the maximum; what is below counts as
+// zero in the gradient (not in the sum). Rounding to the integer is the addition of
+// 2^23, whose low mantissa bits are then the code.
 template <bool FULL>
-__device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row, int rowsA, int nb, int ncols,
-                                             const GemmArgs& a, int lane)
+__device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA, int tile, int ncols,
+                                             const GemmArgs& a, Outbox& box)
 {
-    const bool row_ok = row < rowsA;
-    if (!__any_sync(0xffffffffu, row_ok)) return;  // the warp's rows are all past the last one
+    const int row = row0 + box.lane;
     constexpr int NCH = kXentTile / 32;
     float m = -INFINITY;
 #pragma unroll 1
@@ -281,8 +295,8 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row, int rowsA,
     // no finite logit in the tile: the sum is 0 and every code the zero code
     const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kLog2e);
     const float magic = 8388608.f;
-    float sum[2] = {0.f, 0.f};
-    uint16_t* out = a.codes ? a.codes + (size_t)(row_ok ? row : 0) * a.ldcode + (size_t)nb * kXentTile : nullptr;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile;
 #pragma unroll 1
     for (int ch = 0; ch < NCH; ++ch) {
         if (!FULL && ch * 32 >= ncols) break;
@@ -292,36 +306,87 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row, int rowsA,
         for (int c = 0; c < 32; ++c) {
             float t = fmaf(__uint_as_float(v[c]), kLog2e, -m2);
             if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
-            sum[c & 1] += exp2_approx(t);
+            sum[c & 3] += exp2_approx(t);
             v[c] = __float_as_uint(fminf(fmaf(t, -kXentSteps, magic), magic + (float)kXentZero));
         }
-        if (out && row_ok) {
+        if (a.codes) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                uint4 o;
-                o.x = __byte_perm(v[g * 8 + 0], v[g * 8 + 1], 0x5410);
-                o.y = __byte_perm(v[g * 8 + 2], v[g * 8 + 3], 0x5410);
-                o.z = __byte_perm(v[g * 8 + 4], v[g * 8 + 5], 0x5410);
-                o.w = __byte_perm(v[g * 8 + 6], v[g * 8 + 7], 0x5410);
-                *reinterpret_cast<uint4*>(out + ch * 32 + g * 8) = o;
+                const uint32_t* q = v + g * 8;
+                box.put((ch & 1) * 4 + g, make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                                                     __byte_perm(q[4], q[5], 0x5410), __byte_perm(q[6], q[7], 0x5410)));
             }
+            // after 64 columns, or the last ones: the row stride is whole 64s, and what
+            // the other half then holds lies past the vocabulary, where nothing reads it
+            if ((ch & 1) == 1 || (!FULL && ch * 32 + 32 >= ncols))
+                box.drain([&](int r, int c, const uint4& q) {
+                    if (row0 + r < rowsA)
+                        *reinterpret_cast<uint4*>(to + (size_t)r * a.ldcode + (ch >> 1) * 64 + c * 8) = q;
+                });
         }
     }
-    // the target's logit: one column read back for each lane whose target is in this tile
-    int tcol = -1;
-    if (row_ok) {
-        const int t = a.target[row] - nb * kXentTile;
-        if (t >= 0 && t < ncols) tcol = t;
+    if (row < rowsA)
+        a.xstat[(size_t)row * a.NB + tile] =
+            make_float2(m == -INFINITY ? -INFINITY : m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
+
+// The product times scale as it leaves for 32 rows x 128 columns: fp32 (part
+// `split` of the parts, or stored, or added to what is there) or bf16, rows
+// through the row map if there is one.
+template <int MODE>
+__device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int rowsA, int col0, int split, float scale,
+                                                const GemmArgs& a, Outbox& box)
+{
+    const bool f32 = MODE == GEMM_SPLITK || a.out_f32;
+    float* out = MODE == GEMM_SPLITK ? a.out_f32 + (size_t)split * a.rowsA * a.ldo : a.out_f32;
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        const int cc = col0 + ch * 32;
+        if (cc >= a.rowsB) break;
+        uint32_t v[32];
+        tmem_ld32_wait(tbase + ch * 32, v);
+        if (MODE != GEMM_SPLITK) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * scale);
+        }
+        if (f32) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) box.put(g, make_uint4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]));
+            box.drain([&](int r, int c, const uint4& q) {
+                const int col = cc + c * 4;
+                if (row0 + r >= rowsA || col >= a.rowsB) return;
+                float4* to = reinterpret_cast<float4*>(out + (size_t)(row0 + r) * a.ldo + col);
+                float4 f = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
+                                       __uint_as_float(q.w));
+                if (MODE != GEMM_SPLITK && a.accumulate) {
+                    const float4 p = *to;
+                    f.x += p.x;
+                    f.y += p.y;
+                    f.z += p.z;
+                    f.w += p.w;
+                }
+                *to = f;
+            });
+            continue;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t* q = v + g * 8;
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = pack_bf16x2(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1]));
+            box.put((ch & 1) * 4 + g, make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        if ((ch & 1) == 1 || cc + 32 >= a.rowsB)
+            box.drain([&](int r, int c, const uint4& q) {
+                const int col = col0 + (ch >> 1) * 64 + c * 8;
+                // (pieces of the other half, if it was not filled, lie past the last column)
+                if (row0 + r >= rowsA || col >= a.rowsB) return;
+                const size_t row = a.row_map ? (size_t)a.row_map[row0 + r] : (size_t)(row0 + r);
+                *reinterpret_cast<uint4*>(a.out + row * a.ldo + col) = q;
+            });
     }
-    uint32_t mine = __ballot_sync(0xffffffffu, tcol >= 0);
-    while (mine) {
-        const int l = __ffs(mine) - 1;
-        mine &= mine - 1;
-        const uint32_t z = tmem_ld1_wait(tbase + (uint32_t)__shfl_sync(0xffffffffu, tcol, l));
-        if (lane == l) a.ztarget[row] = __uint_as_float(z);
-    }
-    if (row_ok)
-        a.xstat[(size_t)row * a.NB + nb] = make_float2(m == -INFINITY ? -INFINITY : m2, sum[0] + sum[1]);
 }
 
 template <int BN, int MODE, int STAGES, int CAP = BN, int KSUB = 1>
@@ -633,17 +698,24 @@ __device__ __forceinline__ void pair_tile_coords(int tile, int num_m, int num_n,
     *nb = first_n + local % gn;
 }
 
-template <int STAGES>
+// Epilogue warps of a CTA: eight for the epilogues that go through shared memory.
+constexpr bool boxed(int mode) { return mode == GEMM_SPLITK || mode == GEMM_XENT || mode == GEMM_SCALED; }
+constexpr int epi_warps(int mode) { return boxed(mode) ? 8 : kEpiThreads / 32; }
+constexpr int kBoxBytes = 4096;  // 32 rows x 128 bytes of one epilogue warp
+
+template <int STAGES, int MODE>
 struct PairLayout {
     static constexpr int A_BYTES = HALF * BK * 2;
     static constexpr int B_BYTES = HALF * BK * 2;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+    static constexpr int BOX_OFF = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFF = BOX_OFF + (boxed(MODE) ? epi_warps(MODE) * kBoxBytes : 0);
     static constexpr int NBARS = 2 * STAGES + 5;
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int BIAS_OFF = (MISC_OFF + 16 + 15) & ~15;
-    static constexpr int COL_OFF = BIAS_OFF + PAIR_N * 4;
-    static constexpr int TOTAL = COL_OFF + 4 * PAIR_N * 4 + 1024;  // + alignment slack
+    static constexpr int COL_OFF = BIAS_OFF + (boxed(MODE) ? 0 : PAIR_N * 4);
+    static constexpr int TOTAL = COL_OFF + (boxed(MODE) ? 0 : 4 * PAIR_N * 4) + 1024;  // + alignment slack
+    static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
     static constexpr uint32_t TMEM_COLS = 2 * PAIR_N;
     static_assert(STAGE_BYTES % 1024 == 0, "stages must stay 1024-byte aligned");
 };
@@ -662,19 +734,20 @@ __device__ __forceinline__ uint64_t operand_desc(bool mn, uint32_t addr)
 }
 
 template <int MODE, int STAGES, int CAP = PAIR_N, bool A_MN = false, bool B_MN = false>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
     k_gemm_pair(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const GemmArgs a)
 {
     static_assert(MODE != GEMM_GATE_SWAP, "row-wise epilogues only");
-    static_assert(MODE == GEMM_DENSE || MODE == GEMM_SPLITK || (!A_MN && !B_MN),
+    static_assert(MODE == GEMM_DENSE || MODE == GEMM_SPLITK || MODE == GEMM_SCALED || (!A_MN && !B_MN),
                   "MN-major operands: dense epilogues only");
     constexpr bool SPLIT = MODE == GEMM_SPLITK;
-    using L = PairLayout<STAGES>;
+    using L = PairLayout<STAGES, MODE>;
     constexpr uint32_t IDESC =
         idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
     constexpr uint64_t A_KSTEP = A_MN ? (16u * 128u) >> 4 : 2u;  // descriptor units (16 B) per 16-deep K step
     constexpr uint64_t B_KSTEP = B_MN ? (16u * 128u) >> 4 : 2u;
-    constexpr int kEpiWarps = 2 * (kEpiThreads / 32);  // tmem-empty arrivals: both CTAs
+    constexpr int kEpiWarps = 2 * epi_warps(MODE);  // tmem-empty arrivals: both CTAs
+    constexpr int kEpiPair = 32 * epi_warps(MODE);
     extern __shared__ uint8_t smem_raw[];
     // Same offset in both CTAs (same kernel, same static shared memory), as the
     // pair MMA addresses the peer's operands with the leader's descriptors.
@@ -834,38 +907,63 @@ __global__ void __launch_bounds__(192, 1)
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int et = threadIdx.x - 64;
         const uint32_t tempty_leader = cluster_addr(tempty, 0);
+        Outbox box{smem + L::BOX_OFF + (boxed(MODE) ? warp - 2 : 0) * kBoxBytes, lane};
+        const float scale = MODE == GEMM_SCALED ? *a.scale : 1.f;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = pair; tile < num_tiles; tile += num_pairs) {
             int mb, nb;
             pair_tile_coords(SPLIT ? tile % mn_tiles : tile, num_m, num_n, &mb, &nb);
-            named_bar_sync(1, kEpiThreads);  // previous tile's shared-memory reads are done
-            if constexpr (MODE != GEMM_XENT) for (int c = et; c < PAIR_N; c += kEpiThreads) {
-                const int col = nb * PAIR_N + c;
-                float bv;
-                if (MODE == GEMM_TWELL_RELU)
-                    bv = col < a.rowsB ? a.bias[col] : -INFINITY;
-                else
-                    bv = (a.bias && col < a.rowsB) ? a.bias[col] : 0.f;
-                bias_sm[c] = bv;
+            named_bar_sync(1, kEpiPair);  // previous tile's shared-memory reads are done
+            int target = -1;
+            if constexpr (MODE == GEMM_XENT) {
+                const int trow = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
+                if (trow < rowsA) target = a.target[trow];
+            }
+            if constexpr (!boxed(MODE)) {
+                for (int c = et; c < PAIR_N; c += kEpiPair) {
+                    const int col = nb * PAIR_N + c;
+                    float bv;
+                    if (MODE == GEMM_TWELL_RELU)
+                        bv = col < a.rowsB ? a.bias[col] : -INFINITY;
+                    else
+                        bv = (a.bias && col < a.rowsB) ? a.bias[col] : 0.f;
+                    bias_sm[c] = bv;
+                }
             }
             if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) *epi_fail = 1;
-            named_bar_sync(1, kEpiThreads);
+            named_bar_sync(1, kEpiPair);
             if (*epi_fail) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * PAIR_N);
             const int row = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
-            if constexpr (MODE == GEMM_TWELL_RELU)
+            if constexpr (boxed(MODE)) {
+                const int half = (warp - 2) >> 2;  // this warp's 128 of the tile's columns
+                const uint32_t tb = tbase + 128u * (uint32_t)half;
+                const int row0 = row - lane, col0 = nb * PAIR_N + 128 * half;
+                if (row0 < rowsA && col0 < a.rowsB) {  // else all past the last row or column
+                    if constexpr (MODE == GEMM_XENT) {
+                        // the target's logit: one column for each lane whose target is here
+                        const int tc = target - col0;
+                        const bool here = row < rowsA && tc >= 0 && tc < kXentTile;
+                        uint32_t lanes = __ballot_sync(0xffffffffu, here);
+                        while (lanes) {
+                            const int l = __ffs(lanes) - 1;
+                            lanes &= lanes - 1;
+                            const uint32_t z = tmem_ld1_wait(tb + (uint32_t)__shfl_sync(0xffffffffu, tc, l));
+                            if (lane == l) a.ztarget[row] = __uint_as_float(z);
+                        }
+                        const int ncols = min(kXentTile, a.rowsB - col0);
+                        if (ncols == kXentTile)
+                            epi_xent_row<true>(tb, row0, rowsA, col0 / kXentTile, ncols, a, box);
+                        else
+                            epi_xent_row<false>(tb, row0, rowsA, col0 / kXentTile, ncols, a, box);
+                    } else {
+                        epi_product_row<MODE>(tb, row0, rowsA, col0, SPLIT ? tile / mn_tiles : 0, scale, a, box);
+                    }
+                }
+            } else if constexpr (MODE == GEMM_TWELL_RELU)
                 epi_twell_row<PAIR_N, CAP>(tbase, row, rowsA, nb, a, bias_sm);
-            else if constexpr (MODE == GEMM_XENT) {
-                const int ncols = min(kXentTile, a.rowsB - nb * PAIR_N);
-                if (ncols == kXentTile)
-                    epi_xent_row<true>(tbase, row, rowsA, nb, ncols, a, lane);
-                else
-                    epi_xent_row<false>(tbase, row, rowsA, nb, ncols, a, lane);
-            } else if constexpr (SPLIT)
-                epi_partial_row<PAIR_N>(tbase, row, rowsA, nb, a,
-                                        a.out_f32 + (size_t)(tile / mn_tiles) * a.split_stride);
             else
                 epi_dense_row<PAIR_N>(tbase, row, rowsA, nb, a, bias_sm, s_col, 2 * mb + (int)rank, q, et);
             tc_fence_before();
@@ -977,7 +1075,7 @@ int pair_capacity(cudaLaunchConfig_t cfg)
 template <int MODE, int STAGES, int CAP = PAIR_N, bool A_MN = false, bool B_MN = false>
 cudaError_t run_pair(const uint16_t* A, const uint16_t* B, const GemmArgs& a, cudaStream_t s, bool* launched)
 {
-    using L = PairLayout<STAGES>;
+    using L = PairLayout<STAGES, MODE>;
     *launched = false;
     auto kern = k_gemm_pair<MODE, STAGES, CAP, A_MN, B_MN>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
@@ -989,7 +1087,7 @@ cudaError_t run_pair(const uint16_t* A, const uint16_t* B, const GemmArgs& a, cu
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(192, 1, 1);
+    cfg.blockDim = dim3(64 + 32 * epi_warps(MODE), 1, 1);
     cfg.dynamicSmemBytes = L::TOTAL;
     cfg.stream = s;
     cfg.attrs = attr;
@@ -1057,11 +1155,18 @@ cudaError_t launch_gemm(int mode, const uint16_t* A, const uint16_t* B, const Ge
             return launched ? cudaSuccess : cudaErrorNotSupported;
         }
         case GEMM_SPLITK:
+        case GEMM_SCALED:
         case GEMM_XENT: {
             bool launched = false;
-            const cudaError_t e = mode == GEMM_XENT
-                                      ? run_pair<GEMM_XENT, 6>(A, B, a, s, &launched)
-                                      : run_pair<GEMM_SPLITK, 6, PAIR_N, false, true>(A, B, a, s, &launched);
+            cudaError_t e;
+            if (mode == GEMM_XENT)
+                e = run_pair<GEMM_XENT, 6>(A, B, a, s, &launched);
+            else if (mode == GEMM_SPLITK)
+                e = run_pair<GEMM_SPLITK, 6, PAIR_N, false, true>(A, B, a, s, &launched);
+            else if (a.a_mn)
+                e = run_pair<GEMM_SCALED, 6, PAIR_N, true, true>(A, B, a, s, &launched);
+            else
+                e = run_pair<GEMM_SCALED, 6, PAIR_N, false, true>(A, B, a, s, &launched);
             if (e != cudaSuccess) return e;
             return launched ? cudaSuccess : cudaErrorNotSupported;
         }

@@ -3,16 +3,17 @@
 //
 //   z = x W^T          x [N, d] hidden rows, W [V, d] the head, one row per word
 //   lse_r = log sum_j exp z_rj,   nll_r = lse_r - z_r,target(r)
-//   dz_rj = g (exp(z_rj - lse_r) - [j = target(r)])
-//   dx = dz W,  dW = dz^T x
+//   dz_rj = exp(z_rj - lse_r) - [j = target(r)]
+//   dx = g dz W,  dW = g dz^T x     g = grad_scale, or grad_scale / scored rows
 //
 // Three products of 2 N V d operations bound it. The softmax needs a whole row
 // before its first gradient, so a gradient without stored logits either
 // computes the logits twice (a fourth product) or keeps something smaller. What
 // is kept here, for one chunk of rows at a time, are 16-bit codes of the
-// logits' distances to their (row, 256 words) maximum, written by the first
+// logits' distances to their (row, 128 words) maximum, written by the first
 // product's epilogue (twell_gemm.cu). One pass rewrites the codes in place as
-// bf16 dz, the operand of the two other products. Six bytes a logit cost
+// bf16 dz, the operand of the two other products; g enters with their fp32
+// results, so that a target's -1 stays exact whatever g is. Six bytes a logit cost
 // 0.9 ps at the memory's rate, a fourth product d * 1.03 fs: the codes cost
 // less from d = 860 on, and they round dz once, as any bf16 operand is.
 //
@@ -22,12 +23,12 @@
 //
 //   k_xent_prep    orders the rows (scored first), counts them, checks the targets
 //   k_xent_gather  the scored rows of x together; zeros for the others
-//   GEMM_XENT      codes, per-(row, 256 words) maxima and sums, target logits
+//   GEMM_XENT      codes, per-(row, 128 words) maxima and sums, target logits
 //   k_xent_lse     one warp per row: lse, nll
 //   k_xent_dz      codes -> bf16 dz, in place
 //   GEMM_SPLITK    dx; with few output tiles the vocabulary (its depth) is split
 //                  over the GPU and k_xent_dx adds the parts in order
-//   GEMM_DENSE     dW (operands read MN-major, nothing is transposed)
+//   GEMM_SCALED    dx as a whole, and dW (operands read MN-major, nothing is transposed)
 //   k_xent_loss    the sum or mean of the losses
 // Every sum is taken in a fixed order.
 #include "common.cuh"
@@ -257,10 +258,9 @@ __global__ void __launch_bounds__(256)
     w.lse2[row] = (float)(l * 1.4426950408889634074);
 }
 
-// Codes to bf16 dz in place, one warp per (row, 256 words):
-// dz = g 2^(m2 - q / 2048 - lse2). The target's entry is g (p - 1) =
-// g expm1(-nll), which stays exact where p is close to 1. A row without a
-// finite lse is NaN throughout.
+// Codes to bf16 dz in place, one warp per (row, 256 words), eight words a lane:
+// dz = 2^(m2 - q / 2048 - lse2). The target's entry is p - 1 = expm1(-nll), which
+// stays exact where p is close to 1. A row without a finite lse is NaN throughout.
 __global__ void __launch_bounds__(256)
     k_xent_dz(XentWs w, size_t ldcode, int tiles, const int32_t* __restrict__ target,
               const int32_t* __restrict__ rows_dev, int max_rows, const int32_t* status)
@@ -269,11 +269,11 @@ __global__ void __launch_bounds__(256)
     const int lane = threadIdx.x & 31;
     const int rows = *rows_dev;
     const int padded = min(max_rows, max((rows + 63) / 64 * 64, 64));  // zeros up to the depth dW reads
-    const float g = *w.gscale;
-    const size_t total = (size_t)padded * tiles;
+    const int spans = (int)((ldcode + 255) / 256);
+    const size_t total = (size_t)padded * spans;
     for (size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (size_t)gridDim.x * 8) {
-        const int row = (int)(i / tiles), nb = (int)(i % tiles);
-        const int col = nb * kXentTile + lane * 8;
+        const int row = (int)(i / spans);
+        const int col = (int)(i % spans) * 256 + lane * 8;
         if ((size_t)col >= ldcode) continue;
         uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + col);
         if (row >= rows) {
@@ -282,19 +282,20 @@ __global__ void __launch_bounds__(256)
         }
         const uint4 q = *p;
         const float l2 = w.lse2[row];
-        const float shift = w.stat[i].x - l2;
-        const float gg = isfinite(l2) ? g : NAN;
+        const int tile = min(col / kXentTile, tiles - 1);  // the padding past the last word has no tile of its own
+        const float shift = w.stat[(size_t)row * tiles + tile].x - l2;
+        const float one = isfinite(l2) ? 1.f : NAN;
         const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
         float f[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t c = (e & 1) ? qw[e >> 1] >> 16 : qw[e >> 1] & 0xffffu;
             f[e] = c == kXentZero ? 0.f : exp2_approx(fmaf((float)c, -1.f / kXentSteps, shift));
-            f[e] *= gg;
+            f[e] *= one;
         }
         const int t = target[row] - col;
         if (t >= 0 && t < 8) {
-            const float ft = gg * expm1f(-w.nll[row]);
+            const float ft = one * expm1f(-w.nll[row]);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (e == t) f[e] = ft;
@@ -304,12 +305,14 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// dx = bf16 of the parts added in order, each scored row at its place.
+// dx = bf16 of g times the parts added in order, each scored row at its place.
 __global__ void __launch_bounds__(256)
     k_xent_dx(const float* __restrict__ parts, int splits, size_t stride, const int32_t* __restrict__ rows_dev, int d,
-              const int32_t* __restrict__ perm, uint16_t* __restrict__ dx, const int32_t* status)
+              const float* __restrict__ scale, const int32_t* __restrict__ perm, uint16_t* __restrict__ dx,
+              const int32_t* status)
 {
     if (has_error(status)) return;
+    const float g = *scale;
     const int d4 = d / 4;
     const size_t n4 = (size_t)*rows_dev * d4;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
@@ -323,7 +326,7 @@ __global__ void __launch_bounds__(256)
         }
         const size_t row = i / d4, c = i % d4;
         reinterpret_cast<uint2*>(dx + (size_t)perm[row] * d)[c] =
-            make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+            make_uint2(pack_bf16x2(g * a.x, g * a.y), pack_bf16x2(g * a.z, g * a.w));
     }
 }
 
@@ -391,7 +394,7 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     const int tiles = (V + kXentTile - 1) / kXentTile;
     const size_t ldcode = code_stride(V);
     count_launches(1);
-    k_xent_dz<<<blocks_for((size_t)rows * tiles, 8, sms), 256, 0, s>>>(w, ldcode, tiles, w.target + r0, w.rows_dev + c,
+    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + 255) / 256), 8, sms), 256, 0, s>>>(w, ldcode, tiles, w.target + r0, w.rows_dev + c,
                                                                        rows, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -410,17 +413,17 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     if (splits == 1) {
         g2.out = g.dx;
         g2.row_map = w.perm + r0;
-        e = launch_gemm(GEMM_DENSE, w.codes, W, g2, sms, s);
+        g2.scale = w.gscale;
+        e = launch_gemm(GEMM_SCALED, w.codes, W, g2, sms, s);
     } else {
         g2.k_splits = splits;
         g2.kb_per_split = per;
-        g2.split_stride = (size_t)rows * d;
         g2.out_f32 = w.parts;
         e = launch_gemm(GEMM_SPLITK, w.codes, W, g2, sms, s);
         if (e != cudaSuccess) return e;
         count_launches(1);
         k_xent_dx<<<blocks_for((size_t)rows * d / 4, 256, sms), 256, 0, s>>>(
-            w.parts, splits, g2.split_stride, w.rows_dev + c, d, w.perm + r0, g.dx, status);
+            w.parts, splits, (size_t)rows * d, w.rows_dev + c, d, w.gscale, w.perm + r0, g.dx, status);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
@@ -434,6 +437,7 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     g3.a_mn = 1;
     g3.b_mn = 1;
     g3.ldo = d;
+    g3.scale = w.gscale;
     g3.status = status;
     if (w.dw_acc || g.dw_type == TWELL_F32) {
         g3.out_f32 = w.dw_acc ? w.dw_acc : static_cast<float*>(g.dW);
@@ -441,7 +445,7 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     } else {
         g3.out = static_cast<uint16_t*>(g.dW);
     }
-    return launch_gemm(GEMM_DENSE, w.codes, w.xs + (size_t)r0 * d, g3, sms, s);
+    return launch_gemm(GEMM_SCALED, w.codes, w.xs + (size_t)r0 * d, g3, sms, s);
 }
 
 // Both entry points: losses, and with g.dW the gradients.
