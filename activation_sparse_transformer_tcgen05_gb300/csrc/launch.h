@@ -153,7 +153,7 @@ struct GemmArgs {
     const uint16_t* mask;  //   if set, [rowsA, ldm] bf16: result kept only where mask is nonzero
     int ldm;
     float add_scalar;      //   added to every result before the mask (fp32 and bf16 outputs)
-    int lda;               // SPLITK / SCALED: row stride of A's array in elements (0: packed)
+    int lda, ldb;          // SPLITK / SCALED / XENT: row strides of A's and B's arrays in elements (0: packed)
     int k_splits;          // SPLITK: the depth in this many parts of kb_per_split 64-deep k-blocks (the last one
     int kb_per_split;      //   may be shorter, none empty); out_f32 is [k_splits, rowsA, ldo]
     const float* scale;    // SCALED: device scalar that multiplies the product (out, with row_map if set, or

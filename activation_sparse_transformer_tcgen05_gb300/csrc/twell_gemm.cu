@@ -367,25 +367,25 @@ __device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int ro
                 }
                 *to = f;
             });
-            continue;
-        }
+        } else if constexpr (MODE != GEMM_SPLITK) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const uint32_t* q = v + g * 8;
-            uint32_t o[4];
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t* q = v + g * 8;
+                uint32_t o[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = pack_bf16x2(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1]));
-            box.put((ch & 1) * 4 + g, make_uint4(o[0], o[1], o[2], o[3]));
+                for (int e = 0; e < 4; ++e)
+                    o[e] = pack_bf16x2(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1]));
+                box.put((ch & 1) * 4 + g, make_uint4(o[0], o[1], o[2], o[3]));
+            }
+            if ((ch & 1) == 1 || cc + 32 >= a.rowsB)
+                box.drain([&](int r, int c, const uint4& q) {
+                    const int col = col0 + (ch >> 1) * 64 + c * 8;
+                    // (pieces of the other half, if it was not filled, lie past the last column)
+                    if (row0 + r >= rowsA || col >= a.rowsB) return;
+                    const size_t row = a.row_map ? (size_t)a.row_map[row0 + r] : (size_t)(row0 + r);
+                    *reinterpret_cast<uint4*>(a.out + row * a.ldo + col) = q;
+                });
         }
-        if ((ch & 1) == 1 || cc + 32 >= a.rowsB)
-            box.drain([&](int r, int c, const uint4& q) {
-                const int col = col0 + (ch >> 1) * 64 + c * 8;
-                // (pieces of the other half, if it was not filled, lie past the last column)
-                if (row0 + r >= rowsA || col >= a.rowsB) return;
-                const size_t row = a.row_map ? (size_t)a.row_map[row0 + r] : (size_t)(row0 + r);
-                *reinterpret_cast<uint4*>(a.out + row * a.ldo + col) = q;
-            });
     }
 }
 
@@ -1096,7 +1096,7 @@ cudaError_t run_pair(const uint16_t* A, const uint16_t* B, const GemmArgs& a, cu
     if (cap <= 0) return cudaSuccess;
     CUtensorMap ma, mb;
     const bool ok_a = A_MN ? make_map_mn(&ma, A, a.rowsA, a.K, a.lda) : make_map(&ma, A, a.rowsA, a.K, HALF, a.lda);
-    const bool ok_b = B_MN ? make_map_mn(&mb, B, a.rowsB, a.K) : make_map(&mb, B, a.rowsB, a.K, HALF);
+    const bool ok_b = B_MN ? make_map_mn(&mb, B, a.rowsB, a.K, a.ldb) : make_map(&mb, B, a.rowsB, a.K, HALF, a.ldb);
     if (!ok_a || !ok_b) return cudaErrorInvalidValue;
     const int tiles = ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + PAIR_N - 1) / PAIR_N) *
                       (MODE == GEMM_SPLITK ? a.k_splits : 1);

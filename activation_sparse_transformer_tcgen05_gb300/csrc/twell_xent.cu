@@ -24,12 +24,11 @@
 //   k_xent_prep    orders the rows (scored first), counts them, checks the targets
 //   k_xent_gather  the scored rows of x together; zeros for the others
 //   GEMM_XENT      codes, per-(row, 128 words) maxima and sums, target logits
-//   k_xent_lse     one warp per row: lse, nll
+//   k_xent_lse     one warp per row: lse, nll; the sum or mean of the losses
 //   k_xent_dz      codes -> bf16 dz, in place
 //   GEMM_SPLITK    dx; with few output tiles the vocabulary (its depth) is split
 //                  over the GPU and k_xent_dx adds the parts in order
 //   GEMM_SCALED    dx as a whole, and dW (operands read MN-major, nothing is transposed)
-//   k_xent_loss    the sum or mean of the losses
 // Every sum is taken in a fixed order.
 #include "common.cuh"
 #include "launch.h"
@@ -48,7 +47,8 @@ struct XentWs {
     int32_t* k_dev;     // [chunks] the same as a depth of dW (at least 1 in chunk 0, so that dW is written)
     int32_t* perm;      // [N] scored rows ascending, then the others
     int32_t* target;    // [N] targets of the scored rows, in perm's order
-    uint16_t* xs;       // [N, d] scored rows of x, zeros in the 64 rows after them
+    uint16_t* xs;       // [N, row_stride(d)] scored rows of x, zeros in the 64 rows after them
+    int32_t* done;      // blocks of k_xent_lse that have finished
     float2* stat;       // [chunk, tiles] (maximum in log2 units, sum relative to it)
     float* ztarget;     // [chunk]
     float* lse2;        // [chunk] log2 of the sum of exponentials
@@ -60,8 +60,10 @@ struct XentWs {
 
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 
-// Row stride of the codes: whole 128-byte lines.
-size_t code_stride(int V) { return ((size_t)V + 63) & ~size_t(63); }
+// Row stride of the codes and of the scored rows of x: whole 128-byte lines. (Rows
+// that start inside a line cost the tiles' loads a second line each: with rows of
+// W and x of 1000 elements, 777 x 50001 losses took 85 us, of 1024 62 us.)
+size_t row_stride(int n) { return ((size_t)n + 63) & ~size_t(63); }
 
 // Parts of the depth V of dx = dz W: each (256 x 256 tile, part) is one unit of
 // work of a CTA pair; the time is the waves of units times a unit's k-blocks
@@ -115,13 +117,14 @@ size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, Xent
     w.k_dev = reinterpret_cast<int32_t*>(take(chunks * 4));
     w.perm = reinterpret_cast<int32_t*>(take((size_t)N * 4));
     w.target = reinterpret_cast<int32_t*>(take((size_t)N * 4));
-    w.xs = reinterpret_cast<uint16_t*>(take((size_t)N * d * 2));
+    w.xs = reinterpret_cast<uint16_t*>(take((size_t)N * row_stride(d) * 2));
+    w.done = reinterpret_cast<int32_t*>(take(4));
     w.stat = reinterpret_cast<float2*>(take((size_t)chunk * tiles * 8));
     w.ztarget = reinterpret_cast<float*>(take((size_t)chunk * 4));
     w.lse2 = reinterpret_cast<float*>(take((size_t)chunk * 4));
     w.nll = reinterpret_cast<float*>(take((size_t)chunk * 4));
     if (grad) {
-        w.codes = reinterpret_cast<uint16_t*>(take((size_t)chunk * code_stride(V) * 2));
+        w.codes = reinterpret_cast<uint16_t*>(take((size_t)chunk * row_stride(V) * 2));
         // full chunks and the last, shorter one are each planned on their own
         const size_t full = parts_rows(chunk, d, V), last = parts_rows(chunk > 0 ? N % chunk : 0, d, V);
         w.parts = reinterpret_cast<float*>(take((full > last ? full : last) * d * 4));
@@ -192,6 +195,7 @@ __global__ void __launch_bounds__(kPrepThreads)
         w.k_dev[c] = rows == 0 && c == 0 ? 1 : rows;
     }
     if (threadIdx.x == 0) {
+        *w.done = 0;
         *w.count = total;
         *w.gscale = mean ? grad_scale / (float)(total > 0 ? total : 1) : grad_scale;
     }
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kPrepThreads)
 // 64 rows after them (the depth of dW is read in steps of 64), and zero results
 // for the rows that are not scored.
 __global__ void __launch_bounds__(256)
-    k_xent_gather(const uint16_t* __restrict__ x, int N, int d, XentWs w, float* __restrict__ nll,
+    k_xent_gather(const uint16_t* __restrict__ x, int N, int d, XentWs w, int ldx, float* __restrict__ nll,
                   float* __restrict__ lse, uint16_t* __restrict__ dx, const int32_t* status)
 {
     if (has_error(status)) return;
@@ -210,7 +214,7 @@ __global__ void __launch_bounds__(256)
     const uint4 zero = make_uint4(0, 0, 0, 0);
     for (long long i = blockIdx.x * 8 + (threadIdx.x >> 5); i < N; i += gridDim.x * 8) {
         const int row = w.perm[i];
-        uint4* to = reinterpret_cast<uint4*>(w.xs + (size_t)i * d);
+        uint4* to = reinterpret_cast<uint4*>(w.xs + (size_t)i * ldx);
         if (i < count) {
             const uint4* from = reinterpret_cast<const uint4*>(x + (size_t)row * d);
             for (int c = lane; c < d8; c += 32) to[c] = from[c];
@@ -228,14 +232,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // One warp per scored row: the tiles' (maximum, sum) pairs joined, in the order
-// of the lanes' strides and then a butterfly.
-__global__ void __launch_bounds__(256)
-    k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ perm,
-               float* __restrict__ nll, float* __restrict__ lse, const int32_t* status)
+// of the lanes' strides and then a butterfly. In the call's last chunk the block
+// that finishes last adds up the N losses, in a fixed order and 64 bits.
+__device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int lane, const int32_t* perm, float* nll,
+                                        float* lse)
 {
-    if (has_error(status)) return;
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= *rows_dev) return;
     float m = -INFINITY;
     const float2* st = w.stat + (size_t)row * tiles;
     for (int t = lane; t < tiles; t += 32) m = fmaxf(m, st[t].x);
@@ -256,6 +257,34 @@ __global__ void __launch_bounds__(256)
     nll[perm[row]] = loss;
     w.nll[row] = loss;
     w.lse2[row] = (float)(l * 1.4426950408889634074);
+}
+
+__global__ void __launch_bounds__(256)
+    k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ perm, float* nll,
+               float* lse, int last_chunk, int N, int mean, float* loss, const int32_t* status)
+{
+    if (has_error(status)) return;
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row < *rows_dev) row_lse(w, tiles, row, threadIdx.x & 31, perm, nll, lse);
+    if (!last_chunk) return;
+    __shared__ bool last;
+    __shared__ double part[256];
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) last = atomicAdd(w.done, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!last) return;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < N; i += 256) s += (double)__ldcg(nll + i);
+    part[threadIdx.x] = s;
+    for (int half = 128; half >= 1; half >>= 1) {
+        __syncthreads();
+        if ((int)threadIdx.x < half) part[threadIdx.x] += part[threadIdx.x + half];
+    }
+    if (threadIdx.x == 0) {
+        const int n = *w.count;
+        *loss = n == 0 ? 0.f : (float)(mean ? part[0] / (double)n : part[0]);
+    }
 }
 
 // Codes to bf16 dz in place, one warp per (row, 256 words), eight words a lane:
@@ -341,26 +370,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Sum or mean of the losses, one block, fixed order, in 64 bits.
-__global__ void __launch_bounds__(kPrepThreads)
-    k_xent_loss(const float* __restrict__ nll, int N, const int32_t* __restrict__ count, int mean, float* loss,
-                const int32_t* status)
-{
-    if (has_error(status)) return;
-    double s = 0.0;
-    for (int i = threadIdx.x; i < N; i += kPrepThreads) s += (double)nll[i];
-    __shared__ double part[kPrepThreads];
-    part[threadIdx.x] = s;
-    for (int half = kPrepThreads / 2; half >= 1; half >>= 1) {
-        __syncthreads();
-        if ((int)threadIdx.x < half) part[threadIdx.x] += part[threadIdx.x + half];
-    }
-    if (threadIdx.x == 0) {
-        const int n = *count;
-        *loss = n == 0 ? 0.f : (float)(mean ? part[0] / (double)n : part[0]);
-    }
-}
-
 int sms_current()
 {
     int dev = 0, n = 0;
@@ -392,10 +401,10 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
                         int sms, int32_t* status, cudaStream_t s)
 {
     const int tiles = (V + kXentTile - 1) / kXentTile;
-    const size_t ldcode = code_stride(V);
+    const size_t ldcode = row_stride(V);
     count_launches(1);
-    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + 255) / 256), 8, sms), 256, 0, s>>>(w, ldcode, tiles, w.target + r0, w.rows_dev + c,
-                                                                       rows, status);
+    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + 255) / 256), 8, sms), 256, 0, s>>>(
+        w, ldcode, tiles, w.target + r0, w.rows_dev + c, rows, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
@@ -445,7 +454,8 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     } else {
         g3.out = static_cast<uint16_t*>(g.dW);
     }
-    return launch_gemm(GEMM_SCALED, w.codes, w.xs + (size_t)r0 * d, g3, sms, s);
+    g3.ldb = (int)row_stride(d);
+    return launch_gemm(GEMM_SCALED, w.codes, w.xs + (size_t)r0 * row_stride(d), g3, sms, s);
 }
 
 // Both entry points: losses, and with g.dW the gradients.
@@ -465,10 +475,13 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
     if (e != cudaSuccess) return e;
     if (N > 0) {
         count_launches(1);
-        k_xent_gather<<<blocks_for((size_t)N, 8, sms), 256, 0, s>>>(x, N, d, w, nll, lse, g.dx, status);
+        k_xent_gather<<<blocks_for((size_t)N, 8, sms), 256, 0, s>>>(x, N, d, w, (int)row_stride(d), nll, lse, g.dx,
+                                                                    status);
         e = cudaGetLastError();
-    } else if (grad && !g.accumulate) {
-        e = cudaMemsetAsync(g.dW, 0, (size_t)V * d * (g.dw_type == TWELL_F32 ? 4 : 2), s);
+    } else {
+        e = cudaMemsetAsync(loss, 0, sizeof(float), s);
+        if (e == cudaSuccess && grad && !g.accumulate)
+            e = cudaMemsetAsync(g.dW, 0, (size_t)V * d * (g.dw_type == TWELL_F32 ? 4 : 2), s);
     }
     for (int r0 = 0, c = 0; r0 < N && e == cudaSuccess; r0 += chunk, ++c) {
         const int rows = N - r0 < chunk ? N - r0 : chunk;
@@ -479,15 +492,17 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
         g1.K = d;
         g1.NB = tiles;
         g1.codes = w.codes;
-        g1.ldcode = code_stride(V);
+        g1.ldcode = row_stride(V);
         g1.xstat = w.stat;
         g1.target = w.target + r0;
         g1.ztarget = w.ztarget;
         g1.status = status;
-        e = launch_gemm(GEMM_XENT, w.xs + (size_t)r0 * d, W, g1, sms, s);
+        g1.lda = (int)row_stride(d);
+        e = launch_gemm(GEMM_XENT, w.xs + (size_t)r0 * row_stride(d), W, g1, sms, s);
         if (e != cudaSuccess) return e;
         count_launches(1);
-        k_xent_lse<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(w, tiles, w.rows_dev + c, w.perm + r0, nll, lse, status);
+        k_xent_lse<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(w, tiles, w.rows_dev + c, w.perm + r0, nll, lse,
+                                                              N - r0 <= chunk ? 1 : 0, N, mean, loss, status);
         e = cudaGetLastError();
         if (e == cudaSuccess && grad) e = chunk_grads(w, W, r0, c, rows, d, V, g, sms, status, s);
         if (rows < chunk) break;  // the last chunk; r0 + chunk may pass the range of int
@@ -496,11 +511,6 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
         const size_t n4 = (size_t)V * d / 4;
         count_launches(1);
         k_xent_round<<<blocks_for(n4, 256, sms), 256, 0, s>>>(w.dw_acc, n4, static_cast<uint16_t*>(g.dW), status);
-        e = cudaGetLastError();
-    }
-    if (e == cudaSuccess) {
-        count_launches(1);
-        k_xent_loss<<<1, kPrepThreads, 0, s>>>(nll, N, w.count, mean, loss, status);
         e = cudaGetLastError();
     }
     return e;
