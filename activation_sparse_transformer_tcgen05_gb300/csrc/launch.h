@@ -154,8 +154,8 @@ struct GemmArgs {
     int ldm;
     float add_scalar;      //   added to every result before the mask (fp32 and bf16 outputs)
     int lda, ldb;          // SPLITK / SCALED / XENT: row strides of A's and B's arrays in elements (0: packed)
-    int k_splits;          // SPLITK: the depth in this many parts of kb_per_split 64-deep k-blocks (the last one
-    int kb_per_split;      //   may be shorter, none empty); out_f32 is [k_splits, rowsA, ldo]
+    const int2* split;     // SPLITK: on the device, the depth in split->x parts of split->y 64-deep k-blocks (the
+                           //   last one may be shorter, none empty); out_f32 is [split->x, rows used, ldo]
     const float* scale;    // SCALED: device scalar that multiplies the product (out, with row_map if set, or
                            //   out_f32, with accumulate)
     uint16_t* codes;       // XENT: logit codes [rowsA, ldcode], or null: statistics only

@@ -338,7 +338,7 @@ __device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int ro
                                                 const GemmArgs& a, Outbox& box)
 {
     const bool f32 = MODE == GEMM_SPLITK || a.out_f32;
-    float* out = MODE == GEMM_SPLITK ? a.out_f32 + (size_t)split * a.rowsA * a.ldo : a.out_f32;
+    float* out = MODE == GEMM_SPLITK ? a.out_f32 + (size_t)split * rowsA * a.ldo : a.out_f32;
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
         const int cc = col0 + ch * 32;
@@ -805,7 +805,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
     const int num_kb = (gemm_k(a) + BK - 1) / BK;  // same in both CTAs
     const int mn_tiles = num_m * num_n;
     // no k-block: nothing to add or store
-    const int num_tiles = num_kb > 0 ? (SPLIT ? mn_tiles * a.k_splits : mn_tiles) : 0;
+    const int2 parts = SPLIT ? *a.split : make_int2(1, num_kb);  // written by an earlier kernel
+    const int num_tiles = num_kb > 0 ? mn_tiles * parts.x : 0;
     const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
 
     if (warp == 0) {
@@ -819,8 +820,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
             for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
                 int mb, nb;
                 pair_tile_coords(SPLIT ? tile % mn_tiles : tile, num_m, num_n, &mb, &nb);
-                const int kb0 = SPLIT ? tile / mn_tiles * a.kb_per_split : 0;
-                const int kb1 = SPLIT ? min(kb0 + a.kb_per_split, num_kb) : num_kb;
+                const int kb0 = SPLIT ? tile / mn_tiles * parts.y : 0;
+                const int kb1 = SPLIT ? min(kb0 + parts.y, num_kb) : num_kb;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                         ok = false;
@@ -873,8 +874,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                 }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PAIR_N);
-                const int kb0 = SPLIT ? tile / mn_tiles * a.kb_per_split : 0;
-                const int kb1 = SPLIT ? min(kb0 + a.kb_per_split, num_kb) : num_kb;
+                const int kb0 = SPLIT ? tile / mn_tiles * parts.y : 0;
+                const int kb1 = SPLIT ? min(kb0 + parts.y, num_kb) : num_kb;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&full[stage], phase, abort_flag)) {
                         ok = false;
@@ -914,7 +915,7 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
         for (int tile = pair; tile < num_tiles; tile += num_pairs) {
             int mb, nb;
             pair_tile_coords(SPLIT ? tile % mn_tiles : tile, num_m, num_n, &mb, &nb);
-            named_bar_sync(1, kEpiPair);  // previous tile's shared-memory reads are done
+            if constexpr (!boxed(MODE)) named_bar_sync(1, kEpiPair);  // previous tile's shared-memory reads are done
             int target = -1;
             if constexpr (MODE == GEMM_XENT) {
                 const int trow = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
@@ -931,9 +932,16 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                     bias_sm[c] = bv;
                 }
             }
-            if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) *epi_fail = 1;
-            named_bar_sync(1, kEpiPair);
-            if (*epi_fail) break;
+            if constexpr (boxed(MODE)) {  // nothing is shared between the warps
+                if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
+                    *epi_fail = 1;
+                    break;
+                }
+            } else {
+                if (!mbar_wait(&tfull[acc], acc_phase, abort_flag)) *epi_fail = 1;
+                named_bar_sync(1, kEpiPair);
+                if (*epi_fail) break;
+            }
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * PAIR_N);
             const int row = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
@@ -968,7 +976,13 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                 epi_dense_row<PAIR_N>(tbase, row, rowsA, nb, a, bias_sm, s_col, 2 * mb + (int)rank, q, et);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(tempty_leader + 8u * (uint32_t)acc);
+            if (lane == 0) {
+                // a release would wait for the results' stores (a third of the epilogue's time)
+                if constexpr (boxed(MODE))
+                    mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
+                else
+                    mbar_arrive_cluster(tempty_leader + 8u * (uint32_t)acc);
+            }
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
         }
@@ -1098,9 +1112,8 @@ cudaError_t run_pair(const uint16_t* A, const uint16_t* B, const GemmArgs& a, cu
     const bool ok_a = A_MN ? make_map_mn(&ma, A, a.rowsA, a.K, a.lda) : make_map(&ma, A, a.rowsA, a.K, HALF, a.lda);
     const bool ok_b = B_MN ? make_map_mn(&mb, B, a.rowsB, a.K, a.ldb) : make_map(&mb, B, a.rowsB, a.K, HALF, a.ldb);
     if (!ok_a || !ok_b) return cudaErrorInvalidValue;
-    const int tiles = ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + PAIR_N - 1) / PAIR_N) *
-                      (MODE == GEMM_SPLITK ? a.k_splits : 1);
-    cfg.gridDim = dim3(2 * (tiles < cap ? tiles : cap), 1, 1);
+    const int tiles = ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + PAIR_N - 1) / PAIR_N);
+    cfg.gridDim = dim3(2 * (tiles < cap && MODE != GEMM_SPLITK ? tiles : cap), 1, 1);
     count_launches(1);
     *launched = true;
     return cudaLaunchKernelEx(&cfg, kern, ma, mb, a);

@@ -45,6 +45,7 @@ struct XentWs {
     float* gscale;      // gradient factor of a scored row
     int32_t* rows_dev;  // [chunks] scored rows of each chunk
     int32_t* k_dev;     // [chunks] the same as a depth of dW (at least 1 in chunk 0, so that dW is written)
+    int2* split;        // [chunks] parts of dx and the k-blocks of one
     int32_t* perm;      // [N] scored rows ascending, then the others
     int32_t* target;    // [N] targets of the scored rows, in perm's order
     uint16_t* xs;       // [N, row_stride(d)] scored rows of x, zeros in the 64 rows after them
@@ -54,7 +55,7 @@ struct XentWs {
     float* lse2;        // [chunk] log2 of the sum of exponentials
     float* nll;         // [chunk]
     uint16_t* codes;    // [chunk, ldcode] codes, then bf16 dz
-    float* parts;       // [splits, chunk, d] partial dx
+    float* parts;       // [parts, scored rows, d] partial dx
     float* dw_acc;      // [V, d] when a bf16 dW is summed over several chunks
 };
 
@@ -65,38 +66,52 @@ size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 // W and x of 1000 elements, 777 x 50001 losses took 85 us, of 1024 62 us.)
 size_t row_stride(int n) { return ((size_t)n + 63) & ~size_t(63); }
 
-// Parts of the depth V of dx = dz W: each (256 x 256 tile, part) is one unit of
-// work of a CTA pair; the time is the waves of units times a unit's k-blocks
-// plus its epilogue (about 8 k-blocks' worth), and what the parts' fp32 sums
-// cost to write and read again. One part writes dx directly.
-int plan_splits(int rows, int d, int V, int* kb_per)
+// Parts of the depth V of dx = dz W, and the k-blocks of a part: each (256 x 256
+// tile, part) is one unit of work of a CTA pair; the time is the waves of units
+// times a unit's k-blocks (0.28 us each) plus its epilogue (about 8 k-blocks'
+// worth), and what the parts' fp32 sums cost to write and read again. At most
+// three waves of units, which bounds the parts' room.
+constexpr int kMaxUnits = 3 * kPairsNominal;
+
+// Estimated time of `s` parts (1 <= s <= kMaxSplits) in us; infinite where a part would be empty
+// or the units too many.
+__host__ __device__ inline float split_time(int s, int rows, int d, int V)
 {
-    const long long tiles = (long long)((rows + 255) / 256) * ((d + 255) / 256);
-    const int num_kb = (V + 63) / 64;
-    int best = 1, best_per = num_kb;
-    double best_t = 1e30;
-    for (int s = 1; s <= kMaxSplits && s <= num_kb; ++s) {
-        const int per = (num_kb + s - 1) / s;
-        if ((num_kb + per - 1) / per != s) continue;  // an empty part
-        const long long waves = (tiles * s + kPairsNominal - 1) / kPairsNominal;
-        // 0.28 us a k-block; the parts move 8 bytes an element at ~5 TB/s
-        double t = (double)waves * (per + 8) * 0.28;
-        if (s > 1) t += (double)s * rows * d * 8 / 5e6 + 3.0;
-        if (t < best_t) {
-            best_t = t;
-            best = s;
-            best_per = per;
-        }
-    }
-    *kb_per = best_per;
-    return best;
+    const unsigned tiles = (unsigned)((rows + 255) / 256) * (unsigned)((d + 255) / 256);
+    const unsigned num_kb = (unsigned)(V + 63) / 64;
+    if ((unsigned)s > num_kb || (s > 1 && tiles > (unsigned)(kMaxUnits / s))) return INFINITY;
+    const unsigned per = (num_kb + s - 1) / s;
+    if ((num_kb + per - 1) / per != (unsigned)s) return INFINITY;
+    const unsigned waves = (tiles * s + kPairsNominal - 1) / kPairsNominal;
+    const float t = (float)waves * (float)(per + 8) * 0.28f;
+    return s == 1 ? t : t + (float)s * (float)rows * (float)d * 1.6e-6f + 3.f;  // 8 bytes at ~5 TB/s, a launch
 }
 
-size_t parts_rows(int rows, int d, int V)
+bool in_parts(int rows, int d, int V)
 {
-    int per;
-    const int splits = rows > 0 ? plan_splits(rows, d, V, &per) : 1;
-    return splits > 1 ? (size_t)splits * rows : 0;
+    for (int s = 2; s <= kMaxSplits; ++s)
+        if (split_time(s, rows, d, V) < split_time(1, rows, d, V)) return true;
+    return false;
+}
+
+// The best split for a number of rows known on the device; one warp, a lane for each number of parts.
+__device__ __forceinline__ void plan_splits(int rows, int d, int V, int lane, int2* out)
+{
+    static_assert(kMaxSplits == 32, "one lane each");
+    const float mine = split_time(lane + 1, rows, d, V);
+    float best = mine;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, off));
+    const int s = __ffs(__ballot_sync(0xffffffffu, mine == best));
+    const int num_kb = (V + 63) / 64;
+    if (lane == 0) *out = make_int2(s, (num_kb + s - 1) / s);
+}
+
+// Elements of the parts for any number of scored rows up to `rows`.
+size_t parts_elements(int rows, int d)
+{
+    const size_t most = (size_t)kMaxUnits * 256 * 256, all = (size_t)kMaxSplits * rows * d;
+    return most < all ? most : all;
 }
 
 size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, XentWs* out)
@@ -115,6 +130,7 @@ size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, Xent
     w.gscale = reinterpret_cast<float*>(take(4));
     w.rows_dev = reinterpret_cast<int32_t*>(take(chunks * 4));
     w.k_dev = reinterpret_cast<int32_t*>(take(chunks * 4));
+    w.split = reinterpret_cast<int2*>(take(chunks * 8));
     w.perm = reinterpret_cast<int32_t*>(take((size_t)N * 4));
     w.target = reinterpret_cast<int32_t*>(take((size_t)N * 4));
     w.xs = reinterpret_cast<uint16_t*>(take((size_t)N * row_stride(d) * 2));
@@ -125,9 +141,7 @@ size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, Xent
     w.nll = reinterpret_cast<float*>(take((size_t)chunk * 4));
     if (grad) {
         w.codes = reinterpret_cast<uint16_t*>(take((size_t)chunk * row_stride(V) * 2));
-        // full chunks and the last, shorter one are each planned on their own
-        const size_t full = parts_rows(chunk, d, V), last = parts_rows(chunk > 0 ? N % chunk : 0, d, V);
-        w.parts = reinterpret_cast<float*>(take((full > last ? full : last) * d * 4));
+        w.parts = reinterpret_cast<float*>(take(parts_elements(chunk, d) * 4));
         if (acc) w.dw_acc = reinterpret_cast<float*>(take((size_t)V * d * 4));
     }
     if (out) *out = w;
@@ -149,7 +163,7 @@ __device__ __forceinline__ int warp_scan(int v, int lane)
 // thread a run of consecutive rows: their counts are scanned, then each thread
 // places its rows.
 __global__ void __launch_bounds__(kPrepThreads)
-    k_xent_prep(const int64_t* __restrict__ target, int N, int V, int64_t ignore_index, int chunk, int mean,
+    k_xent_prep(const int64_t* __restrict__ target, int N, int d, int V, int64_t ignore_index, int chunk, int mean,
                 float grad_scale, XentWs w, int32_t* status)
 {
     const int run = (N + kPrepThreads - 1) / kPrepThreads;
@@ -193,6 +207,12 @@ __global__ void __launch_bounds__(kPrepThreads)
         const int rows = (int)(left < 0 ? 0 : left < chunk ? left : chunk);
         w.rows_dev[c] = rows;
         w.k_dev[c] = rows == 0 && c == 0 ? 1 : rows;
+    }
+    if (w.parts) {  // gradients
+        for (long long c = warp; c * chunk < N; c += kPrepThreads / 32) {
+            const long long left = (long long)total - c * chunk;
+            plan_splits((int)(left < 0 ? 0 : left < chunk ? left : chunk), d, V, lane, w.split + c);
+        }
     }
     if (threadIdx.x == 0) {
         *w.done = 0;
@@ -287,63 +307,82 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Codes to bf16 dz in place, one warp per (row, 256 words), eight words a lane:
-// dz = 2^(m2 - q / 2048 - lse2). The target's entry is p - 1 = expm1(-nll), which
-// stays exact where p is close to 1. A row without a finite lse is NaN throughout.
+// Codes to bf16 dz in place: dz = 2^(m2 - q / 2048 - lse2). The target's entry is
+// p - 1 = expm1(-nll), which stays exact where p is close to 1. A row without a
+// finite lse is NaN throughout. Bound by memory (4 bytes a logit); a block takes
+// kDzSpan columns of one row, two 16-byte pieces a thread, all asked for at once.
+constexpr int kDzPieces = 2, kDzSpan = 256 * 8 * kDzPieces;
+
 __global__ void __launch_bounds__(256)
-    k_xent_dz(XentWs w, size_t ldcode, int tiles, const int32_t* __restrict__ target,
+    k_xent_dz(XentWs w, size_t ldcode, int tiles, const int32_t* __restrict__ targets,
               const int32_t* __restrict__ rows_dev, int max_rows, const int32_t* status)
 {
     if (has_error(status)) return;
-    const int lane = threadIdx.x & 31;
     const int rows = *rows_dev;
     const int padded = min(max_rows, max((rows + 63) / 64 * 64, 64));  // zeros up to the depth dW reads
-    const int spans = (int)((ldcode + 255) / 256);
-    const size_t total = (size_t)padded * spans;
-    for (size_t i = (size_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (size_t)gridDim.x * 8) {
+    const int spans = (int)((ldcode + kDzSpan - 1) / kDzSpan);
+    for (long long i = blockIdx.x; i < (long long)padded * spans; i += gridDim.x) {
         const int row = (int)(i / spans);
-        const int col = (int)(i % spans) * 256 + lane * 8;
-        if ((size_t)col >= ldcode) continue;
-        uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + col);
+        const long long c0 = (i % spans) * kDzSpan + threadIdx.x * 8;
+        uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + c0);
         if (row >= rows) {
-            *p = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < kDzPieces; ++k)
+                if (c0 + k * 2048 < (long long)ldcode) p[k * 256] = make_uint4(0, 0, 0, 0);
             continue;
         }
-        const uint4 q = *p;
+        uint4 q[kDzPieces];
+        float m2[kDzPieces];
+#pragma unroll
+        for (int k = 0; k < kDzPieces; ++k) {
+            const long long c = c0 + k * 2048;
+            if (c < (long long)ldcode) {
+                q[k] = p[k * 256];
+                // (the padding past the last word has no tile of its own)
+                m2[k] = w.stat[(size_t)row * tiles + min((int)(c / kXentTile), tiles - 1)].x;
+            }
+        }
         const float l2 = w.lse2[row];
-        const int tile = min(col / kXentTile, tiles - 1);  // the padding past the last word has no tile of its own
-        const float shift = w.stat[(size_t)row * tiles + tile].x - l2;
         const float one = isfinite(l2) ? 1.f : NAN;
-        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
-        float f[8];
+        const int target = targets[row];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t c = (e & 1) ? qw[e >> 1] >> 16 : qw[e >> 1] & 0xffffu;
-            f[e] = c == kXentZero ? 0.f : exp2_approx(fmaf((float)c, -1.f / kXentSteps, shift));
-            f[e] *= one;
-        }
-        const int t = target[row] - col;
-        if (t >= 0 && t < 8) {
-            const float ft = one * expm1f(-w.nll[row]);
+        for (int k = 0; k < kDzPieces; ++k) {
+            const long long c = c0 + k * 2048;
+            if (c >= (long long)ldcode) break;
+            const float shift = m2[k] - l2;
+            const uint32_t qw[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
+            float f[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e == t) f[e] = ft;
+            for (int e = 0; e < 8; ++e) {
+                // the code as the low mantissa bits of 2^23 + code: an integer conversion shares
+                // the special-function unit with the exponential (8192 x 4096 x 65536: 373 us with it, 290 without)
+                const float v = __uint_as_float(__byte_perm(qw[e >> 1], 0x4b00u, (e & 1) ? 0x5432 : 0x5410)) - 8388608.f;
+                f[e] = v == (float)kXentZero ? 0.f : exp2_approx(fmaf(v, -1.f / kXentSteps, shift));
+                f[e] *= one;
+            }
+            const long long t = target - c;
+            if (t >= 0 && t < 8) {
+                const float ft = one * expm1f(-w.nll[row]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e == (int)t) f[e] = ft;
+            }
+            p[k * 256] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                    pack_bf16x2(f[6], f[7]));
         }
-        *p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                        pack_bf16x2(f[6], f[7]));
     }
 }
 
 // dx = bf16 of g times the parts added in order, each scored row at its place.
 __global__ void __launch_bounds__(256)
-    k_xent_dx(const float* __restrict__ parts, int splits, size_t stride, const int32_t* __restrict__ rows_dev, int d,
+    k_xent_dx(const float* __restrict__ parts, const int2* __restrict__ split, const int32_t* __restrict__ rows_dev, int d,
               const float* __restrict__ scale, const int32_t* __restrict__ perm, uint16_t* __restrict__ dx,
               const int32_t* status)
 {
     if (has_error(status)) return;
     const float g = *scale;
-    const int d4 = d / 4;
-    const size_t n4 = (size_t)*rows_dev * d4;
+    const int d4 = d / 4, splits = split->x;
+    const size_t n4 = (size_t)*rows_dev * d4, stride = n4 * 4;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
         float4 a = reinterpret_cast<const float4*>(parts)[i];
         for (int p = 1; p < splits; ++p) {
@@ -403,13 +442,11 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     const int tiles = (V + kXentTile - 1) / kXentTile;
     const size_t ldcode = row_stride(V);
     count_launches(1);
-    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + 255) / 256), 8, sms), 256, 0, s>>>(
+    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + kDzSpan - 1) / kDzSpan), 1, sms), 256, 0, s>>>(
         w, ldcode, tiles, w.target + r0, w.rows_dev + c, rows, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 
-    int per = 0;
-    const int splits = plan_splits(rows, d, V, &per);
     GemmArgs g2{};
     g2.rowsA = rows;
     g2.rowsA_dev = w.rows_dev + c;
@@ -419,20 +456,20 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     g2.b_mn = 1;
     g2.ldo = d;
     g2.status = status;
-    if (splits == 1) {
+    // whole or in parts by the rows there may be; how many parts by those that are scored
+    if (!in_parts(rows, d, V)) {
         g2.out = g.dx;
         g2.row_map = w.perm + r0;
         g2.scale = w.gscale;
         e = launch_gemm(GEMM_SCALED, w.codes, W, g2, sms, s);
     } else {
-        g2.k_splits = splits;
-        g2.kb_per_split = per;
+        g2.split = w.split + c;
         g2.out_f32 = w.parts;
         e = launch_gemm(GEMM_SPLITK, w.codes, W, g2, sms, s);
         if (e != cudaSuccess) return e;
         count_launches(1);
         k_xent_dx<<<blocks_for((size_t)rows * d / 4, 256, sms), 256, 0, s>>>(
-            w.parts, splits, (size_t)rows * d, w.rows_dev + c, d, w.gscale, w.perm + r0, g.dx, status);
+            w.parts, w.split + c, w.rows_dev + c, d, w.gscale, w.perm + r0, g.dx, status);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
@@ -470,7 +507,7 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
     carve(ws, N, chunk, d, V, grad, grad && g.dw_type == TWELL_BF16 && chunk < N, &w);
     const int tiles = (V + kXentTile - 1) / kXentTile;
     count_launches(1);
-    k_xent_prep<<<1, kPrepThreads, 0, s>>>(target, N, V, ignore_index, chunk > 0 ? chunk : 1, mean, g.scale, w, status);
+    k_xent_prep<<<1, kPrepThreads, 0, s>>>(target, N, d, V, ignore_index, chunk > 0 ? chunk : 1, mean, g.scale, w, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (N > 0) {
