@@ -176,7 +176,13 @@ def twell_device_sm_count() -> int:
 
 # ------------------------------------------------------------- marshalling --
 
+# The current stream's handle without building a torch.cuda.Stream (0.3 against 2.9 us on the host, of a call's ~10).
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None) -> ctypes.c_void_p:
+    if stream is None and _current_handle is not None:
+        return ctypes.c_void_p(_current_handle(torch.cuda.current_device()))
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -421,12 +427,14 @@ def twell_dense_ffn_bwd(x, W_up, W_down, h_dense, dy, l1: float, dx, dW_up, dW_d
         _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_dense_ffn_bwd")
 
 
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.int16: DTYPE_BF16, torch.float32: DTYPE_F32}
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
-    if t.dtype is torch.bfloat16 or t.dtype is torch.int16:
-        return DTYPE_BF16
-    if t.dtype is torch.float32:
-        return DTYPE_F32
-    raise ValueError(f"{name} must be bfloat16 (or its int16 bits) or float32, got {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 (or its int16 bits) or float32, got {t.dtype}")
+    return code
 
 
 def _rows(t: torch.Tensor | None, name: str, N: int, d: int, dtype: int):
@@ -435,11 +443,12 @@ def _rows(t: torch.Tensor | None, name: str, N: int, d: int, dtype: int):
         return None, 0
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[0] != N or t.shape[1] != d or (d > 1 and t.stride(1) != 1):
+    strides = t.stride()
+    if t.shape != (N, d) or (d > 1 and strides[1] != 1):
         raise ValueError(f"{name} must be a [{N}, {d}] matrix with unit column stride")
-    if _dtype(t, name) != dtype:
+    if _DTYPES.get(t.dtype) != dtype:
         raise ValueError(f"{name} has another element type ({t.dtype}) than the tensors it goes with")
-    return t.data_ptr(), t.stride(0) if N > 1 else d
+    return t.data_ptr(), strides[0] if N > 1 else d
 
 
 def _vec(t: torch.Tensor | None, name: str, n: int, dtype: int):
@@ -450,7 +459,7 @@ def _vec(t: torch.Tensor | None, name: str, n: int, dtype: int):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must have {n} contiguous elements")
-    if _dtype(t, name) != dtype:
+    if _DTYPES.get(t.dtype) != dtype:
         raise ValueError(f"{name} has the wrong element type ({t.dtype})")
     return t.data_ptr()
 
