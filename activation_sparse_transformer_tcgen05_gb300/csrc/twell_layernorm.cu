@@ -4,8 +4,6 @@
 //   forward   s = x + res, hat = (s - mean) rstd, y = hat w + b
 //   backward  v = w dy, dx = rstd (v - mean(v) - hat mean(v hat)) + dres,
 //             dw = sum_r dy hat, db = sum_r dy
-#include <string.h>
-
 #include "common.cuh"
 #include "launch.h"
 
@@ -235,8 +233,33 @@ struct Piece<bf16_t, 1> {
     __device__ __forceinline__ void set(const float* f) { v = f32_to_bf16_bits(f[0]); }
     __device__ __forceinline__ void store(uint16_t* p) const { *p = v; }
 };
+template <>
+struct Piece<bf16_t, 4> {
+    uint2 v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint2*>(p); }
+    __device__ __forceinline__ void zero() { v = make_uint2(0, 0); }
+    __device__ __forceinline__ float get(int i) const
+    {
+        const uint32_t w = i < 2 ? v.x : v.y;
+        return (i & 1) ? bf16_hi(w) : bf16_lo(w);
+    }
+    __device__ __forceinline__ void set(const float* f)
+    {
+        v = make_uint2(Piece<bf16_t, 8>::pair(f[0], f[1]), Piece<bf16_t, 8>::pair(f[2], f[3]));
+    }
+    __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = v; }
+};
+template <>
+struct Piece<f32_t, 4> {
+    float4 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float4*>(p); }
+    __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+    __device__ __forceinline__ void set(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = v; }
+};
 template <int VEC>
-struct Piece<f32_t, VEC> {
+struct Piece<f32_t, VEC> {  // (weights only)
     static_assert(VEC == 8, "");
     float4 a, b;
     __device__ __forceinline__ void load(const float* p)
@@ -248,16 +271,6 @@ struct Piece<f32_t, VEC> {
     __device__ __forceinline__ float get(int i) const
     {
         return i == 0 ? a.x : i == 1 ? a.y : i == 2 ? a.z : i == 3 ? a.w : i == 4 ? b.x : i == 5 ? b.y : i == 6 ? b.z : b.w;
-    }
-    __device__ __forceinline__ void set(const float* f)
-    {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
-    }
-    __device__ __forceinline__ void store(float* p) const
-    {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
     }
 };
 template <>
@@ -345,9 +358,13 @@ __device__ __forceinline__ void load_weights(const void* p, int i, bool f32, flo
     }
 }
 
-__device__ __forceinline__ void copy_async16(void* smem, const void* global)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* smem, const void* global)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -356,64 +373,76 @@ __device__ __forceinline__ void copies_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-// Rows on their way: STAGES rows of every stream (x; res or dy; dres), each
-// thread's own pieces side by side (16-byte words, one word of all threads after
-// the other, so that a warp's accesses fall into different banks).
-template <int STAGES, int WORDS>
+// Elements of an aligned piece: 16 bytes of the wider type, so that neighbouring
+// threads' pieces touch (two halves of 32 bytes a thread took each sector twice:
+// 4096 x 2048 fp32 with residual 29.6 us instead of 20.7).
+template <class TX, class TY>
+constexpr int vec_of()
+{
+    return sizeof(typename TX::type) + sizeof(typename TY::type) == 4 ? 8 : 4;
+}
+
+template <class T, int VEC>
+constexpr int piece_bytes()
+{
+    return (int)sizeof(typename T::type) * VEC;
+}
+
+// Rows on their way: STAGES rows of every stream (x; res or dy; dres), BYTES of a
+// row to a thread. A piece is named by its offset in those bytes; the pieces of all
+// threads at one offset lie side by side. `stage`: the bytes before the oldest row.
+template <int STAGES, int BYTES>
 struct Ring {
-    uint4* mine;
-    int stride, stage = 0;
-    __device__ Ring(void* smem) : mine(static_cast<uint4*>(smem) + threadIdx.x), stride(blockDim.x) {}
-    static size_t bytes(int threads) { return (size_t)STAGES * WORDS * threads * 16; }
-    __device__ __forceinline__ uint4* word(int st, int k) { return mine + (size_t)(st * WORDS + k) * stride; }
+    char* base;
+    int threads, stage = 0;
+    __device__ Ring(void* smem) : base(static_cast<char*>(smem)), threads(blockDim.x) {}
+    static size_t bytes(int threads) { return (size_t)STAGES * BYTES * threads; }
+
+    __device__ __forceinline__ void turn()
+    {
+        stage += BYTES * threads;
+        if (stage == STAGES * BYTES * threads) stage = 0;
+    }
+    template <class T, int VEC>
+    __device__ __forceinline__ char* at(int off)
+    {
+        return base + (off * threads + (int)threadIdx.x * piece_bytes<T, VEC>()) + stage;
+    }
+    template <class T, int VEC>
+    __device__ __forceinline__ void get(int off, Piece<T, VEC>& p)
+    {
+        p.load(reinterpret_cast<const typename T::type*>(at<T, VEC>(off)));
+    }
+    template <class T, int VEC>
+    __device__ __forceinline__ void ask(int off, const typename T::type* from)
+    {
+        copy_async<piece_bytes<T, VEC>()>(at<T, VEC>(off), from);
+    }
 };
-
-// 16-byte words of one piece of eight elements.
-template <class T>
-constexpr int words()
-{
-    return (int)sizeof(typename T::type) / 2;
-}
-
-// Piece v of this thread as it arrived in the ring.
-template <class T, class R>
-__device__ __forceinline__ void from_ring(R& ring, int st, int k, Piece<T, 8>& p)
-{
-    uint4 w[words<T>()];
-#pragma unroll
-    for (int i = 0; i < words<T>(); ++i) w[i] = *ring.word(st, k + i);
-    memcpy(&p, w, sizeof(p));
-}
-
-template <class T, class R>
-__device__ __forceinline__ void to_ring(R& ring, int st, int k, const typename T::type* from)
-{
-#pragma unroll
-    for (int i = 0; i < words<T>(); ++i) copy_async16(ring.word(st, k + i), reinterpret_cast<const uint4*>(from) + i);
-}
 
 // Stages of the ring: rows in flight for at most 98 KB with 256 threads of 16
 // elements, so that two blocks fit an SM.
-constexpr int stages_for(int words) { return words <= 6 ? 4 : words <= 8 ? 3 : 2; }
+constexpr int stages_for(int bytes) { return bytes <= 96 ? 4 : bytes <= 128 ? 3 : 2; }
 
 // Blocks of 512 threads that share an SM: two (64 registers a thread) with 8
 // elements a thread, one with 16.
 constexpr int blocks_per_sm(int per) { return per == 8 ? 2 : 1; }
 
 template <class TX, int PER, bool RES>
-constexpr int fwd_words()
+constexpr int fwd_bytes()
 {
-    return PER / 8 * words<TX>() * (RES ? 2 : 1);
+    return PER * (int)sizeof(typename TX::type) * (RES ? 2 : 1);
 }
 
 template <class TX, class TY, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const FwdArgs a, int G)
 {
-    constexpr int NV = PER / VEC, WORDS = fwd_words<TX, PER, RES>(), STAGES = stages_for(WORDS);
+    constexpr int NV = PER / VEC, BYTES = fwd_bytes<TX, PER, RES>(), STAGES = stages_for(BYTES);
+    constexpr int SX = piece_bytes<TX, VEC>();
     extern __shared__ uint4 dyn[];
     __shared__ float2 buf[32];
     RowSum rs(buf, G);
-    Ring<STAGES, WORDS> ring(dyn);
+    Ring<STAGES, BYTES> ring(dyn);
     const int t = threadIdx.x % G;
     const float inv_d = 1.f / (float)a.d;
     float w[PER], b[PER];
@@ -434,14 +463,14 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
     int64_t asked = r;
     const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
     const typename TX::type* aq = RES ? row_of<TX>(a.res, r, a.ldres) + t * VEC : nullptr;
-    auto request = [&](int st) {
-        if constexpr (VEC == 8) {
+    auto request = [&] {
+        if constexpr (VEC > 1) {
             if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    if ((v * G + t) * 8 < a.d) {
-                        to_ring<TX>(ring, st, v * words<TX>(), ax + v * G * 8);
-                        if (RES) to_ring<TX>(ring, st, (NV + v) * words<TX>(), aq + v * G * 8);
+                    if ((v * G + t) * VEC < a.d) {
+                        ring.template ask<TX, VEC>(v * SX, ax + v * G * VEC);
+                        if (RES) ring.template ask<TX, VEC>((NV + v) * SX, aq + v * G * VEC);
                     }
                 }
             }
@@ -452,12 +481,14 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
         }
     };
 #pragma unroll
-    for (int st = 0; st < STAGES; ++st) request(st);
-    int st = 0;
+    for (int i = 0; i < STAGES; ++i) {
+        request();
+        ring.turn();
+    }
     for (; r < a.N; r += step) {
         float f[PER];
         float s = 0.f;
-        if (VEC == 8) copies_wait<STAGES - 1>();
+        if (VEC > 1) copies_wait<STAGES - 1>();
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int i = (v * G + t) * VEC;
@@ -465,9 +496,9 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
             x.zero();
             q.zero();
             if (i < a.d) {
-                if constexpr (VEC == 8) {
-                    from_ring<TX>(ring, st, v * words<TX>(), x);
-                    if (RES) from_ring<TX>(ring, st, (NV + v) * words<TX>(), q);
+                if constexpr (VEC > 1) {
+                    ring.get(v * SX, x);
+                    if (RES) ring.get((NV + v) * SX, q);
                 } else {
                     x.load(row_of<TX>(a.x, r, a.ldx) + i);
                     if (RES) q.load(row_of<TX>(a.res, r, a.ldres) + i);
@@ -486,8 +517,8 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
 #pragma unroll
             for (int e = 0; e < VEC; ++e) s += f[v * VEC + e];
         }
-        request(st);
-        st = st + 1 == STAGES ? 0 : st + 1;
+        request();
+        ring.turn();
         const float mean = rs.sum(s) * inv_d;
         float c2 = 0.f;
 #pragma unroll
@@ -515,13 +546,13 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
             if (a.rstd) a.rstd[r] = rstd;
         }
     }
-    if (VEC == 8) copies_wait<0>();
+    if (VEC > 1) copies_wait<0>();
 }
 
 template <class TX, class TY, int PER, bool RES>
-constexpr int bwd_words()
+constexpr int bwd_bytes()
 {
-    return PER / 8 * (words<TX>() * (RES ? 2 : 1) + words<TY>());
+    return PER * ((int)sizeof(typename TX::type) * (RES ? 2 : 1) + (int)sizeof(typename TY::type));
 }
 
 // The normalised values and w dy are formed twice from what was read (before
@@ -529,12 +560,13 @@ constexpr int bwd_words()
 template <class TX, class TY, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const BwdArgs a, int G)
 {
-    constexpr int NV = PER / VEC, WORDS = bwd_words<TX, TY, PER, RES>(), STAGES = stages_for(WORDS);
-    constexpr int G0 = NV * words<TX>(), Q0 = G0 + NV * words<TY>();  // first words of dy and dres
+    constexpr int NV = PER / VEC, BYTES = bwd_bytes<TX, TY, PER, RES>(), STAGES = stages_for(BYTES);
+    constexpr int SX = piece_bytes<TX, VEC>(), SY = piece_bytes<TY, VEC>();
+    constexpr int G0 = NV * SX, Q0 = G0 + NV * SY;  // offsets of dy and dres
     extern __shared__ uint4 dyn[];
     __shared__ float2 buf[32];
     RowSum rs(buf, G);
-    Ring<STAGES, WORDS> ring(dyn);
+    Ring<STAGES, BYTES> ring(dyn);
     const int t = threadIdx.x % G, groups = blockDim.x / G;
     const float inv_d = 1.f / (float)a.d;
     float w[PER], dw[PER], db[PER];
@@ -554,15 +586,15 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
     const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
     const typename TY::type* ag = row_of<TY>(a.dy, r, a.lddy) + t * VEC;
     const typename TX::type* aq = RES ? row_of<TX>(a.dres, r, a.lddres) + t * VEC : nullptr;
-    auto request = [&](int st) {
-        if constexpr (VEC == 8) {
+    auto request = [&] {
+        if constexpr (VEC > 1) {
             if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
-                    if ((v * G + t) * 8 < a.d) {
-                        to_ring<TX>(ring, st, v * words<TX>(), ax + v * G * 8);
-                        to_ring<TY>(ring, st, G0 + v * words<TY>(), ag + v * G * 8);
-                        if (RES) to_ring<TX>(ring, st, Q0 + v * words<TX>(), aq + v * G * 8);
+                    if ((v * G + t) * VEC < a.d) {
+                        ring.template ask<TX, VEC>(v * SX, ax + v * G * VEC);
+                        ring.template ask<TY, VEC>(G0 + v * SY, ag + v * G * VEC);
+                        if (RES) ring.template ask<TX, VEC>(Q0 + v * SX, aq + v * G * VEC);
                     }
                 }
             }
@@ -574,8 +606,10 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         }
     };
 #pragma unroll
-    for (int st = 0; st < STAGES; ++st) request(st);
-    int st = 0;
+    for (int i = 0; i < STAGES; ++i) {
+        request();
+        ring.turn();
+    }
     float next_mean = r < a.N ? a.mean[r] : 0.f, next_rstd = r < a.N ? a.rstd[r] : 0.f;
     for (; r < a.N; r += step) {
         const float mean = next_mean, rstd = next_rstd;
@@ -585,7 +619,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         }
         Piece<TX, VEC> x[NV];
         Piece<TY, VEC> g[NV];
-        if (VEC == 8) copies_wait<STAGES - 1>();
+        if (VEC > 1) copies_wait<STAGES - 1>();
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -594,9 +628,9 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             x[v].zero();
             g[v].zero();
             if (in) {
-                if constexpr (VEC == 8) {
-                    from_ring<TX>(ring, st, v * words<TX>(), x[v]);
-                    from_ring<TY>(ring, st, G0 + v * words<TY>(), g[v]);
+                if constexpr (VEC > 1) {
+                    ring.get(v * SX, x[v]);
+                    ring.get(G0 + v * SY, g[v]);
                 } else {
                     x[v].load(row_of<TX>(a.x, r, a.ldx) + i);
                     g[v].load(row_of<TY>(a.dy, r, a.lddy) + i);
@@ -622,8 +656,8 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             if (i >= a.d) continue;
             Piece<TX, VEC> q;
             if constexpr (RES) {
-                if constexpr (VEC == 8)
-                    from_ring<TX>(ring, st, Q0 + v * words<TX>(), q);
+                if constexpr (VEC > 1)
+                    ring.get(Q0 + v * SX, q);
                 else
                     q.load(row_of<TX>(a.dres, r, a.lddres) + i);
             }
@@ -637,10 +671,10 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             q.set(f);
             q.store(row_of<TX>(a.dx, r, a.lddx) + i);
         }
-        request(st);
-        st = st + 1 == STAGES ? 0 : st + 1;
+        request();
+        ring.turn();
     }
-    if (VEC == 8) copies_wait<0>();
+    if (VEC > 1) copies_wait<0>();
     if (!a.part) return;
     float* part = a.part + (size_t)blockIdx.x * 2 * a.d;
     if (groups == 1) {
@@ -738,9 +772,10 @@ cudaError_t launch_rows(void (*kern)(Args, int), const Args& a, int G, unsigned 
 template <class TX, class TY, int PER, bool RES>
 cudaError_t launch_fwd(const FwdArgs& a, int G, bool vec, unsigned blocks, unsigned threads, cudaStream_t s)
 {
-    constexpr int W = fwd_words<TX, PER, RES>();
+    constexpr int B = fwd_bytes<TX, PER, RES>();
     if (!vec) return launch_rows(k_ln_fwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, 0, s);
-    return launch_rows(k_ln_fwd<TX, TY, 8, PER, RES>, a, G, blocks, threads, Ring<stages_for(W), W>::bytes(threads), s);
+    return launch_rows(k_ln_fwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, blocks, threads,
+                       Ring<stages_for(B), B>::bytes(threads), s);
 }
 
 template <class TX, class TY>
@@ -765,12 +800,12 @@ cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t s)
 template <class TX, class TY, int PER, bool RES>
 cudaError_t launch_bwd(const BwdArgs& a, int G, bool vec, unsigned threads, cudaStream_t s)
 {
-    constexpr int W = bwd_words<TX, TY, PER, RES>();
+    constexpr int B = bwd_bytes<TX, TY, PER, RES>();
     // the block's column sums, when it holds several rows at a time (over the ring where there is one)
     const size_t sums = G < 256 ? (size_t)2 * a.d * sizeof(float) : 0;
     if (!vec) return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, sums, s);
-    const size_t ring = Ring<stages_for(W), W>::bytes(threads);
-    return launch_rows(k_ln_bwd<TX, TY, 8, PER, RES>, a, G, a.parts, threads, ring > sums ? ring : sums, s);
+    const size_t ring = Ring<stages_for(B), B>::bytes(threads);
+    return launch_rows(k_ln_bwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, a.parts, threads, ring > sums ? ring : sums, s);
 }
 
 template <class TX, class TY>
