@@ -307,68 +307,65 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Codes to bf16 dz in place: dz = 2^(m2 - q / 2048 - lse2). The target's entry is
-// p - 1 = expm1(-nll), which stays exact where p is close to 1. A row without a
-// finite lse is NaN throughout. Bound by memory (4 bytes a logit); a block takes
-// kDzSpan columns of one row, two 16-byte pieces a thread, all asked for at once.
-constexpr int kDzPieces = 2, kDzSpan = 256 * 8 * kDzPieces;
-
-__global__ void __launch_bounds__(256)
-    k_xent_dz(XentWs w, size_t ldcode, int tiles, const int32_t* __restrict__ targets,
+// Codes to bf16 dz in place, one warp per (row, 256 words), eight words a lane:
+// dz = 2^(m2 - q / 2048 - lse2). The target's entry is p - 1 = expm1(-nll), which
+// stays exact where p is close to 1. A row without a finite lse is NaN throughout.
+// Bound by memory (4 bytes a logit). A code becomes a float as the low mantissa
+// bits of 2^23 + code: an integer conversion shares the special-function unit with
+// the exponential. Few registers and many warps do better than several pieces a
+// thread (777 x 50001: 26 against 37 us with two; 8192 x 65536: 335 against 465).
+__global__ void __launch_bounds__(256, 8)
+    k_xent_dz(XentWs w, unsigned ldcode, int tiles, const int32_t* __restrict__ targets,
               const int32_t* __restrict__ rows_dev, int max_rows, const int32_t* status)
 {
     if (has_error(status)) return;
+    const int lane = threadIdx.x & 31;
     const int rows = *rows_dev;
     const int padded = min(max_rows, max((rows + 63) / 64 * 64, 64));  // zeros up to the depth dW reads
-    const int spans = (int)((ldcode + kDzSpan - 1) / kDzSpan);
-    for (long long i = blockIdx.x; i < (long long)padded * spans; i += gridDim.x) {
-        const int row = (int)(i / spans);
-        const long long c0 = (i % spans) * kDzSpan + threadIdx.x * 8;
-        uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + c0);
-        if (row >= rows) {
-#pragma unroll
-            for (int k = 0; k < kDzPieces; ++k)
-                if (c0 + k * 2048 < (long long)ldcode) p[k * 256] = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        uint4 q[kDzPieces];
-        float m2[kDzPieces];
-#pragma unroll
-        for (int k = 0; k < kDzPieces; ++k) {
-            const long long c = c0 + k * 2048;
-            if (c < (long long)ldcode) {
-                q[k] = p[k * 256];
+    const unsigned spans = (ldcode + 255) / 256;
+    const unsigned step = gridDim.x * 8;
+    // (row, span) of this warp, advanced by `step` spans at a time
+    unsigned i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    unsigned row = i / spans, span = i % spans;
+    const unsigned rows_step = step / spans, span_step = step % spans;
+    for (; row < (unsigned)padded;) {
+        const unsigned col = span * 256 + lane * 8;
+        if (col < ldcode) {
+            uint4* p = reinterpret_cast<uint4*>(w.codes + (size_t)row * ldcode + col);
+            if (row >= (unsigned)rows) {
+                *p = make_uint4(0, 0, 0, 0);
+            } else {
+                const uint4 q = *p;
+                const float l2 = w.lse2[row];
                 // (the padding past the last word has no tile of its own)
-                m2[k] = w.stat[(size_t)row * tiles + min((int)(c / kXentTile), tiles - 1)].x;
+                const float m2 = w.stat[(size_t)row * tiles + min((int)(col / kXentTile), tiles - 1)].x;
+                const int target = targets[row] - (int)col;
+                const float shift = m2 - l2;
+                const float one = isfinite(l2) ? 1.f : NAN;
+                const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v =
+                        __uint_as_float(__byte_perm(qw[e >> 1], 0x4b00u, (e & 1) ? 0x5432 : 0x5410)) - 8388608.f;
+                    f[e] = v == (float)kXentZero ? 0.f : exp2_approx(fmaf(v, -1.f / kXentSteps, shift));
+                    f[e] *= one;
+                }
+                if (target >= 0 && target < 8) {
+                    const float ft = one * expm1f(-w.nll[row]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e == target) f[e] = ft;
+                }
+                *p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                pack_bf16x2(f[6], f[7]));
             }
         }
-        const float l2 = w.lse2[row];
-        const float one = isfinite(l2) ? 1.f : NAN;
-        const int target = targets[row];
-#pragma unroll
-        for (int k = 0; k < kDzPieces; ++k) {
-            const long long c = c0 + k * 2048;
-            if (c >= (long long)ldcode) break;
-            const float shift = m2[k] - l2;
-            const uint32_t qw[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                // the code as the low mantissa bits of 2^23 + code: an integer conversion shares
-                // the special-function unit with the exponential (8192 x 4096 x 65536: 373 us with it, 290 without)
-                const float v = __uint_as_float(__byte_perm(qw[e >> 1], 0x4b00u, (e & 1) ? 0x5432 : 0x5410)) - 8388608.f;
-                f[e] = v == (float)kXentZero ? 0.f : exp2_approx(fmaf(v, -1.f / kXentSteps, shift));
-                f[e] *= one;
-            }
-            const long long t = target - c;
-            if (t >= 0 && t < 8) {
-                const float ft = one * expm1f(-w.nll[row]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e == (int)t) f[e] = ft;
-            }
-            p[k * 256] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                    pack_bf16x2(f[6], f[7]));
+        row += rows_step;
+        span += span_step;
+        if (span >= spans) {
+            span -= spans;
+            ++row;
         }
     }
 }
@@ -442,8 +439,8 @@ cudaError_t chunk_grads(const XentWs& w, const uint16_t* W, int r0, int c, int r
     const int tiles = (V + kXentTile - 1) / kXentTile;
     const size_t ldcode = row_stride(V);
     count_launches(1);
-    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + kDzSpan - 1) / kDzSpan), 1, sms), 256, 0, s>>>(
-        w, ldcode, tiles, w.target + r0, w.rows_dev + c, rows, status);
+    k_xent_dz<<<blocks_for((size_t)rows * ((ldcode + 255) / 256), 8, sms), 256, 0, s>>>(
+        w, (unsigned)ldcode, tiles, w.target + r0, w.rows_dev + c, rows, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
 

@@ -128,7 +128,7 @@ class Model:
             raise RuntimeError(f"device status {code}: {tw.twell_status_string(code)}")
 
 
-def train(steps: int = 600, M: int = 4096, d: int = 256, F: int = 1024, vocab: int = 2000, T: int = 128, lam: float = 0.02,
+def train(steps: int = 600, M: int = 4096, d: int = 256, F: int = 1024, vocab: int = 2000, T: int = 128, lam: float = 0.001,
           lr: float = 3e-3, max_norm: float = 1.0, seed: int = 0, log_every: int = 100, verbose: bool = True):
     """Runs the demo; returns the per-log history (training and held-out loss, gradient norm, hidden density, ms)."""
     g = torch.Generator(device="cuda").manual_seed(seed)
@@ -171,7 +171,7 @@ def main(argv=None):
     ap.add_argument("--d", type=int, default=256)
     ap.add_argument("--F", type=int, default=1024)
     ap.add_argument("--vocab", type=int, default=2000)
-    ap.add_argument("--lam", type=float, default=0.02)
+    ap.add_argument("--lam", type=float, default=0.001)
     ap.add_argument("--lr", type=float, default=3e-3)
     ap.add_argument("--max-norm", type=float, default=1.0)
     args = ap.parse_args(argv)
