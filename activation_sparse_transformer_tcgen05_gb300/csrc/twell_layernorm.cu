@@ -190,10 +190,11 @@ __global__ void __launch_bounds__(1024)
 //
 // A row is held by G threads (a warp to 512 threads, 8 or 16 elements each), so
 // that it is read from memory once. Blocks stay and walk over the rows: w, b and
-// the column sums live in registers. Where rows are aligned, each thread copies
-// its 16-byte pieces of the next rows asynchronously into shared memory, where
-// only it reads them: bytes in flight without registers and without barriers.
-// Other rows are read element by element when their turn comes. The mean is
+// the column sums live in registers. Each thread copies its pieces of the next
+// rows (16 bytes where the rows' addresses allow it, else two elements, else one)
+// asynchronously into shared memory, where only it reads them: bytes in flight
+// without registers and without barriers. Odd rows of bf16, whose single elements
+// such copies do not move, are read when their turn comes. The mean is
 // summed first and the variance from the centred values, which holds for rows
 // whose mean is far larger than their deviation.
 
@@ -226,12 +227,13 @@ struct Piece<bf16_t, VEC> {
 };
 template <>
 struct Piece<bf16_t, 1> {
-    uint16_t v;
+    // a whole register: two halves packed into one would wait for both loads at once
+    uint32_t v;
     __device__ __forceinline__ void load(const uint16_t* p) { v = *p; }
     __device__ __forceinline__ void zero() { v = 0; }
-    __device__ __forceinline__ float get(int) const { return bf16_to_f32(v); }
+    __device__ __forceinline__ float get(int) const { return bf16_lo(v); }
     __device__ __forceinline__ void set(const float* f) { v = f32_to_bf16_bits(f[0]); }
-    __device__ __forceinline__ void store(uint16_t* p) const { *p = v; }
+    __device__ __forceinline__ void store(uint16_t* p) const { *p = (uint16_t)v; }
 };
 template <>
 struct Piece<bf16_t, 4> {
@@ -248,6 +250,24 @@ struct Piece<bf16_t, 4> {
         v = make_uint2(Piece<bf16_t, 8>::pair(f[0], f[1]), Piece<bf16_t, 8>::pair(f[2], f[3]));
     }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = v; }
+};
+template <>
+struct Piece<bf16_t, 2> {
+    uint32_t v;
+    __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void zero() { v = 0; }
+    __device__ __forceinline__ float get(int i) const { return i ? bf16_hi(v) : bf16_lo(v); }
+    __device__ __forceinline__ void set(const float* f) { v = Piece<bf16_t, 8>::pair(f[0], f[1]); }
+    __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint32_t*>(p) = v; }
+};
+template <>
+struct Piece<f32_t, 2> {
+    float2 v;
+    __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const float2*>(p); }
+    __device__ __forceinline__ void zero() { v = make_float2(0.f, 0.f); }
+    __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
+    __device__ __forceinline__ void set(const float* f) { v = make_float2(f[0], f[1]); }
+    __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float2*>(p) = v; }
 };
 template <>
 struct Piece<f32_t, 4> {
@@ -364,7 +384,8 @@ __device__ __forceinline__ void copy_async(void* smem, const void* global)
     if constexpr (BYTES == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(smem)), "l"(global) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(smem)), "l"(global), "n"(BYTES)
+                     : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -380,6 +401,13 @@ template <class TX, class TY>
 constexpr int vec_of()
 {
     return sizeof(typename TX::type) + sizeof(typename TY::type) == 4 ? 8 : 4;
+}
+
+// Whether rows come through the ring: its copies move at least 4 bytes.
+template <class TX, class TY, int VEC>
+constexpr bool ringed()
+{
+    return VEC > 1 || sizeof(typename TX::type) + sizeof(typename TY::type) == 8;
 }
 
 template <class T, int VEC>
@@ -439,6 +467,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
 {
     constexpr int NV = PER / VEC, BYTES = fwd_bytes<TX, PER, RES>(), STAGES = stages_for(BYTES);
     constexpr int SX = piece_bytes<TX, VEC>();
+    constexpr bool RING = ringed<TX, TY, VEC>();
     extern __shared__ uint4 dyn[];
     __shared__ float2 buf[32];
     RowSum rs(buf, G);
@@ -464,7 +493,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
     const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
     const typename TX::type* aq = RES ? row_of<TX>(a.res, r, a.ldres) + t * VEC : nullptr;
     auto request = [&] {
-        if constexpr (VEC > 1) {
+        if constexpr (RING) {
             if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
@@ -488,27 +517,33 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
     for (; r < a.N; r += step) {
         float f[PER];
         float s = 0.f;
-        if (VEC > 1) copies_wait<STAGES - 1>();
+        if (RING) copies_wait<STAGES - 1>();
+        // all of the row is asked for before any of it is used, at an address that is
+        // always there (a load under a branch waits for the one before it)
+        Piece<TX, VEC> xs[NV], qs[RES ? NV : 1];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int i = (v * G + t) * VEC;
-            Piece<TX, VEC> x, q;
-            x.zero();
-            q.zero();
-            if (i < a.d) {
-                if constexpr (VEC > 1) {
-                    ring.get(v * SX, x);
-                    if (RES) ring.get((NV + v) * SX, q);
-                } else {
-                    x.load(row_of<TX>(a.x, r, a.ldx) + i);
-                    if (RES) q.load(row_of<TX>(a.res, r, a.ldres) + i);
-                }
+            const bool in = i < a.d;
+            if constexpr (RING) {
+                ring.get(v * SX, xs[v]);
+                if (RES) ring.get((NV + v) * SX, qs[v]);
+            } else {
+                xs[v].load(row_of<TX>(a.x, r, a.ldx) + (in ? i : 0));
+                if (RES) qs[v].load(row_of<TX>(a.res, r, a.ldres) + (in ? i : 0));
             }
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int i = (v * G + t) * VEC;
+            Piece<TX, VEC> x = xs[v];
+            if (i >= a.d) x.zero();
 #pragma unroll
             for (int e = 0; e < VEC; ++e) f[v * VEC + e] = x.get(e);
             if (RES) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) f[v * VEC + e] += q.get(e);
+                for (int e = 0; e < VEC; ++e)
+                    if (i < a.d) f[v * VEC + e] += qs[v].get(e);
                 x.set(f + v * VEC);
                 if (i < a.d) x.store(row_of<TX>(a.sum, r, a.ldsum) + i);
 #pragma unroll
@@ -546,13 +581,29 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const 
             if (a.rstd) a.rstd[r] = rstd;
         }
     }
-    if (VEC > 1) copies_wait<0>();
+    if (RING) copies_wait<0>();
 }
 
 template <class TX, class TY, int PER, bool RES>
 constexpr int bwd_bytes()
 {
     return PER * ((int)sizeof(typename TX::type) * (RES ? 2 : 1) + (int)sizeof(typename TY::type));
+}
+
+// VEC column sums (d is a multiple of VEC; element by element these stores took 6 us
+// of a backward over 300 x 4096).
+template <int VEC>
+__device__ __forceinline__ void store_sums(float* p, const float* s)
+{
+    if constexpr (VEC == 1) {
+        *p = s[0];
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<float2*>(p) = make_float2(s[0], s[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+            *reinterpret_cast<float4*>(p + e) = make_float4(s[e], s[e + 1], s[e + 2], s[e + 3]);
+    }
 }
 
 // The normalised values and w dy are formed twice from what was read (before
@@ -562,6 +613,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
 {
     constexpr int NV = PER / VEC, BYTES = bwd_bytes<TX, TY, PER, RES>(), STAGES = stages_for(BYTES);
     constexpr int SX = piece_bytes<TX, VEC>(), SY = piece_bytes<TY, VEC>();
+    constexpr bool RING = ringed<TX, TY, VEC>();
     constexpr int G0 = NV * SX, Q0 = G0 + NV * SY;  // offsets of dy and dres
     extern __shared__ uint4 dyn[];
     __shared__ float2 buf[32];
@@ -587,7 +639,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
     const typename TY::type* ag = row_of<TY>(a.dy, r, a.lddy) + t * VEC;
     const typename TX::type* aq = RES ? row_of<TX>(a.dres, r, a.lddres) + t * VEC : nullptr;
     auto request = [&] {
-        if constexpr (VEC > 1) {
+        if constexpr (RING) {
             if (asked < a.N) {
 #pragma unroll
                 for (int v = 0; v < NV; ++v) {
@@ -617,30 +669,31 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             next_mean = a.mean[r + step];
             next_rstd = a.rstd[r + step];
         }
-        Piece<TX, VEC> x[NV];
+        Piece<TX, VEC> x[NV], add[RES && !RING ? NV : 1];
         Piece<TY, VEC> g[NV];
-        if (VEC > 1) copies_wait<STAGES - 1>();
-        float s1 = 0.f, s2 = 0.f;
+        if (RING) copies_wait<STAGES - 1>();
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int i = (v * G + t) * VEC;
-            const bool in = i < a.d;
-            x[v].zero();
-            g[v].zero();
-            if (in) {
-                if constexpr (VEC > 1) {
-                    ring.get(v * SX, x[v]);
-                    ring.get(G0 + v * SY, g[v]);
-                } else {
-                    x[v].load(row_of<TX>(a.x, r, a.ldx) + i);
-                    g[v].load(row_of<TY>(a.dy, r, a.lddy) + i);
-                }
+            if constexpr (RING) {
+                ring.get(v * SX, x[v]);
+                ring.get(G0 + v * SY, g[v]);
+            } else {
+                const int at = i < a.d ? i : 0;
+                x[v].load(row_of<TX>(a.x, r, a.ldx) + at);
+                g[v].load(row_of<TY>(a.dy, r, a.lddy) + at);
+                if constexpr (RES) add[v].load(row_of<TX>(a.dres, r, a.lddres) + at);
             }
+        }
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            if ((v * G + t) * VEC >= a.d) g[v].zero();  // beyond the row
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int k = v * VEC + e;
                 const float dy = g[v].get(e);
-                const float hat = in ? (x[v].get(e) - mean) * rstd : 0.f;
+                const float hat = (v * G + t) * VEC < a.d ? (x[v].get(e) - mean) * rstd : 0.f;
                 dw[k] = fmaf(dy, hat, dw[k]);
                 db[k] += dy;
                 const float dv = dy * w[k];
@@ -656,10 +709,10 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
             if (i >= a.d) continue;
             Piece<TX, VEC> q;
             if constexpr (RES) {
-                if constexpr (VEC > 1)
+                if constexpr (RING)
                     ring.get(Q0 + v * SX, q);
                 else
-                    q.load(row_of<TX>(a.dres, r, a.lddres) + i);
+                    q = add[v];
             }
             float f[VEC];
 #pragma unroll
@@ -674,7 +727,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         request();
         ring.turn();
     }
-    if (VEC > 1) copies_wait<0>();
+    if (RING) copies_wait<0>();
     if (!a.part) return;
     float* part = a.part + (size_t)blockIdx.x * 2 * a.d;
     if (groups == 1) {
@@ -682,11 +735,8 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         for (int v = 0; v < NV; ++v) {
             const int i = (v * G + t) * VEC;
             if (i < a.d) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    part[i + e] = dw[v * VEC + e];
-                    part[a.d + i + e] = db[v * VEC + e];
-                }
+                store_sums<VEC>(part + i, dw + v * VEC);
+                store_sums<VEC>(part + a.d + i, db + v * VEC);
             }
         }
         return;
@@ -749,11 +799,13 @@ bool elem_aligned(const void* p, int type)
     return (reinterpret_cast<uintptr_t>(p) & (type == TWELL_F32 ? 3u : 1u)) == 0;
 }
 
-// 16-byte pieces: every row of p starts on a 16-byte boundary.
-bool vec_rows(const void* p, int64_t ld, int64_t N, int type)
+// Elements of a piece every row of p allows (by its address and stride), at most `most`: most, 2 or 1.
+int pieces(const void* p, int64_t ld, int64_t N, int type, int most)
 {
     const int64_t size = type == TWELL_F32 ? 4 : 2;
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (N <= 1 || ld * size % 16 == 0);
+    for (int v = most; v > 1; v = v > 2 ? 2 : 1)
+        if (reinterpret_cast<uintptr_t>(p) % (v * size) == 0 && (N <= 1 || ld % v == 0)) return v;
+    return 1;
 }
 
 // Launches a kernel that may want more than 48 KB of shared memory (its static part included).
@@ -770,16 +822,18 @@ cudaError_t launch_rows(void (*kern)(Args, int), const Args& a, int G, unsigned 
 }
 
 template <class TX, class TY, int PER, bool RES>
-cudaError_t launch_fwd(const FwdArgs& a, int G, bool vec, unsigned blocks, unsigned threads, cudaStream_t s)
+cudaError_t launch_fwd(const FwdArgs& a, int G, int vec, unsigned blocks, unsigned threads, cudaStream_t s)
 {
     constexpr int B = fwd_bytes<TX, PER, RES>();
-    if (!vec) return launch_rows(k_ln_fwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, 0, s);
-    return launch_rows(k_ln_fwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, blocks, threads,
-                       Ring<stages_for(B), B>::bytes(threads), s);
+    const size_t ring = Ring<stages_for(B), B>::bytes(threads);
+    if (vec == 1)
+        return launch_rows(k_ln_fwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, ringed<TX, TY, 1>() ? ring : 0, s);
+    if (vec == 2) return launch_rows(k_ln_fwd<TX, TY, 2, PER, RES>, a, G, blocks, threads, ring, s);
+    return launch_rows(k_ln_fwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, blocks, threads, ring, s);
 }
 
 template <class TX, class TY>
-cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t s)
+cudaError_t fwd(const FwdArgs& a, int vec, cudaStream_t s)
 {
     const int G = group_of(a.d);
     count_launches(1);
@@ -798,18 +852,20 @@ cudaError_t fwd(const FwdArgs& a, bool vec, cudaStream_t s)
 }
 
 template <class TX, class TY, int PER, bool RES>
-cudaError_t launch_bwd(const BwdArgs& a, int G, bool vec, unsigned threads, cudaStream_t s)
+cudaError_t launch_bwd(const BwdArgs& a, int G, int vec, unsigned threads, cudaStream_t s)
 {
     constexpr int B = bwd_bytes<TX, TY, PER, RES>();
     // the block's column sums, when it holds several rows at a time (over the ring where there is one)
     const size_t sums = G < 256 ? (size_t)2 * a.d * sizeof(float) : 0;
-    if (!vec) return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, sums, s);
-    const size_t ring = Ring<stages_for(B), B>::bytes(threads);
-    return launch_rows(k_ln_bwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, a.parts, threads, ring > sums ? ring : sums, s);
+    const size_t ring = Ring<stages_for(B), B>::bytes(threads), both = ring > sums ? ring : sums;
+    if (vec == 1)
+        return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, ringed<TX, TY, 1>() ? both : sums, s);
+    if (vec == 2) return launch_rows(k_ln_bwd<TX, TY, 2, PER, RES>, a, G, a.parts, threads, both, s);
+    return launch_rows(k_ln_bwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, a.parts, threads, both, s);
 }
 
 template <class TX, class TY>
-cudaError_t bwd(const BwdArgs& a, bool vec, float* dw, float* db, cudaStream_t s)
+cudaError_t bwd(const BwdArgs& a, int vec, float* dw, float* db, cudaStream_t s)
 {
     const int G = group_of(a.d);
     cudaError_t e;
@@ -864,9 +920,14 @@ extern "C" twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const vo
         !elem_aligned(y, y_type) || !elem_aligned(w, w_type) || !elem_aligned(b, w_type) ||
         !elem_aligned(mean, TWELL_F32) || !elem_aligned(rstd, TWELL_F32))
         return TWELL_ERR_INVALID_ARG;
-    const bool vec = d % 8 == 0 && vec_rows(x, ldx, N, x_type) && vec_rows(res, ldres, N, x_type) &&
-                     vec_rows(sum, ldsum, N, x_type) && vec_rows(y, ldy, N, y_type) && vec_rows(w, 0, 1, w_type) &&
-                     vec_rows(b, 0, 1, w_type);
+    int vec = x_type == TWELL_BF16 && y_type == TWELL_BF16 ? 8 : 4;
+    while (vec > 1 && d % vec) vec = vec > 2 ? 2 : 1;
+    vec = pieces(x, ldx, N, x_type, vec);
+    vec = pieces(res, ldres, N, x_type, vec);
+    vec = pieces(sum, ldsum, N, x_type, vec);
+    vec = pieces(y, ldy, N, y_type, vec);
+    vec = pieces(w, 0, 1, w_type, vec);
+    vec = pieces(b, 0, 1, w_type, vec);
     const FwdArgs a{x, res, w, b, sum, y, ldx, ldres, ldsum, ldy, N, d, eps, mean, rstd,
                     w_type == TWELL_F32};
     const cudaError_t e = by_types(x_type, y_type, [&](auto tx, auto ty) {
@@ -907,8 +968,13 @@ extern "C" twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const 
         return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_layernorm_bwd_workspace_bytes(N, d)) return TWELL_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return TWELL_ERR_INVALID_ARG;
-    const bool vec = d % 8 == 0 && vec_rows(dy, lddy, N, y_type) && vec_rows(x, ldx, N, x_type) &&
-                     vec_rows(dres, lddres, N, x_type) && vec_rows(dx, lddx, N, x_type) && vec_rows(w, 0, 1, w_type);
+    int vec = x_type == TWELL_BF16 && y_type == TWELL_BF16 ? 8 : 4;
+    while (vec > 1 && d % vec) vec = vec > 2 ? 2 : 1;
+    vec = pieces(dy, lddy, N, y_type, vec);
+    vec = pieces(x, ldx, N, x_type, vec);
+    vec = pieces(dres, lddres, N, x_type, vec);
+    vec = pieces(dx, lddx, N, x_type, vec);
+    vec = pieces(w, 0, 1, w_type, vec);
     const BwdArgs a{dy, x, w, dres, dx, lddy, ldx, lddres, lddx, N, d, mean, rstd,
                     dw ? static_cast<float*>(ws) : nullptr, parts_for(N, d), w_type == TWELL_F32};
     const cudaError_t e = by_types(x_type, y_type, [&](auto tx, auto ty) {
