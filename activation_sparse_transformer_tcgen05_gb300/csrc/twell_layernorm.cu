@@ -741,26 +741,25 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         }
         return;
     }
-    // several rows at a time in the block: their sums added in order, over the ring
+    // several rows at a time in the block: the groups' sums side by side (over the
+    // ring), then added in order
     float* sums = reinterpret_cast<float*>(dyn);
+    float* mine = sums + (int)threadIdx.x / G * 2 * a.d;
     __syncthreads();
-    for (int k = 0; k < groups; ++k) {
-        if ((int)threadIdx.x / G == k) {
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int i = (v * G + t) * VEC;
-                if (i < a.d) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        sums[i + e] = (k ? sums[i + e] : 0.f) + dw[v * VEC + e];
-                        sums[a.d + i + e] = (k ? sums[a.d + i + e] : 0.f) + db[v * VEC + e];
-                    }
-                }
-            }
+    for (int v = 0; v < NV; ++v) {
+        const int i = (v * G + t) * VEC;
+        if (i < a.d) {
+            store_sums<VEC>(mine + i, dw + v * VEC);
+            store_sums<VEC>(mine + a.d + i, db + v * VEC);
         }
-        __syncthreads();
     }
-    for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) part[i] = sums[i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.d; i += blockDim.x) {
+        float s = sums[i];
+        for (int k = 1; k < groups; ++k) s += sums[k * 2 * a.d + i];
+        part[i] = s;
+    }
 }
 
 // Elements of a row per thread. What a warp does once a row (sums over lanes and
@@ -855,8 +854,8 @@ template <class TX, class TY, int PER, bool RES>
 cudaError_t launch_bwd(const BwdArgs& a, int G, int vec, unsigned threads, cudaStream_t s)
 {
     constexpr int B = bwd_bytes<TX, TY, PER, RES>();
-    // the block's column sums, when it holds several rows at a time (over the ring where there is one)
-    const size_t sums = G < 256 ? (size_t)2 * a.d * sizeof(float) : 0;
+    // the groups' column sums, when a block holds several rows at a time (over the ring where there is one)
+    const size_t sums = G < 256 ? (size_t)rows_per_block(G) * 2 * a.d * sizeof(float) : 0;
     const size_t ring = Ring<stages_for(B), B>::bytes(threads), both = ring > sums ? ring : sums;
     if (vec == 1)
         return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, ringed<TX, TY, 1>() ? both : sums, s);
