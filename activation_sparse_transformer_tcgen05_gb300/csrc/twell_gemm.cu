@@ -269,7 +269,7 @@ struct Outbox {
 
 // Cross-entropy epilogue of one accumulator row (one thread) and 128 columns
 // (words). Two readings of the accumulator: the maximum m, then, with
-// m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0, the sum of 2^t and the
+// m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0 (log2(e) times z_scale), the sum of 2^t and the
 // code round(-2048 t). A logit is kept as its distance to the maximum on a
 // logarithmic scale, in steps of 2^-11: the exponential rebuilt from a code is off
 // by at most 2^(2^-12) - 1 = 1.7e-4, a twentieth of its later rounding to bf16 (up
@@ -293,7 +293,8 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
             if (FULL || ch * 32 + c < ncols) m = fmaxf(m, __uint_as_float(v[c]));
     }
     // no finite logit in the tile: the sum is 0 and every code the zero code
-    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kLog2e);
+    const float unit = kLog2e * a.z_scale;
+    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, unit);
     const float magic = 8388608.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile;
@@ -304,7 +305,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
         tmem_ld32_wait(tbase + ch * 32, v);
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-            float t = fmaf(__uint_as_float(v[c]), kLog2e, -m2);
+            float t = fmaf(__uint_as_float(v[c]), unit, -m2);
             if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
             sum[c & 3] += exp2_approx(t);
             v[c] = __float_as_uint(fminf(fmaf(t, -kXentSteps, magic), magic + (float)kXentZero));
@@ -959,7 +960,7 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                             const int l = __ffs(lanes) - 1;
                             lanes &= lanes - 1;
                             const uint32_t z = tmem_ld1_wait(tb + (uint32_t)__shfl_sync(0xffffffffu, tc, l));
-                            if (lane == l) a.ztarget[row] = __uint_as_float(z);
+                            if (lane == l) a.ztarget[row] = __uint_as_float(z) * a.z_scale;
                         }
                         const int ncols = min(kXentTile, a.rowsB - col0);
                         if (ncols == kXentTile)
