@@ -4,6 +4,15 @@
 //   forward   s = x + res, hat = (s - mean) rstd, y = hat w + b
 //   backward  v = w dy, dx = rstd (v - mean(v) - hat mean(v hat)) + dres,
 //             dw = sum_r dy hat, db = sum_r dy
+//
+// Bound by memory: every element read once and written once (forward: x, res in,
+// sum, y out; backward: x, dy, dres in, dx out). 16384 x 4096 bf16 with residual, 537
+// MB either way, 79 us at the measured copy rate: forward 88 us, backward 87 us (6 us of it the column sums).
+//
+//   k_ln_fwd       rows up to 8192 elements, held by their threads
+//   k_ln_bwd       the same: dx, and partial dw, db of each block
+//   k_ln_reduce    the blocks' partial sums added in order
+//   k_ln_fwd_long, k_ln_bwd_long, k_ln_cols_long   longer rows, read several times
 #include "common.cuh"
 #include "launch.h"
 
