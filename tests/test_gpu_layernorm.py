@@ -310,3 +310,25 @@ def test_wrong_arguments_are_refused():
                                torch.empty(64, device="cuda"), ws)
     assert e.value.status == 3
     assert np.isfinite(float(w.sum()))
+
+
+@pytest.mark.parametrize("N,d", [(9, 2), (50, 1002), (700, 130), (33, 4094), (5, 8190), (3000, 34)])
+@pytest.mark.parametrize("types", [(BF, BF, F32), (F32, BF, BF), (F32, F32, F32), (BF, F32, F32)])
+@pytest.mark.parametrize("res", [False, True])
+def test_even_widths(N, d, types, res):
+    """Rows of an even number of elements that is no multiple of 4 start on a pair's boundary only."""
+    tx, ty, tp = types
+    x, r = _rand((N, d), tx, 1, 2.0, 0.3), _rand((N, d), tx, 2) if res else None
+    w, b = _rand((d,), tp, 3, 0.2, 1.0), _rand((d,), tp, 4, 0.3)
+    _, s, mean, rstd = _check_fwd(x, r, w, b, ty)
+    _check_bwd(_rand((N, d), ty, 5), x if s is None else s, w, _rand((N, d), tx, 6) if res else None, mean, rstd)
+
+
+@pytest.mark.parametrize("N", [1, 2, 151, 152, 153, 303, 304, 305, 608, 609, 1216, 1217, 3000])
+def test_rows_around_a_full_gpu(N):
+    """Fewer rows than resident blocks, exactly as many, one more: groups with no row, one row, several."""
+    for d in (24, 512, 1001):
+        x = _rand((N, d), BF, 1, 2.0, 0.3)
+        w = _rand((d,), F32, 3, 0.2, 1.0)
+        _, _, mean, rstd = _check_fwd(x, None, w, None, BF)
+        _check_bwd(_rand((N, d), BF, 5), x, w, None, mean, rstd)

@@ -155,6 +155,36 @@ def test_sum_scale_and_accumulation(chunk):
     _check(x, W, t, out, mean=False, grad_scale=0.125, dW0=dW0)
 
 
+@pytest.mark.parametrize("N", [2047, 2048, 2049, 5000])
+@pytest.mark.parametrize("chunk", [0, 700])
+def test_many_rows(N, chunk):
+    x, W, t = _inputs(N, 72, 333, seed=13, ignored=0.4)
+    _check(x, W, t, _run(x, W, t, chunk=chunk, dw_dtype=F32))
+    _check(x, W, t, _run(x, W, t, chunk=chunk))
+
+
+@pytest.mark.parametrize("N,scored", [(600, 1), (600, 255), (600, 257), (3000, 63), (3000, 64), (3000, 65)])
+def test_few_of_the_rows_are_scored(N, scored):
+    """The vocabulary is split for dx by the rows that are scored, known on the device only."""
+    x, W, t = _inputs(N, 136, 9000, seed=14, ignored=0.0)
+    order = torch.randperm(N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1))
+    t[order[scored:]] = IGN
+    _check(x, W, t, _run(x, W, t))
+    _check(x, W, t, _run(x, W, t, chunk=500, dw_dtype=F32))
+
+
+def test_losses_of_deep_products_are_centred():
+    """d = 4096: the mean error of the log-sums. Sums that drop half a unit towards zero at each of 256 steps would be
+    9e-6 low on these inputs (logits weighted by their probabilities average 2.2, 4e-6 of each is lost)."""
+    x, W, t = _inputs(2048, 4096, 4096, seed=15, ignored=0.0)
+    nll, lse, _ = _run(x, W, t, grad=False)
+    z = x.double() @ W.double().T
+    ref = torch.logsumexp(z, 1)
+    assert abs(float((lse.double() - ref).mean())) < 2e-6
+    want = ref - z.gather(1, t[:, None])[:, 0]
+    assert float((nll.double() - want).norm() / want.norm()) < 1e-6
+
+
 @pytest.mark.parametrize("dw", [BF, F32])
 def test_no_row_is_scored(dw):
     x, W, t = _inputs(70, 64, 300)
