@@ -151,24 +151,20 @@ __device__ __forceinline__ int find_tensor(const Table<CAP>& t, int u)
     return lo;
 }
 
-__device__ double block_sum(double v)
+__device__ __forceinline__ double warp_sum_f64(double v)
 {
-    __shared__ double part[kThreads / 32];
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) s += part[i];
-    return s;
+    return v;
 }
 
-// Sum of the squares of one thread's 32 elements. In fp32, unless the largest is
-// so large that its square overflows or so small that squares are lost below
-// fp32's range: then in 64 bits from the same registers (unrolled as well: a loop
-// that indexes them moves all elements to local memory, and both passes over 2.1 GB
-// took 1.26 instead of 1.00 ms).
+// Sum of the squares of a warp's 1024 elements. In fp32, unless the largest is so
+// large that its square overflows or so small that squares are lost below fp32's
+// range: then in 64 bits from the same registers (unrolled as well: a loop that
+// indexes them moves all elements to local memory, and both passes over 2.1 GB took
+// 1.26 instead of 1.00 ms). 64-bit additions are rare on purpose: this GPU does two
+// a clock and SM, and sums of blocks in which every thread took part in them cost 8
+// of the 15 us of a call on 500 one-element tensors.
 __device__ __forceinline__ double sum_squares(const float (&v)[kPer])
 {
     float s[4] = {0.f, 0.f, 0.f, 0.f}, m = 0.f;
@@ -177,13 +173,13 @@ __device__ __forceinline__ double sum_squares(const float (&v)[kPer])
         s[k & 3] = fmaf(v[k], v[k], s[k & 3]);
         m = fmaxf(m, fabsf(v[k]));
     }
-    if (m > 0x1p+60f || (m < 0x1p-40f && m > 0.f)) {
+    if (__any_sync(0xffffffffu, m > 0x1p+58f || (m < 0x1p-40f && m > 0.f))) {
         double d = 0.0;
 #pragma unroll
         for (int k = 0; k < kPer; ++k) d = fma((double)v[k], (double)v[k], d);
-        return d;
+        return warp_sum_f64(d);
     }
-    return (double)((s[0] + s[1]) + (s[2] + s[3]));
+    return (double)warp_sum((s[0] + s[1]) + (s[2] + s[3]));
 }
 
 template <int CAP>
@@ -203,8 +199,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             s += sum_squares(v);
         });
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    __shared__ double part[kThreads / 32];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {  // one warp: the others' additions would wait for the same unit
+        s = part[0];
+#pragma unroll
+        for (int i = 1; i < kThreads / 32; ++i) s += part[i];
+        if (threadIdx.x == 0) partial[blockIdx.x] = s;
+    }
 }
 
 // n_partial sums were written; this launch scales the tensors of its table.
@@ -213,9 +216,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     k_clip_scale(const __grid_constant__ Table<CAP> t, const double* __restrict__ partial, int n_partial,
                  float max_norm, float* __restrict__ norm_out)
 {
-    double s = 0.0;
-    for (int i = threadIdx.x; i < n_partial; i += kThreads) s += partial[i];
-    const float norm = (float)sqrt(block_sum(s));
+    __shared__ float norm_s;
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+        for (int i = threadIdx.x; i < n_partial; i += 32 * 8) {
+            double v[8];  // asked for together
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = i + 32 * k < n_partial ? partial[i + 32 * k] : 0.0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + 32 * k < n_partial) s += v[k];
+        }
+        s = warp_sum_f64(s);
+        if (threadIdx.x == 0) norm_s = (float)sqrt(s);
+    }
+    __syncthreads();
+    const float norm = norm_s;
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
     // a norm that is NaN keeps a NaN factor; an infinite one gives 0 (NaN where g is infinite)
     const float r = max_norm / norm;

@@ -11,7 +11,8 @@
 //
 //   k_ln_fwd       rows up to 8192 elements, held by their threads
 //   k_ln_bwd       the same: dx, and partial dw, db of each block
-//   k_ln_reduce    the blocks' partial sums added in order
+//   k_ln_reduce    the blocks' partial sums added in order (few rows: blocks of
+//                  k_ln_bwd sum whole columns instead)
 //   k_ln_fwd_long, k_ln_bwd_long, k_ln_cols_long   longer rows, read several times
 #include "common.cuh"
 #include "launch.h"
@@ -46,13 +47,19 @@ struct BwdArgs {
     int64_t lddy, ldx, lddres, lddx, N;
     int d;
     const float *mean, *rstd;
-    float* part;  // [parts, 2, d] partial sums of dw and db; null: not wanted
-    int parts;
+    float* part;  // [parts, 2, d] partial sums of dw and db; null: not wanted, or dw and db direct
+    int parts;    // blocks that work on rows
+    float *dw, *db;  // few rows: blocks after those sum whole columns
     bool w_f32;
 };
 
 constexpr int kRowThreads = 256;
 constexpr int kMaxLongParts = 304;
+// Up to so many rows the column sums are taken by blocks of their own in the same
+// launch. Backward with those / with partial sums and a second launch, us, bf16:
+// 256 x 1024 3.2 / 6.3, 768 x 1024 5.4 / 7.6, 768 x 4096 10.7 / 11.9, 1024 x 1024 7.6 / 7.3,
+// 1024 x 4096 13.1 / 14.3, 1536 x 4096 20.6 / 17.7.
+constexpr int64_t kFewRows = 896;
 
 // Element i of a weight vector of either type; `none` where there is no vector.
 __device__ __forceinline__ float weight(const void* p, int i, bool f32, float none)
@@ -615,6 +622,37 @@ __device__ __forceinline__ void store_sums(float* p, const float* s)
     }
 }
 
+// dw and db of 16 columns over all rows, one block: sixteenths (or 32nds) of the
+// rows summed side by side, then joined in order.
+constexpr int kColBlock = 16;
+template <class TX, class TY>
+__device__ __forceinline__ void column_sums(const BwdArgs& a, int block)
+{
+    __shared__ float2 sums[kMaxGroup / kColBlock][kColBlock];
+    const int c = threadIdx.x % kColBlock, lane = threadIdx.x / kColBlock, lanes = blockDim.x / kColBlock;
+    const int col = block * kColBlock + c;
+    float dw = 0.f, db = 0.f;
+    if (col < a.d) {
+#pragma unroll 8
+        for (int64_t r = lane; r < a.N; r += lanes) {
+            const float x = TX::load(row_of<TX>(a.x, r, a.ldx) + col);
+            const float g = TY::load(row_of<TY>(a.dy, r, a.lddy) + col);
+            dw = fmaf(g, (x - a.mean[r]) * a.rstd[r], dw);
+            db += g;
+        }
+    }
+    sums[lane][c] = make_float2(dw, db);
+    __syncthreads();
+    if (lane == 0 && col < a.d) {
+        for (int i = 1; i < lanes; ++i) {
+            dw += sums[i][c].x;
+            db += sums[i][c].y;
+        }
+        a.dw[col] = dw;
+        a.db[col] = db;
+    }
+}
+
 // The normalised values and w dy are formed twice from what was read (before
 // and after the row's sums): two products cost less than the registers.
 template <class TX, class TY, int VEC, int PER, bool RES>
@@ -624,6 +662,10 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
     constexpr int SX = piece_bytes<TX, VEC>(), SY = piece_bytes<TY, VEC>();
     constexpr bool RING = ringed<TX, TY, VEC>();
     constexpr int G0 = NV * SX, Q0 = G0 + NV * SY;  // offsets of dy and dres
+    if ((int)blockIdx.x >= a.parts) {
+        column_sums<TX, TY>(a, blockIdx.x - a.parts);
+        return;
+    }
     extern __shared__ uint4 dyn[];
     __shared__ float2 buf[32];
     RowSum rs(buf, G);
@@ -641,7 +683,7 @@ __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const 
         }
         if (i < a.d && a.w) load_weights<VEC>(a.w, i, a.w_f32, w + v * VEC);
     }
-    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t step = (int64_t)a.parts * groups;
     int64_t r = (int64_t)blockIdx.x * groups + threadIdx.x / G;
     int64_t asked = r;
     const typename TX::type* ax = row_of<TX>(a.x, r, a.ldx) + t * VEC;
@@ -863,13 +905,14 @@ template <class TX, class TY, int PER, bool RES>
 cudaError_t launch_bwd(const BwdArgs& a, int G, int vec, unsigned threads, cudaStream_t s)
 {
     constexpr int B = bwd_bytes<TX, TY, PER, RES>();
+    const unsigned blocks = a.parts + (a.dw ? (a.d + kColBlock - 1) / kColBlock : 0);
     // the groups' column sums, when a block holds several rows at a time (over the ring where there is one)
-    const size_t sums = G < 256 ? (size_t)rows_per_block(G) * 2 * a.d * sizeof(float) : 0;
+    const size_t sums = a.part && G < 256 ? (size_t)rows_per_block(G) * 2 * a.d * sizeof(float) : 0;
     const size_t ring = Ring<stages_for(B), B>::bytes(threads), both = ring > sums ? ring : sums;
     if (vec == 1)
-        return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, a.parts, threads, ringed<TX, TY, 1>() ? both : sums, s);
-    if (vec == 2) return launch_rows(k_ln_bwd<TX, TY, 2, PER, RES>, a, G, a.parts, threads, both, s);
-    return launch_rows(k_ln_bwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, a.parts, threads, both, s);
+        return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, ringed<TX, TY, 1>() ? both : sums, s);
+    if (vec == 2) return launch_rows(k_ln_bwd<TX, TY, 2, PER, RES>, a, G, blocks, threads, both, s);
+    return launch_rows(k_ln_bwd<TX, TY, vec_of<TX, TY>(), PER, RES>, a, G, blocks, threads, both, s);
 }
 
 template <class TX, class TY>
@@ -888,13 +931,13 @@ cudaError_t bwd(const BwdArgs& a, int vec, float* dw, float* db, cudaStream_t s)
                        : launch_bwd<TX, TY, 16, false>(a, G, vec, threads, s);
     } else {
         k_ln_bwd_long<TX, TY><<<(unsigned)(a.N < 65536 ? a.N : 65536), kRowThreads, 0, s>>>(a);
-        if (dw) {
+        if (a.part) {
             count_launches(1);
             k_ln_cols_long<TX, TY><<<dim3((unsigned)((a.d + 31) / 32), (unsigned)a.parts), dim3(32, 8), 0, s>>>(a);
         }
         e = cudaGetLastError();
     }
-    if (e != cudaSuccess || !dw) return e;
+    if (e != cudaSuccess || !a.part) return e;
     count_launches(1);
     k_ln_reduce<<<(unsigned)((2 * (int64_t)a.d + 31) / 32), dim3(32, 32), 0, s>>>(a.part, a.parts, a.d, dw, db);
     return cudaGetLastError();
@@ -983,8 +1026,11 @@ extern "C" twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const 
     vec = pieces(dres, lddres, N, x_type, vec);
     vec = pieces(dx, lddx, N, x_type, vec);
     vec = pieces(w, 0, 1, w_type, vec);
+    // few rows: the column sums by blocks of their own, which read the rows again (from L2)
+    const bool direct = dw && N <= kFewRows && group_of(d) != 0;
     const BwdArgs a{dy, x, w, dres, dx, lddy, ldx, lddres, lddx, N, d, mean, rstd,
-                    dw ? static_cast<float*>(ws) : nullptr, parts_for(N, d), w_type == TWELL_F32};
+                    dw && !direct ? static_cast<float*>(ws) : nullptr, parts_for(N, d),
+                    direct ? dw : nullptr, direct ? db : nullptr, w_type == TWELL_F32};
     const cudaError_t e = by_types(x_type, y_type, [&](auto tx, auto ty) {
         return bwd<decltype(tx), decltype(ty)>(a, vec, dw, db, s);
     });

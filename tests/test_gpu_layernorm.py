@@ -324,7 +324,7 @@ def test_even_widths(N, d, types, res):
     _check_bwd(_rand((N, d), ty, 5), x if s is None else s, w, _rand((N, d), tx, 6) if res else None, mean, rstd)
 
 
-@pytest.mark.parametrize("N", [1, 2, 151, 152, 153, 303, 304, 305, 608, 609, 1216, 1217, 3000])
+@pytest.mark.parametrize("N", [1, 2, 151, 152, 153, 303, 304, 305, 608, 609, 896, 897, 1216, 1217, 3000])
 def test_rows_around_a_full_gpu(N):
     """Fewer rows than resident blocks, exactly as many, one more: groups with no row, one row, several."""
     for d in (24, 512, 1001):
