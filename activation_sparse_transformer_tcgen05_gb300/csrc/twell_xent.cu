@@ -313,9 +313,18 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (i < N) gather_row(x, d, w, ldx, i, perm[i], o.total, threadIdx.x & 31, nll, lse, dx);
 }
 
+// a + b rounded, and what the rounding lost.
+__device__ __forceinline__ float two_sum(float a, float b, float* lost)
+{
+    const float s = a + b, bb = s - a;
+    *lost = (a - (s - bb)) + (b - bb);
+    return s;
+}
+
 // One warp per scored row: the tiles' (maximum, sum) pairs joined, in the order
 // of the lanes' strides and then a butterfly. In the call's last chunk the block
-// that finishes last adds up the N losses, in a fixed order and 64 bits.
+// that finishes last adds up the N losses, in a fixed order and with what each
+// addition lost.
 __device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int lane, const int32_t* perm, float* nll,
                                         float* lse)
 {
@@ -333,12 +342,26 @@ __device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int
     }
     s = warp_sum(s);
     if (lane != 0) return;
-    const double l = s == 0.f ? -INFINITY : (double)m * 0.69314718055994530942 + (double)logf(s);
-    const float loss = (float)(l - (double)w.ztarget[row]);
-    lse[perm[row]] = (float)l;
+    // m ln 2 + log s as a sum l and its rounding error e, so that a small loss keeps
+    // its digits; in fp32, as this GPU does two 64-bit additions a clock and SM
+    constexpr float ln2 = 0.69314718055994530942f;
+    constexpr float ln2_rest = (float)(0.69314718055994530942 - (double)ln2);
+    float l, e = 0.f;
+    if (s == 0.f) {
+        l = -INFINITY;
+    } else {
+        const float hi = m * ln2, lo = fmaf(m, ln2, -hi) + m * ln2_rest, lg = logf(s);
+        l = two_sum(hi, lg, &e);
+        e += lo;
+    }
+    const float zt = w.ztarget[row];
+    float e2;
+    const float diff = two_sum(l, -zt, &e2);
+    const float loss = isfinite(diff) ? diff + (e + e2) : diff;
+    lse[perm[row]] = isfinite(l) ? l + e : l;
     nll[perm[row]] = loss;
     w.nll[row] = loss;
-    w.lse2[row] = (float)(l * 1.4426950408889634074);
+    w.lse2[row] = s == 0.f ? -INFINITY : m + log2f(s);
 }
 
 __global__ void __launch_bounds__(256)
@@ -350,22 +373,30 @@ __global__ void __launch_bounds__(256)
     if (row < *rows_dev) row_lse(w, tiles, row, threadIdx.x & 31, perm, nll, lse);
     if (!last_chunk) return;
     __shared__ bool last;
-    __shared__ double part[256];
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) last = atomicAdd(w.done, 1) == (int)gridDim.x - 1;
     __syncthreads();
     if (!last) return;
-    double s = 0.0;
-    for (int i = threadIdx.x; i < N; i += 256) s += (double)__ldcg(nll + i);
-    part[threadIdx.x] = s;
-    for (int half = 128; half >= 1; half >>= 1) {
-        __syncthreads();
-        if ((int)threadIdx.x < half) part[threadIdx.x] += part[threadIdx.x + half];
+    float s = 0.f, c = 0.f, lost;
+    for (int i = threadIdx.x; i < N; i += 256) {
+        s = two_sum(s, __ldcg(nll + i), &lost);
+        c += lost;
     }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) {
+        c += __shfl_xor_sync(0xffffffffu, c, off);
+        s = two_sum(s, __shfl_xor_sync(0xffffffffu, s, off), &lost);
+        c += lost;
+    }
+    __shared__ float2 part[8];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(s, c);
+    __syncthreads();
     if (threadIdx.x == 0) {
+        double total = 0.0;
+        for (int i = 0; i < 8; ++i) total += (double)part[i].x + (isfinite(part[i].x) ? (double)part[i].y : 0.0);
         const int n = *w.count;
-        *loss = n == 0 ? 0.f : (float)(mean ? part[0] / (double)n : part[0]);
+        *loss = n == 0 ? 0.f : (float)(mean ? total / (double)n : total);
     }
 }
 

@@ -229,6 +229,34 @@ def test_bad_row_stays_alone():
         assert torch.equal(out[k][keep], ref[k][keep])
 
 
+def test_words_at_minus_infinity():
+    """Words masked by a logit of -inf (whole tiles of them too) add nothing; a target among them has an infinite loss."""
+    N, d, V = 70, 64, 900
+    x, W, t = _inputs(N, d, V, seed=16, ignored=0.0)
+    x[:, 0] = 1.0
+    W[:, 0] = 0.0
+    masked = torch.zeros(V, dtype=torch.bool, device="cuda")
+    masked[:300] = True
+    masked[520:650] = True
+    masked[::7] = True
+    W[masked, 0] = -float("inf")
+    allowed = torch.nonzero(~masked)[:, 0]
+    t = allowed[t % len(allowed)]
+    kept = W[allowed].contiguous()
+    place = torch.cumsum(~masked, 0) - 1
+    ref = _run(x, kept, place[t], mean=False, grad=False)
+    out = _run(x, W, t, mean=False, grad=False)
+    for a, b in zip(out, ref):
+        assert torch.allclose(a, b, rtol=2e-6, atol=0)
+    t[5] = 10
+    out = _run(x, W, t, mean=False, grad=False)
+    assert float(out[0][5]) == float("inf") and float(out[2]) == float("inf")
+    assert bool(out[0][6:].isfinite().all()) and torch.allclose(out[1], ref[1], rtol=2e-6, atol=0)
+    W[:, 0] = -float("inf")  # nothing is left
+    out = _run(x, W, t, mean=False, grad=False)
+    assert bool((out[1] == -float("inf")).all()) and bool(out[0].isnan().all())
+
+
 def test_ignore_index_may_be_a_word():
     x, W, t = _inputs(100, 64, 50, seed=6, ignored=0.0)
     t[::3] = 0
