@@ -768,6 +768,8 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const bool leader = rank == 0;
+    // (written by an earlier kernel, same in both CTAs; read here so that the loads overlap the set-up)
+    const int rowsA = a.rowsA_dev ? min(*a.rowsA_dev, a.rowsA) : a.rowsA;
     if (threadIdx.x == 0) {
         *skip = (leader && has_error(a.status)) ? 1 : 0;
         *abort_flag = 0;
@@ -787,7 +789,6 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
     const int sk = ld_cluster_s32(cluster_addr(const_cast<int*>(skip), 0));
     cluster_sync();  // the leader's flag has been read before anyone may leave
     if (sk) return;  // an earlier kernel of this call failed; uniform over the pair
-    const int rowsA = a.rowsA_dev ? min(*a.rowsA_dev, a.rowsA) : a.rowsA;  // same in both CTAs
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, L::TMEM_COLS);
         tmem_relinquish_pair();

@@ -328,6 +328,9 @@ __device__ __forceinline__ float two_sum(float a, float b, float* lost)
 __device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int lane, const int32_t* perm, float* nll,
                                         float* lse)
 {
+    // asked for first: each load a row waits for is a third of a microsecond of the call
+    const float zt = w.ztarget[row];
+    const int to = perm[row];
     float m = -INFINITY;
     const float2* st = w.stat + (size_t)row * tiles;
     for (int t = lane; t < tiles; t += 32) m = fmaxf(m, st[t].x);
@@ -354,12 +357,11 @@ __device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int
         l = two_sum(hi, lg, &e);
         e += lo;
     }
-    const float zt = w.ztarget[row];
     float e2;
     const float diff = two_sum(l, -zt, &e2);
     const float loss = isfinite(diff) ? diff + (e + e2) : diff;
-    lse[perm[row]] = isfinite(l) ? l + e : l;
-    nll[perm[row]] = loss;
+    lse[to] = isfinite(l) ? l + e : l;
+    nll[to] = loss;
     w.nll[row] = loss;
     w.lse2[row] = s == 0.f ? -INFINITY : m + log2f(s);
 }
@@ -368,9 +370,10 @@ __global__ void __launch_bounds__(256)
     k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ perm, float* nll,
                float* lse, int last_chunk, int N, int mean, float* loss, const int32_t* status)
 {
+    const int rows = *rows_dev, scored = *w.count;
     if (has_error(status)) return;
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row < *rows_dev) row_lse(w, tiles, row, threadIdx.x & 31, perm, nll, lse);
+    if (row < rows) row_lse(w, tiles, row, threadIdx.x & 31, perm, nll, lse);
     if (!last_chunk) return;
     __shared__ bool last;
     __threadfence();
@@ -393,10 +396,13 @@ __global__ void __launch_bounds__(256)
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(s, c);
     __syncthreads();
     if (threadIdx.x == 0) {
-        double total = 0.0;
-        for (int i = 0; i < 8; ++i) total += (double)part[i].x + (isfinite(part[i].x) ? (double)part[i].y : 0.0);
-        const int n = *w.count;
-        *loss = n == 0 ? 0.f : (float)(mean ? total / (double)n : total);
+        // (a 64-bit division alone would take a microsecond here)
+        for (int i = 1; i < 8; ++i) {
+            s = two_sum(s, part[i].x, &lost);
+            c += part[i].y + lost;
+        }
+        const float total = isfinite(s) ? s + c : s;
+        *loss = scored == 0 ? 0.f : mean ? total / (float)scored : total;
     }
 }
 
