@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return (uint32_t)f32_to_bf16_bits(lo) | ((uint32_t)f32_to_bf16_bits(hi) << 16);
 }
 
+// The same pair by one conversion instruction.
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return (uint32_t)__bfloat16_as_ushort(b.x) | (uint32_t)__bfloat16_as_ushort(b.y) << 16;
+}
+
 // 2^x by the special-function unit (about 2 ulp; results below 2^-126 are 0).
 __device__ __forceinline__ float exp2_approx(float x)
 {

@@ -109,8 +109,8 @@ struct Slice {
                                     v[k + 3 < kPer ? k + 3 : k]);
                 } else if constexpr (VEC) {
                     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i0 + i) =
-                        make_uint4(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]),
-                                   pack_bf16x2(v[k + 4], v[k + 5]), pack_bf16x2(v[k + 6], v[k + 7]));
+                        make_uint4(cvt_bf16x2(v[k], v[k + 1]), cvt_bf16x2(v[k + 2], v[k + 3]),
+                                   cvt_bf16x2(v[k + 4], v[k + 5]), cvt_bf16x2(v[k + 6], v[k + 7]));
                 }
             } else {
 #pragma unroll

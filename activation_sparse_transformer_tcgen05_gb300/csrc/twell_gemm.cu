@@ -252,6 +252,25 @@ struct Outbox {
     {
         *reinterpret_cast<uint4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = v;
     }
+    // Stores the 32 rows at `to` (this lane's piece of row 0), `stride` bytes apart; the
+    // first `rows` of them, and those only if this lane's piece exists (`col_ok`).
+    __device__ __forceinline__ void drain_to(void* to, size_t stride, int rows, bool col_ok)
+    {
+        __syncwarp();
+        const int c = lane & 7, r0 = lane >> 3;
+        const uint8_t* from = box + r0 * 128;
+        char* p = static_cast<char*>(to) + r0 * stride;
+        if (col_ok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // row i * 4 + r0: its pieces are permuted by (i * 4 + r0) & 7
+                const uint4 q = *reinterpret_cast<const uint4*>(from + i * 512 + ((c ^ ((i * 4 + r0) & 7)) << 4));
+                if (i * 4 + r0 < rows) *reinterpret_cast<uint4*>(p) = q;
+                p += 4 * stride;
+            }
+        }
+        __syncwarp();
+    }
     // f(row, piece, value) for the 256 pieces, eight in turn for each lane
     template <class F>
     __device__ __forceinline__ void drain(F f)
@@ -297,7 +316,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
     const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, unit);
     const float magic = 8388608.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile;
+    uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile + (box.lane & 7) * 8;
 #pragma unroll 1
     for (int ch = 0; ch < NCH; ++ch) {
         if (!FULL && ch * 32 >= ncols) break;
@@ -320,10 +339,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
             // after 64 columns, or the last ones: the row stride is whole 64s, and what
             // the other half then holds lies past the vocabulary, where nothing reads it
             if ((ch & 1) == 1 || (!FULL && ch * 32 + 32 >= ncols))
-                box.drain([&](int r, int c, const uint4& q) {
-                    if (row0 + r < rowsA)
-                        *reinterpret_cast<uint4*>(to + (size_t)r * a.ldcode + (ch >> 1) * 64 + c * 8) = q;
-                });
+                box.drain_to(to + (ch >> 1) * 64, a.ldcode * 2, rowsA - row0, true);
         }
     }
     if (row < rowsA)
@@ -340,6 +356,7 @@ __device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int ro
 {
     const bool f32 = MODE == GEMM_SPLITK || a.out_f32;
     float* out = MODE == GEMM_SPLITK ? a.out_f32 + (size_t)split * rowsA * a.ldo : a.out_f32;
+    const int c = box.lane & 7;
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
         const int cc = col0 + ch * 32;
@@ -348,26 +365,27 @@ __device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int ro
         tmem_ld32_wait(tbase + ch * 32, v);
         if (MODE != GEMM_SPLITK) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * scale);
+            for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * scale);
         }
         if (f32) {
 #pragma unroll
             for (int g = 0; g < 8; ++g) box.put(g, make_uint4(v[g * 4], v[g * 4 + 1], v[g * 4 + 2], v[g * 4 + 3]));
-            box.drain([&](int r, int c, const uint4& q) {
-                const int col = cc + c * 4;
-                if (row0 + r >= rowsA || col >= a.rowsB) return;
-                float4* to = reinterpret_cast<float4*>(out + (size_t)(row0 + r) * a.ldo + col);
-                float4 f = make_float4(__uint_as_float(q.x), __uint_as_float(q.y), __uint_as_float(q.z),
-                                       __uint_as_float(q.w));
-                if (MODE != GEMM_SPLITK && a.accumulate) {
-                    const float4 p = *to;
-                    f.x += p.x;
-                    f.y += p.y;
-                    f.z += p.z;
-                    f.w += p.w;
-                }
-                *to = f;
-            });
+            if (MODE == GEMM_SPLITK || !a.accumulate) {
+                box.drain_to(out + (size_t)row0 * a.ldo + cc + c * 4, (size_t)a.ldo * 4, rowsA - row0,
+                             cc + c * 4 < a.rowsB);
+            } else {
+                box.drain([&](int r, int pc, const uint4& q) {
+                    const int col = cc + pc * 4;
+                    if (row0 + r >= rowsA || col >= a.rowsB) return;
+                    float4* to = reinterpret_cast<float4*>(out + (size_t)(row0 + r) * a.ldo + col);
+                    float4 f = *to;
+                    f.x += __uint_as_float(q.x);
+                    f.y += __uint_as_float(q.y);
+                    f.z += __uint_as_float(q.z);
+                    f.w += __uint_as_float(q.w);
+                    *to = f;
+                });
+            }
         } else if constexpr (MODE != GEMM_SPLITK) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -375,17 +393,23 @@ __device__ __forceinline__ void epi_product_row(uint32_t tbase, int row0, int ro
                 uint32_t o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    o[e] = pack_bf16x2(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1]));
+                    o[e] = cvt_bf16x2(__uint_as_float(q[2 * e]), __uint_as_float(q[2 * e + 1]));
                 box.put((ch & 1) * 4 + g, make_uint4(o[0], o[1], o[2], o[3]));
             }
-            if ((ch & 1) == 1 || cc + 32 >= a.rowsB)
-                box.drain([&](int r, int c, const uint4& q) {
-                    const int col = col0 + (ch >> 1) * 64 + c * 8;
-                    // (pieces of the other half, if it was not filled, lie past the last column)
-                    if (row0 + r >= rowsA || col >= a.rowsB) return;
-                    const size_t row = a.row_map ? (size_t)a.row_map[row0 + r] : (size_t)(row0 + r);
-                    *reinterpret_cast<uint4*>(a.out + row * a.ldo + col) = q;
-                });
+            if ((ch & 1) == 1 || cc + 32 >= a.rowsB) {
+                // (pieces of the other half, if it was not filled, lie past the last column)
+                const int cp = col0 + (ch >> 1) * 64;
+                if (!a.row_map) {
+                    box.drain_to(a.out + (size_t)row0 * a.ldo + cp + c * 8, (size_t)a.ldo * 2, rowsA - row0,
+                                 cp + c * 8 < a.rowsB);
+                } else {
+                    box.drain([&](int r, int pc, const uint4& q) {
+                        const int col = cp + pc * 8;
+                        if (row0 + r >= rowsA || col >= a.rowsB) return;
+                        *reinterpret_cast<uint4*>(a.out + (size_t)a.row_map[row0 + r] * a.ldo + col) = q;
+                    });
+                }
+            }
         }
     }
 }

@@ -232,14 +232,9 @@ struct Piece<bf16_t, VEC> {
     }
     __device__ __forceinline__ void set(const float* f)
     {
-        v = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+        v = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]), cvt_bf16x2(f[6], f[7]));
     }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = v; }
-    static __device__ __forceinline__ uint32_t pair(float lo, float hi)
-    {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-        return (uint32_t)__bfloat16_as_ushort(b.x) | (uint32_t)__bfloat16_as_ushort(b.y) << 16;
-    }
 };
 template <>
 struct Piece<bf16_t, 1> {
@@ -263,7 +258,7 @@ struct Piece<bf16_t, 4> {
     }
     __device__ __forceinline__ void set(const float* f)
     {
-        v = make_uint2(Piece<bf16_t, 8>::pair(f[0], f[1]), Piece<bf16_t, 8>::pair(f[2], f[3]));
+        v = make_uint2(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]));
     }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint2*>(p) = v; }
 };
@@ -273,7 +268,7 @@ struct Piece<bf16_t, 2> {
     __device__ __forceinline__ void load(const uint16_t* p) { v = *reinterpret_cast<const uint32_t*>(p); }
     __device__ __forceinline__ void zero() { v = 0; }
     __device__ __forceinline__ float get(int i) const { return i ? bf16_hi(v) : bf16_lo(v); }
-    __device__ __forceinline__ void set(const float* f) { v = Piece<bf16_t, 8>::pair(f[0], f[1]); }
+    __device__ __forceinline__ void set(const float* f) { v = cvt_bf16x2(f[0], f[1]); }
     __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint32_t*>(p) = v; }
 };
 template <>

@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(256, 8)
                     for (int e = 0; e < 8; ++e)
                         if (e == target) f[e] = ft;
                 }
-                *p = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                pack_bf16x2(f[6], f[7]));
+                *p = make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                                cvt_bf16x2(f[6], f[7]));
             }
         }
         row += rows_step;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(256)
         }
         const size_t row = i / d4, c = i % d4;
         reinterpret_cast<uint2*>(dx + (size_t)perm[row] * d)[c] =
-            make_uint2(pack_bf16x2(g * a.x, g * a.y), pack_bf16x2(g * a.z, g * a.w));
+            make_uint2(cvt_bf16x2(g * a.x, g * a.y), cvt_bf16x2(g * a.z, g * a.w));
     }
 }
 
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(256)
     if (has_error(status)) return;
     for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
         const float4 a = reinterpret_cast<const float4*>(acc)[i];
-        reinterpret_cast<uint2*>(out)[i] = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        reinterpret_cast<uint2*>(out)[i] = make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(a.z, a.w));
     }
 }
 
