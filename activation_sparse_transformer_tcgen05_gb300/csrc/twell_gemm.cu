@@ -327,9 +327,13 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
             float t = fmaf(__uint_as_float(v[c]), unit, -m2);
             if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
             sum[c & 3] += exp2_approx(t);
-            v[c] = __float_as_uint(fminf(fmaf(t, -kXentSteps, magic), magic + (float)kXentZero));
+            v[c] = __float_as_uint(t);
         }
         if (a.codes) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                v[c] = __float_as_uint(
+                    fminf(fmaf(__uint_as_float(v[c]), -kXentSteps, magic), magic + (float)kXentZero));
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const uint32_t* q = v + g * 8;
