@@ -54,7 +54,7 @@ struct BwdArgs {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kMaxLongParts = 304;
+constexpr int kMaxLongParts = 304;  // two blocks on each of 152 SMs
 // Up to so many rows the column sums are taken by blocks of their own in the same
 // launch. Backward with those / with partial sums and a second launch, us, bf16:
 // 256 x 1024 3.2 / 6.3, 768 x 1024 5.4 / 7.6, 768 x 4096 10.7 / 11.9, 1024 x 1024 7.6 / 7.3,

@@ -365,8 +365,8 @@ twell_status twell_ffn_fwd_static_ws(const uint16_t* x, const uint16_t* W_up, co
 
 /*
  * Layer norm around the feed-forward layer. Rows of d elements; row strides
- * (ld*) in elements, >= d, of any alignment (aligned rows whose d is a multiple
- * of 8 are read in 16-byte pieces). x_type is the type of the residual stream
+ * (ld*) in elements, >= d, of any alignment (rows that all start on 16-byte
+ * boundaries are read in 16-byte pieces, others in pairs or single elements). x_type is the type of the residual stream
  * (x, res, sum, dres, dx), y_type that of y and dy, w_type that of w and b; each
  * TWELL_BF16 or TWELL_F32. w or b may be NULL (1 and 0). N >= 0, d >= 1.
  * Statistics and sums are fp32; outputs are rounded once. Outputs must not
@@ -409,7 +409,7 @@ twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
  *   x [N, d] bf16, W [V, d] bf16 (one row per word), target [N] int64;
  *   nll, lse [N] fp32, loss [1] fp32. N >= 0, V >= 1, d % 8 == 0.
  * The logits are never stored: twell_xent_fwd keeps a maximum and a sum for
- * every (row, 256 words).
+ * every (row, 128 words), and the scored rows of x copied together.
  *
  * twell_xent_fwd_bwd also gives the gradients of grad_scale * loss:
  *   dz_rj = g (exp(z_rj - lse_r) - [j = target(r)]), g = grad_scale (/ scored rows)
