@@ -7,7 +7,8 @@
 //
 // Bound by memory: every element read once and written once (forward: x, res in,
 // sum, y out; backward: x, dy, dres in, dx out). 16384 x 4096 bf16 with residual, 537
-// MB either way, 79 us at the measured copy rate: forward 88 us, backward 87 us (6 us of it the column sums).
+// MB either way, 79 us at the measured copy rate: forward 82 us, backward 84.5 us (5 us
+// of it the column sums).
 //
 //   k_ln_fwd       rows up to 8192 elements, held by their threads
 //   k_ln_bwd       the same: dx, and partial dw, db of each block
@@ -459,9 +460,10 @@ struct Ring {
     }
 };
 
-// Stages of the ring: rows in flight for at most 98 KB with 256 threads of 16
-// elements, so that two blocks fit an SM.
-constexpr int stages_for(int bytes) { return bytes <= 96 ? 4 : bytes <= 128 ? 3 : 2; }
+// Rows of a stream on their way: the next one while a row is worked on is enough,
+// and more of them slow the memory down (16384 x 4096 bf16 with residual, forward: two
+// rows 82 us, three 86, four 90, six 96).
+constexpr int kStages = 2;
 
 // Blocks of 512 threads that share an SM: two (64 registers a thread) with 8
 // elements a thread, one with 16.
@@ -476,7 +478,7 @@ constexpr int fwd_bytes()
 template <class TX, class TY, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_fwd(const FwdArgs a, int G)
 {
-    constexpr int NV = PER / VEC, BYTES = fwd_bytes<TX, PER, RES>(), STAGES = stages_for(BYTES);
+    constexpr int NV = PER / VEC, BYTES = fwd_bytes<TX, PER, RES>(), STAGES = kStages;
     constexpr int SX = piece_bytes<TX, VEC>();
     constexpr bool RING = ringed<TX, TY, VEC>();
     extern __shared__ uint4 dyn[];
@@ -653,7 +655,7 @@ __device__ __forceinline__ void column_sums(const BwdArgs& a, int block)
 template <class TX, class TY, int VEC, int PER, bool RES>
 __global__ void __launch_bounds__(kMaxGroup, blocks_per_sm(PER)) k_ln_bwd(const BwdArgs a, int G)
 {
-    constexpr int NV = PER / VEC, BYTES = bwd_bytes<TX, TY, PER, RES>(), STAGES = stages_for(BYTES);
+    constexpr int NV = PER / VEC, BYTES = bwd_bytes<TX, TY, PER, RES>(), STAGES = kStages;
     constexpr int SX = piece_bytes<TX, VEC>(), SY = piece_bytes<TY, VEC>();
     constexpr bool RING = ringed<TX, TY, VEC>();
     constexpr int G0 = NV * SX, Q0 = G0 + NV * SY;  // offsets of dy and dres
@@ -870,7 +872,7 @@ template <class TX, class TY, int PER, bool RES>
 cudaError_t launch_fwd(const FwdArgs& a, int G, int vec, unsigned blocks, unsigned threads, cudaStream_t s)
 {
     constexpr int B = fwd_bytes<TX, PER, RES>();
-    const size_t ring = Ring<stages_for(B), B>::bytes(threads);
+    const size_t ring = Ring<kStages, B>::bytes(threads);
     if (vec == 1)
         return launch_rows(k_ln_fwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, ringed<TX, TY, 1>() ? ring : 0, s);
     if (vec == 2) return launch_rows(k_ln_fwd<TX, TY, 2, PER, RES>, a, G, blocks, threads, ring, s);
@@ -903,7 +905,7 @@ cudaError_t launch_bwd(const BwdArgs& a, int G, int vec, unsigned threads, cudaS
     const unsigned blocks = a.parts + (a.dw ? (a.d + kColBlock - 1) / kColBlock : 0);
     // the groups' column sums, when a block holds several rows at a time (over the ring where there is one)
     const size_t sums = a.part && G < 256 ? (size_t)rows_per_block(G) * 2 * a.d * sizeof(float) : 0;
-    const size_t ring = Ring<stages_for(B), B>::bytes(threads), both = ring > sums ? ring : sums;
+    const size_t ring = Ring<kStages, B>::bytes(threads), both = ring > sums ? ring : sums;
     if (vec == 1)
         return launch_rows(k_ln_bwd<TX, TY, 1, PER, RES>, a, G, blocks, threads, ringed<TX, TY, 1>() ? both : sums, s);
     if (vec == 2) return launch_rows(k_ln_bwd<TX, TY, 2, PER, RES>, a, G, blocks, threads, both, s);
