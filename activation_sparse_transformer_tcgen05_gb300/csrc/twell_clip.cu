@@ -233,9 +233,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __syncthreads();
     const float norm = norm_s;
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    // a norm that is NaN keeps a NaN factor; an infinite one gives 0 (NaN where g is infinite)
-    const float r = max_norm / norm;
-    const float c = r >= 1.f ? 1.f : r;
+    // by comparison, as the quotient of two zeros or two infinities has no value: an infinite bound
+    // leaves everything, a NaN norm gives a NaN factor, an infinite one 0 (NaN where g is infinite)
+    const float c = norm <= max_norm || max_norm == INFINITY ? 1.f : max_norm / norm;
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
     int k = u0 < u1 ? find_tensor(t, u1 - 1) : 0;
     for (int u = u1 - 1; u >= u0; --u) {

@@ -440,8 +440,10 @@ twell_status twell_xent_fwd_bwd(const uint16_t* x, const uint16_t* W, const int6
  *   norm = sqrt(sum of g^2 over all elements), c = min(1, max_norm / norm),
  *   out = c g, rounded once to the tensor's type.
  * out[i] may be in[i] (then nothing is written while c = 1) or a tensor that
- * overlaps no input. max_norm >= 0; INFINITY gives the norm alone (in place). A NaN
- * norm makes every written element NaN; an infinite one makes finite elements 0.
+ * overlaps no input. max_norm >= 0; c = 1 where norm <= max_norm (both 0 included).
+ * INFINITY gives the norm alone (in place; copies otherwise), whatever the norm is.
+ * With a finite bound a NaN norm makes every element NaN and an infinite one makes
+ * finite elements 0.
  *   list: host struct of host arrays (read during the call): n tensors, device
  *   addresses, element counts (>= 0) and twell_dtype codes; tensors are
  *   contiguous and aligned to their element size. norm [1] fp32 device.
