@@ -1,7 +1,7 @@
 // twell_clip.cu — L2 norm over many tensors, and the tensors scaled so that it
 // is at most a bound.
 //
-//   norm = sqrt(sum over all elements of g^2),  c = min(1, max_norm / norm)
+//   norm = sqrt(sum over all elements of g^2),  c = 1 where norm <= max_norm, else max_norm / norm
 //   out = c g, rounded once to the tensor's type
 //
 // Bound by memory: every element is read for the norm, and read and written
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     k_clip_scale(const __grid_constant__ Table<CAP> t, const double* __restrict__ partial, int n_partial,
                  float max_norm, float* __restrict__ norm_out)
 {
-    __shared__ float norm_s;
+    __shared__ float norm_s, factor_s, shift_s;
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int i = threadIdx.x; i < n_partial; i += 32 * 8) {
@@ -228,14 +228,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 if (i + 32 * k < n_partial) s += v[k];
         }
         s = warp_sum_f64(s);
-        if (threadIdx.x == 0) norm_s = (float)sqrt(s);
+        if (threadIdx.x == 0) {
+            const double norm64 = sqrt(s);
+            const float norm = (float)norm64;
+            // by comparison, as the quotient of two zeros or two infinities has no value: an infinite bound
+            // leaves everything, a NaN norm gives a NaN factor, an infinite one 0 (NaN where g is infinite);
+            // finite elements whose norm passes fp32's range still have a factor. Factors that fp32 would hold
+            // with few bits, or not at all, leave a power of two of theirs aside. (Only those are divided in 64
+            // bits, which would cost every call a microsecond.)
+            float c = norm <= max_norm || max_norm == INFINITY ? 1.f : max_norm / norm, shift = 1.f;
+            if (c < 0x1p-100f && isfinite(norm64)) {
+                shift = 0x1p-60f;
+                c = (float)((double)max_norm / norm64 * 0x1p+60);
+            }
+            norm_s = norm;
+            factor_s = c;
+            shift_s = shift;
+        }
     }
     __syncthreads();
-    const float norm = norm_s;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm;
-    // by comparison, as the quotient of two zeros or two infinities has no value: an infinite bound
-    // leaves everything, a NaN norm gives a NaN factor, an infinite one 0 (NaN where g is infinite)
-    const float c = norm <= max_norm || max_norm == INFINITY ? 1.f : max_norm / norm;
+    const float c = factor_s, shift = shift_s;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = norm_s;
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
     int k = u0 < u1 ? find_tensor(t, u1 - 1) : 0;
     for (int u = u1 - 1; u >= u0; --u) {
@@ -246,8 +259,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         by_slice(t.f32[k], t.vec[k], [&](auto slice) {
             float v[kPer];
             slice.load(t.in[k], i0, left, v);
+            if (c != 1.f) {
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) v[e] *= c;
+                for (int e = 0; e < kPer; ++e) v[e] = v[e] * shift * c;
+            }
             slice.store(t.out[k], i0, left, v);
         });
     }

@@ -442,8 +442,9 @@ twell_status twell_xent_fwd_bwd(const uint16_t* x, const uint16_t* W, const int6
  * out[i] may be in[i] (then nothing is written while c = 1) or a tensor that
  * overlaps no input. max_norm >= 0; c = 1 where norm <= max_norm (both 0 included).
  * INFINITY gives the norm alone (in place; copies otherwise), whatever the norm is.
- * With a finite bound a NaN norm makes every element NaN and an infinite one makes
- * finite elements 0.
+ * With a finite bound a NaN norm makes every element NaN, and an infinite element
+ * makes the finite ones 0. The norm is a 64-bit sum: finite elements whose norm
+ * passes fp32's range are scaled as others are, and *norm is infinite.
  *   list: host struct of host arrays (read during the call): n tensors, device
  *   addresses, element counts (>= 0) and twell_dtype codes; tensors are
  *   contiguous and aligned to their element size. norm [1] fp32 device.

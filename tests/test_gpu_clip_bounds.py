@@ -56,3 +56,20 @@ def test_zero_bound_and_zero_gradients(in_place):
     outs = None if in_place else [torch.full_like(t, 5.0) for t in ts]
     assert _clip(ts, 0.0, outs) == 0.0
     assert not any(t.any() for t in (ts if in_place else outs))
+
+
+@pytest.mark.parametrize("value", [2e38, 3.38e38])
+@pytest.mark.parametrize("max_norm", [1.0, 1e30, 3e38, INF])
+def test_finite_gradients_whose_norm_passes_32_bits(value, max_norm):
+    """The factor comes from the 64-bit norm; the norm itself is reported as infinite."""
+    g, h = torch.full((5_000,), value, device="cuda"), torch.full((700,), -value, device="cuda").to(BF)
+    g[::7] = 1e30
+    before = [g.double().clone(), h.double().clone()]
+    assert all(bool(b.isfinite().all()) for b in before)
+    ref = math.sqrt(sum(float((b ** 2).sum()) for b in before))
+    assert math.isinf(_clip([g, h], max_norm))
+    c = min(1.0, max_norm / ref)
+    for t, b in ((g, before[0]), (h, before[1])):
+        want = b * c
+        assert bool(((t.double() - want).abs() <= want.abs() * (11 * 2.0 ** -24 + 2.0 ** -23 + (2.0 ** -8 if t.dtype is BF else 0))
+                     + c * 2.0 ** -100).all())
