@@ -160,7 +160,6 @@ struct GemmArgs {
                            //   out_f32, with accumulate)
     uint16_t* codes;       // XENT: logit codes [rowsA, ldcode], or null: statistics only
     size_t ldcode;
-    float z_scale;         // XENT: factor of every logit
     float2* xstat;         // XENT: [rowsA, NB] (maximum in log2 units, sum of 2^(z - maximum)), NB tiles of kXentTile
     const int32_t* target; // XENT: [rowsA] column whose logit goes to ztarget
     float* ztarget;        // XENT: [rowsA]

@@ -286,9 +286,17 @@ struct Outbox {
     }
 };
 
+// k-blocks (64 deep) that the tensor cores sum for a logit by themselves. Their fp32 sums drop
+// what does not fit, towards zero, at each step of 16: a logit comes out too small, by (in
+// units of 2^-23 of it; products of one sign / Gaussian ones) 2 / 3 over 512 of depth,
+// 7 / 7 over 1024, 21 / 15 over 2048, 70 / 31 over 4096. Sums over 512 are therefore added
+// up by the epilogue in rounded fp32. (4096 x 2048 x 32768 losses 346 us a call, all in the
+// tensor cores 325; a longer first piece, which would overlap more of the epilogue, 338 to 350.)
+constexpr int kSumBlocks = 8;
+
 // Cross-entropy epilogue of one accumulator row (one thread) and 128 columns
 // (words). Two readings of the accumulator: the maximum m, then, with
-// m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0 (log2(e) times z_scale), the sum of 2^t and the
+// m2 = m log2(e) rounded up and t = z log2(e) - m2 <= 0, the sum of 2^t and the
 // code round(-2048 t). A logit is kept as its distance to the maximum on a
 // logarithmic scale, in steps of 2^-11: the exponential rebuilt from a code is off
 // by at most 2^(2^-12) - 1 = 1.7e-4, a twentieth of its later rounding to bf16 (up
@@ -312,8 +320,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
             if (FULL || ch * 32 + c < ncols) m = fmaxf(m, __uint_as_float(v[c]));
     }
     // no finite logit in the tile: the sum is 0 and every code the zero code
-    const float unit = kLog2e * a.z_scale;
-    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, unit);
+    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kLog2e);
     const float magic = 8388608.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile + (box.lane & 7) * 8;
@@ -324,7 +331,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
         tmem_ld32_wait(tbase + ch * 32, v);
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-            float t = fmaf(__uint_as_float(v[c]), unit, -m2);
+            float t = fmaf(__uint_as_float(v[c]), kLog2e, -m2);
             if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
             sum[c & 3] += exp2_approx(t);
             v[c] = __float_as_uint(t);
@@ -349,6 +356,29 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
     if (row < rowsA)
         a.xstat[(size_t)row * a.NB + tile] =
             make_float2(m == -INFINITY ? -INFINITY : m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
+
+// 128 accumulator columns of a thread's row added to sum, and sum put in their place.
+__device__ __forceinline__ void add_columns(uint32_t taddr, float (&sum)[128])
+{
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        uint32_t v[16];  // (32 at once would spill)
+        tmem_ld16_wait(taddr + ch * 16, v);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) sum[ch * 16 + c] += __uint_as_float(v[c]);
+    }
+}
+__device__ __forceinline__ void set_columns(uint32_t taddr, const float (&sum)[128])
+{
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[ch * 32 + c]);
+        tmem_st32(taddr + ch * 32, v);
+    }
+    tmem_st_wait();
 }
 
 // The product times scale as it leaves for 32 rows x 128 columns: fp32 (part
@@ -898,36 +928,41 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-                if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PAIR_N);
-                const int kb0 = SPLIT ? tile / mn_tiles * parts.y : 0;
-                const int kb1 = SPLIT ? min(kb0 + parts.y, num_kb) : num_kb;
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!mbar_wait(&full[stage], phase, abort_flag)) {
+                const int first = SPLIT ? tile / mn_tiles * parts.y : 0;
+                const int last = SPLIT ? min(first + parts.y, num_kb) : num_kb;
+                // one accumulator for all k-blocks, or for those of a piece that the epilogue adds to the others
+                for (int kb0 = first, kb1; ok && kb0 < last; kb0 = kb1) {
+                    kb1 = MODE == GEMM_XENT ? min(kb0 + kSumBlocks, last) : last;
+                    if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
-                    const uint64_t adesc = operand_desc(A_MN, sa);
-                    const uint64_t bdesc = operand_desc(B_MN, sa + L::A_BYTES);
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PAIR_N);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!mbar_wait(&full[stage], phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
+                        const uint64_t adesc = operand_desc(A_MN, sa);
+                        const uint64_t bdesc = operand_desc(B_MN, sa + L::A_BYTES);
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, ((kb - kb0) | k) != 0);
-                    umma_commit_pair(&empty[stage], 0x3);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (int k = 0; k < BK / 16; ++k)
+                            umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC,
+                                           ((kb - kb0) | k) != 0);
+                        umma_commit_pair(&empty[stage], 0x3);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
+                    if (!ok) break;
+                    umma_commit_pair(&tfull[acc], 0x3);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
-                if (!ok) break;
-                umma_commit_pair(&tfull[acc], 0x3);
-                acc ^= 1;
-                if (acc == 0) acc_phase ^= 1u;
             }
             if (!ok) fail(a.status, abort_flag);
             umma_commit_pair(mma_done, 0x1);  // every MMA issued above has finished once this arrives
@@ -962,8 +997,39 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                     bias_sm[c] = bv;
                 }
             }
+            const int half = (warp - 2) >> 2;  // boxed: this warp's 128 of the tile's columns
+            const int row = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
+            const int row0 = row - lane, col0 = nb * PAIR_N + 128 * half;
+            const bool live = row0 < rowsA && col0 < a.rowsB;  // boxed: not all past the last row or column
             if constexpr (boxed(MODE)) {  // nothing is shared between the warps
-                if (!__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag))) {
+                bool ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
+                if constexpr (MODE == GEMM_XENT) {
+                    if (ok && num_kb > kSumBlocks) {
+                        float sum[128];
+#pragma unroll
+                        for (int k = 0; k < 128; ++k) sum[k] = 0.f;
+                        int done = 0;
+                        while (true) {
+                            tc_fence_after();
+                            const uint32_t at =
+                                tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * PAIR_N + 128 * half);
+                            done += kSumBlocks;
+                            if (live) add_columns(at, sum);
+                            if (done >= num_kb) {
+                                if (live) set_columns(at, sum);
+                                break;
+                            }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
+                            acc ^= 1;
+                            if (acc == 0) acc_phase ^= 1u;
+                            ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
+                            if (!ok) break;
+                        }
+                    }
+                }
+                if (!ok) {
                     *epi_fail = 1;
                     break;
                 }
@@ -974,12 +1040,9 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
             }
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(acc * PAIR_N);
-            const int row = mb * PAIR_M + (int)rank * HALF + 32 * q + lane;
             if constexpr (boxed(MODE)) {
-                const int half = (warp - 2) >> 2;  // this warp's 128 of the tile's columns
                 const uint32_t tb = tbase + 128u * (uint32_t)half;
-                const int row0 = row - lane, col0 = nb * PAIR_N + 128 * half;
-                if (row0 < rowsA && col0 < a.rowsB) {  // else all past the last row or column
+                if (live) {
                     if constexpr (MODE == GEMM_XENT) {
                         // the target's logit: one column for each lane whose target is here
                         const int tc = target - col0;
@@ -989,7 +1052,7 @@ __global__ void __launch_bounds__(64 + 32 * epi_warps(MODE), 1)
                             const int l = __ffs(lanes) - 1;
                             lanes &= lanes - 1;
                             const uint32_t z = tmem_ld1_wait(tb + (uint32_t)__shfl_sync(0xffffffffu, tc, l));
-                            if (lane == l) a.ztarget[row] = __uint_as_float(z) * a.z_scale;
+                            if (lane == l) a.ztarget[row] = __uint_as_float(z);
                         }
                         const int ncols = min(kXentTile, a.rowsB - col0);
                         if (ncols == kXentTile)

@@ -149,15 +149,6 @@ size_t carve(void* ws, int N, int chunk, int d, int V, bool grad, bool acc, Xent
     return used;
 }
 
-// Factor of the logits. The tensor cores' fp32 sums drop what does not fit, towards
-// zero, at each of the d / 16 steps, so a logit's error is one-sided: measured against
-// 64-bit sums, 0.96e-6, 1.99e-6 and 4.05e-6 of the logit at d = 1024, 2048 and 4096,
-// 1.55e-8 a step (half a unit of a sum that grows evenly would be 2.1e-8). Giving the
-// mean back centres the error; a sum that is complete at once, or only at the end,
-// is then off by as much above as below. (d = 4096: losses within 1.2e-6 of the 64-bit
-// ones without it, 4.5e-7 with it.)
-float logit_scale(int d) { return 1.f + (float)((d + 15) / 16) * 1.55e-8f; }
-
 // Inclusive sum over the lanes of a warp.
 __device__ __forceinline__ int warp_scan(int v, int lane)
 {
@@ -635,7 +626,6 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
         g1.ztarget = w.ztarget;
         g1.status = status;
         g1.lda = ldx;
-        g1.z_scale = logit_scale(d);
         e = launch_gemm(GEMM_XENT, w.xs + (size_t)r0 * row_stride(d), W, g1, sms, s);
         if (e != cudaSuccess) return e;
         count_launches(1);
