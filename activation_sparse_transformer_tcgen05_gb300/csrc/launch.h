@@ -162,7 +162,7 @@ struct GemmArgs {
     size_t ldcode;
     float2* xstat;         // XENT: [rowsA, NB] (maximum in log2 units, sum of 2^(z - maximum)), NB tiles of kXentTile
     const int32_t* target; // XENT: [rowsA] column whose logit goes to ztarget
-    float* ztarget;        // XENT: [rowsA]
+    float* ztarget;        // XENT: [rowsA] the logit itself
     float* colsum;         // DENSE, bf16 output only: if set, column sums of the (masked) fp32 results per
                            //   128-row block: colsum[(row / 128) * ldc + col]
     int ldc;
@@ -187,6 +187,7 @@ cudaError_t launch_spmm_union(const TwellView& tw, const uint16_t* W, int d, con
 // gradient pass reads them): code q of a logit z in a (row, 128-column) tile
 // with maximum m2 (log2 units) stands for z log2(e) = m2 - q / 2048; the
 // largest code stands for a probability of zero.
+constexpr float kXentLog2e = 1.4426950408889634f;  // log2(e) as the epilogue multiplies by it
 constexpr float kXentSteps = 2048.f;
 constexpr uint32_t kXentZero = 65535u;
 constexpr int kXentTile = 128;

@@ -231,8 +231,6 @@ __device__ __forceinline__ void epi_dense_row(uint32_t tbase, int row, int rowsA
     }
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
 // --- Epilogues of eight warps, 32 rows x 128 columns of the tile each. Results go
 // through 4 KB of a warp's own shared memory, so that it stores whole 128-byte
 // pieces of rows: threads that store their own rows touch 32 lines with every
@@ -320,7 +318,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
             if (FULL || ch * 32 + c < ncols) m = fmaxf(m, __uint_as_float(v[c]));
     }
     // no finite logit in the tile: the sum is 0 and every code the zero code
-    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kLog2e);
+    const float m2 = m == -INFINITY ? 0.f : __fmul_ru(m, kXentLog2e);
     const float magic = 8388608.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* to = a.codes + (size_t)row0 * a.ldcode + (size_t)tile * kXentTile + (box.lane & 7) * 8;
@@ -331,7 +329,7 @@ __device__ __forceinline__ void epi_xent_row(uint32_t tbase, int row0, int rowsA
         tmem_ld32_wait(tbase + ch * 32, v);
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-            float t = fmaf(__uint_as_float(v[c]), kLog2e, -m2);
+            float t = fmaf(__uint_as_float(v[c]), kXentLog2e, -m2);
             if (!FULL && ch * 32 + c >= ncols) t = -INFINITY;
             sum[c & 3] += exp2_approx(t);
             v[c] = __float_as_uint(t);

@@ -316,14 +316,15 @@ __device__ __forceinline__ float two_sum(float a, float b, float* lost)
 // of the lanes' strides and then a butterfly. In the call's last chunk the block
 // that finishes last adds up the N losses, in a fixed order and with what each
 // addition lost.
-__device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int lane, const int32_t* perm, float* nll,
-                                        float* lse)
+__device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int lane, const int32_t* targets,
+                                        const int32_t* perm, float* nll, float* lse)
 {
     // asked for first: each load a row waits for is a third of a microsecond of the call
+    const float2* st = w.stat + (size_t)row * tiles;
     const float zt = w.ztarget[row];
+    const float mt = st[targets[row] / kXentTile].x;
     const int to = perm[row];
     float m = -INFINITY;
-    const float2* st = w.stat + (size_t)row * tiles;
     for (int t = lane; t < tiles; t += 32) m = fmaxf(m, st[t].x);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -336,35 +337,33 @@ __device__ __forceinline__ void row_lse(const XentWs& w, int tiles, int row, int
     }
     s = warp_sum(s);
     if (lane != 0) return;
-    // m ln 2 + log s as a sum l and its rounding error e, so that a small loss keeps
-    // its digits; in fp32, as this GPU does two 64-bit additions a clock and SM
-    constexpr float ln2 = 0.69314718055994530942f;
-    constexpr float ln2_rest = (float)(0.69314718055994530942 - (double)ln2);
-    float l, e = 0.f;
-    if (s == 0.f) {
-        l = -INFINITY;
-    } else {
-        const float hi = m * ln2, lo = fmaf(m, ln2, -hi) + m * ln2_rest, lg = logf(s);
-        l = two_sum(hi, lg, &e);
-        e += lo;
-    }
-    float e2;
-    const float diff = two_sum(l, -zt, &e2);
-    const float loss = isfinite(diff) ? diff + (e + e2) : diff;
-    lse[to] = isfinite(l) ? l + e : l;
+    const float lg = s == 0.f ? -INFINITY : logf(s);
+    // The exponentials were taken of z c - m, with c log2(e) rounded to fp32 and m the maximum
+    // of z c: m / c brings the maximum back as it was.
+    constexpr double to_nats = 1.0 / (double)kXentLog2e;
+    constexpr float hi = (float)to_nats, lo = (float)(to_nats - (double)hi);
+    lse[to] = isfinite(lg) ? fmaf(m, hi, fmaf(m, lo, lg)) : lg;
+    // The target's exponent t is the one its tile's sum has, so that it cancels against the log-sum: the loss of a
+    // likely target keeps its digits beside logits of any size. A sum of approximate exponentials may
+    // still be a little less than its largest one. (A tile without a finite logit has no maximum: t is then -inf.)
+    const float t = mt == -INFINITY ? zt : fmaf(zt, kXentLog2e, -mt);
+    const float below = (m - (mt == -INFINITY ? 0.f : mt)) - t;
+    const float value = fmaf(below, hi, lg);
+    const float loss = value < 0.f ? 0.f : value;
     nll[to] = loss;
     w.nll[row] = loss;
     w.lse2[row] = s == 0.f ? -INFINITY : m + log2f(s);
 }
 
 __global__ void __launch_bounds__(256)
-    k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ perm, float* nll,
-               float* lse, int last_chunk, int N, int mean, float* loss, const int32_t* status)
+    k_xent_lse(XentWs w, int tiles, const int32_t* __restrict__ rows_dev, const int32_t* __restrict__ targets,
+               const int32_t* __restrict__ perm, float* nll, float* lse, int last_chunk, int N, int mean, float* loss,
+               const int32_t* status)
 {
     const int rows = *rows_dev, scored = *w.count;
     if (has_error(status)) return;
     const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row < rows) row_lse(w, tiles, row, threadIdx.x & 31, perm, nll, lse);
+    if (row < rows) row_lse(w, tiles, row, threadIdx.x & 31, targets, perm, nll, lse);
     if (!last_chunk) return;
     __shared__ bool last;
     __threadfence();
@@ -629,7 +628,7 @@ cudaError_t run_xent(const uint16_t* x, const uint16_t* W, const int64_t* target
         e = launch_gemm(GEMM_XENT, w.xs + (size_t)r0 * row_stride(d), W, g1, sms, s);
         if (e != cudaSuccess) return e;
         count_launches(1);
-        k_xent_lse<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(w, tiles, w.rows_dev + c, w.perm + r0, nll, lse,
+        k_xent_lse<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(w, tiles, w.rows_dev + c, w.target + r0, w.perm + r0, nll, lse,
                                                               N - r0 <= chunk ? 1 : 0, N, mean, loss, status);
         e = cudaGetLastError();
         if (e == cudaSuccess && grad) e = chunk_grads(w, W, r0, c, rows, d, V, g, sms, status, s);

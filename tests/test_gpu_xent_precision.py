@@ -62,6 +62,58 @@ def test_log_sums_of_exact_logits(d):
     _check_log_sums(2000, d, 300)
 
 
+def _confident(N, d, V, seed=1):
+    """Word 7's logit is between 15 and 60, all others are as far below 0: losses under 1e-11."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    sign = torch.where(torch.rand(d, device="cuda", generator=g) < 0.5, -1.0, 1.0)
+    size = 0.5 + torch.rand(N, d, device="cuda", generator=g)
+    x = (sign * size * torch.linspace(1, 3.5, N, device="cuda")[:, None]).to(BF)
+    W = (-sign * (0.5 + torch.rand(V, d, device="cuda", generator=g)) * (18.0 / d)).to(BF)
+    W[7] = -W[7]
+    return x, W, torch.full((N,), 7, device="cuda")
+
+
+@pytest.mark.parametrize("d", [8, 64, 1000, 1024, 4096])
+def test_confident_rows_have_no_loss_and_no_gradient(d):
+    """The target's logit and the log-sum cancel: a loss is not negative, and its error is that of a sum near 1, not that
+    of logits of 60."""
+    N, V = 256, 600
+    x, W, t = _confident(N, d, V)
+    z = x.double() @ W.double().T
+    assert 10 < float(z[:, 7].min()) and float(z[:, 7].max()) > 50
+    ref = torch.logsumexp(z, 1) - z[:, 7]
+    nll, _, loss = _losses(x, W, t)
+    assert bool((nll >= 0).all()) and float(loss) >= 0
+    assert bool(((nll.double() - ref).abs() <= E).all())
+    # the target's gradient expm1(-nll) is not positive: with one word left, dx = dz W has the sign of -W
+    dx, dW = torch.empty_like(x), torch.empty(V, d, device="cuda")
+    nll, lse, loss = torch.empty(N, device="cuda"), torch.empty(N, device="cuda"), torch.empty(1, device="cuda")
+    ws = torch.empty(tw.twell_xent_bwd_workspace_bytes(N, d, V, 0, tw.DTYPE_F32), dtype=torch.uint8, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tw.twell_xent_fwd_bwd(x, W, t, IGN, False, 1.0, 0, nll, lse, loss, dx, dW, False, ws, st)
+    assert tw.twell_check(st) == 0
+    assert bool((dx.float() * W[7].float() <= 1e-10).all())
+    assert bool((dx.float().abs() <= 1.01 * E * W[7].float().abs() + 1e-10).all())
+
+
+@pytest.mark.parametrize("V", [300, 5001])
+def test_losses_of_likely_targets(V):
+    """Losses between 1e-4 and 1 beside logits of 40: relative to 1, no digit is lost to the logits' size."""
+    N, d = 512, 64
+    x = torch.zeros(N, d, device="cuda", dtype=BF)
+    x[:, 0], x[:, 1] = 1.0, torch.linspace(0, 9, N, device="cuda").to(BF)
+    W = torch.zeros(V, d, device="cuda", dtype=BF)
+    W[:, 0] = 20.0
+    W[3, 0], W[V - 2, 0], W[V - 2, 1] = 40.0, 39.0, -1.0   # logits 40, 39 - x, and 20: exact in fp32
+    for word in (3, V - 2):
+        t = torch.full((N,), word, device="cuda")
+        z = x.double() @ W.double().T
+        ref = torch.logsumexp(z, 1) - z[:, word]
+        nll = _losses(x, W, t)[0].double()
+        # log2(e) times the logits' differences (1.4e-8 and two roundings, 2^-23 of them) and the sum near 1
+        assert bool(((nll - ref).abs() <= E + (2.0 ** -22 + 1.4e-8) * (1 + ref)).all())
+
+
 @pytest.mark.parametrize("d", [1024, 4096, 16384])
 def test_log_sums_of_exact_logits_of_wide_rows(d):
     """A product of one term is that term, whatever the width."""
