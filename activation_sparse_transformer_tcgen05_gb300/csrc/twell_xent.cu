@@ -304,11 +304,12 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (i < N) gather_row(x, d, w, ldx, i, perm[i], o.total, threadIdx.x & 31, nll, lse, dx);
 }
 
-// a + b rounded, and what the rounding lost.
+// a + b rounded, and what the rounding lost (operations that the compiler does not
+// join with others).
 __device__ __forceinline__ float two_sum(float a, float b, float* lost)
 {
-    const float s = a + b, bb = s - a;
-    *lost = (a - (s - bb)) + (b - bb);
+    const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
+    *lost = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
     return s;
 }
 
