@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kPrepThreads)
                        float* __restrict__ nll, float* __restrict__ lse, uint16_t* __restrict__ dx, int32_t* status)
 {
     __shared__ int perm[kFewRows];
+    const bool failed = has_error(status);  // asked for here, together with the targets; nothing is written then
     const bool first = blockIdx.x == 0;
     const Order o = order_rows(target, N, V, ignore_index, [&](int pos, int row, int t, bool scored) {
         perm[pos] = row;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kPrepThreads)
     if (first) publish_order(o, N, d, V, chunk, mean, grad_scale, w);
     __syncthreads();
     const int i = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
-    if (i < N) gather_row(x, d, w, ldx, i, perm[i], o.total, threadIdx.x & 31, nll, lse, dx);
+    if (i < N && !failed) gather_row(x, d, w, ldx, i, perm[i], o.total, threadIdx.x & 31, nll, lse, dx);
 }
 
 // a + b rounded, and what the rounding lost (operations that the compiler does not

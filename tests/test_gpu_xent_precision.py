@@ -134,3 +134,24 @@ def test_deep_sums_of_one_sign(d):
     rel = (lse.double() - z) / z
     assert float(rel.abs().max()) <= (16.5 + d / 512) * 2.0 ** -23
     assert abs(float(rel.mean())) <= 8.25 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("N", [100, 2048, 2049, 5000])
+@pytest.mark.parametrize("grad", [False, True])
+def test_nothing_is_written_after_an_error(N, grad):
+    """A status that an earlier kernel set: every later kernel skips its work, whatever the number of rows."""
+    d, V = 64, 300
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, W = torch.randn(N, d, device="cuda", generator=g).to(BF), torch.randn(V, d, device="cuda", generator=g).to(BF)
+    t = torch.randint(0, V, (N,), device="cuda", generator=g)
+    t[::3] = IGN
+    st = torch.full((1,), 4, dtype=torch.int32, device="cuda")
+    if not grad:
+        out = _losses(x, W, t, status=st)
+    else:
+        out = [torch.full((N,), 7.0, device="cuda"), torch.full((N,), 7.0, device="cuda"), torch.full((1,), 7.0, device="cuda"),
+               torch.full_like(x, 7.0), torch.full_like(W, 7.0)]
+        ws = torch.empty(tw.twell_xent_bwd_workspace_bytes(N, d, V, 0, tw.DTYPE_BF16), dtype=torch.uint8, device="cuda")
+        tw.twell_xent_fwd_bwd(x, W, t, IGN, True, 1.0, 0, *out, False, ws, st)
+    assert tw.twell_check(st) == 4
+    assert all(bool((o == 7.0).all()) for o in out)
