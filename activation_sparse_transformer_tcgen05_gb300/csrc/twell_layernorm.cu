@@ -819,10 +819,13 @@ int per_thread(int d) { return d <= 256 ? 8 : 16; }
 // Threads of a row: the fewest that hold it; 0 where kMaxGroup do not.
 int group_of(int d)
 {
-    int G = 32;
-    while (G * per_thread(d) < d) G *= 2;
-    return G <= kMaxGroup ? G : 0;
+    for (int G = 32; G <= kMaxGroup; G *= 2)
+        if (G * per_thread(d) >= d) return G;
+    return 0;
 }
+
+// Longest rows: twice as many column sums, and the threads past the last, still count in int.
+constexpr int kMaxWidth = 1 << 29;
 
 int rows_per_block(int G) { return G < 256 ? 256 / G : 1; }
 
@@ -971,6 +974,7 @@ extern "C" twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const vo
 {
     if (N < 0 || d < 1 || !type_ok(x_type) || !type_ok(y_type) || !type_ok(w_type) || !(eps >= 0.f))
         return TWELL_ERR_INVALID_ARG;
+    if (d > kMaxWidth) return TWELL_ERR_UNSUPPORTED;
     if (N == 0) return TWELL_OK;
     if (!x || !y || (res != nullptr) != (sum != nullptr) || ldx < d || ldy < d || (res && (ldres < d || ldsum < d)))
         return TWELL_ERR_INVALID_ARG;
@@ -997,7 +1001,7 @@ extern "C" twell_status twell_layernorm_fwd(const void* x, int64_t ldx, const vo
 
 extern "C" size_t twell_layernorm_bwd_workspace_bytes(int64_t N, int d)
 {
-    if (N < 0 || d < 1) return 0;
+    if (N < 0 || d < 1 || d > kMaxWidth) return 0;
     const size_t n = (size_t)parts_for(N, d) * 2 * d * sizeof(float);
     return n > 256 ? n : 256;
 }
@@ -1010,6 +1014,7 @@ extern "C" twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const 
 {
     if (N < 0 || d < 1 || !type_ok(x_type) || !type_ok(y_type) || !type_ok(w_type) || (dw != nullptr) != (db != nullptr))
         return TWELL_ERR_INVALID_ARG;
+    if (d > kMaxWidth) return TWELL_ERR_UNSUPPORTED;
     if (!elem_aligned(dw, TWELL_F32) || !elem_aligned(db, TWELL_F32)) return TWELL_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (N == 0) {

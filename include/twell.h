@@ -368,7 +368,8 @@ twell_status twell_ffn_fwd_static_ws(const uint16_t* x, const uint16_t* W_up, co
  * (ld*) in elements, >= d, of any alignment (rows that all start on 16-byte
  * boundaries are read in 16-byte pieces, others in pairs or single elements). x_type is the type of the residual stream
  * (x, res, sum, dres, dx), y_type that of y and dy, w_type that of w and b; each
- * TWELL_BF16 or TWELL_F32. w or b may be NULL (1 and 0). N >= 0, d >= 1.
+ * TWELL_BF16 or TWELL_F32. w or b may be NULL (1 and 0). N >= 0, d >= 1. Limit of
+ * this build: d <= 2^29 (TWELL_ERR_UNSUPPORTED).
  * Statistics and sums are fp32; outputs are rounded once. Outputs must not
  * overlap inputs (the call rejects equal pointers).
  *
