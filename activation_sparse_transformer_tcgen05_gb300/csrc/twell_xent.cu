@@ -510,6 +510,10 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 
 bool dims_ok(int N, int d, int V) { return N >= 0 && d > 0 && V > 0 && d % 8 == 0; }
 
+// Sizes rounded up to tiles and strides still count in int.
+constexpr int kMaxSize = 1 << 30;
+bool dims_fit(int N, int d, int V) { return N <= kMaxSize && d <= kMaxSize && V <= kMaxSize; }
+
 unsigned blocks_for(size_t work, size_t per_block, int sms)
 {
     const size_t b = (work + per_block - 1) / per_block, most = (size_t)sms * 16;
@@ -656,13 +660,13 @@ using namespace twell;
 
 extern "C" size_t twell_xent_fwd_workspace_bytes(int N, int d, int V)
 {
-    if (!dims_ok(N, d, V)) return 0;
+    if (!dims_ok(N, d, V) || !dims_fit(N, d, V)) return 0;
     return carve(nullptr, N, N, d, V, false, false, nullptr);
 }
 
 extern "C" size_t twell_xent_bwd_workspace_bytes(int N, int d, int V, int chunk_rows, int dw_type)
 {
-    if (!dims_ok(N, d, V) || chunk_rows < 0 || !type_ok(dw_type)) return 0;
+    if (!dims_ok(N, d, V) || !dims_fit(N, d, V) || chunk_rows < 0 || !type_ok(dw_type)) return 0;
     const int chunk = chunk_of(N, chunk_rows);
     return carve(nullptr, N, chunk, d, V, true, dw_type == TWELL_BF16 && chunk < N, nullptr);
 }
@@ -673,6 +677,7 @@ extern "C" twell_status twell_xent_fwd(const uint16_t* x, const uint16_t* W, con
 {
     if (!dims_ok(N, d, V) || !W || !loss || !status || (N > 0 && (!x || !target || !nll || !lse)))
         return TWELL_ERR_INVALID_ARG;
+    if (!dims_fit(N, d, V)) return TWELL_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(target, 8)) return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_xent_fwd_workspace_bytes(N, d, V)) return TWELL_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return TWELL_ERR_INVALID_ARG;
@@ -690,6 +695,7 @@ extern "C" twell_status twell_xent_fwd_bwd(const uint16_t* x, const uint16_t* W,
         return TWELL_ERR_INVALID_ARG;
     if (!W || !loss || !status || !dW || (N > 0 && (!x || !target || !nll || !lse || !dx)))
         return TWELL_ERR_INVALID_ARG;
+    if (!dims_fit(N, d, V)) return TWELL_ERR_UNSUPPORTED;
     if (!aligned(x, 16) || !aligned(W, 16) || !aligned(target, 8) || !aligned(dx, 16) || !aligned(dW, 16))
         return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_xent_bwd_workspace_bytes(N, d, V, chunk_rows, dw_type)) return TWELL_ERR_WORKSPACE;

@@ -408,7 +408,8 @@ twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
  * zero gradients. A target outside [0, V) that is not ignore_index sets
  * *status = TWELL_ERR_INVALID_ARG and the outputs are then unspecified.
  *   x [N, d] bf16, W [V, d] bf16 (one row per word), target [N] int64;
- *   nll, lse [N] fp32, loss [1] fp32. N >= 0, V >= 1, d % 8 == 0.
+ *   nll, lse [N] fp32, loss [1] fp32. N >= 0, V >= 1, d % 8 == 0. Limit of this
+ *   build: N, d, V <= 2^30 (TWELL_ERR_UNSUPPORTED).
  * The logits are never stored: twell_xent_fwd keeps a maximum and a sum for
  * every (row, 128 words), and the scored rows of x copied together.
  *
