@@ -26,7 +26,8 @@
 //   GEMM_XENT        A = hidden rows, B = the head's rows (one per word), CTA
 //                    pairs only: per (row, 128 words) the logits' maximum and
 //                    sum of exponentials, and 16-bit codes of the logits; the
-//                    logits themselves are never written.
+//                    logits themselves are never written. Deep logits are summed
+//                    in pieces of kSumBlocks k-blocks, joined by the epilogue.
 //
 // Warp roles (192 threads, one CTA per SM, persistent over tiles):
 //   warp 0     TMA producer: 128-byte-swizzled A/B tiles into a STAGES-deep ring

@@ -410,6 +410,8 @@ twell_status twell_layernorm_bwd(const void* dy, int64_t lddy, const void* x, in
  *   x [N, d] bf16, W [V, d] bf16 (one row per word), target [N] int64;
  *   nll, lse [N] fp32, loss [1] fp32. N >= 0, V >= 1, d % 8 == 0. Limit of this
  *   build: N, d, V <= 2^30 (TWELL_ERR_UNSUPPORTED).
+ * A logit is an fp32 sum: the tensor cores', which drop what does not fit towards
+ * zero, over 512 of d at a time, joined with rounding.
  * The logits are never stored: twell_xent_fwd keeps a maximum and a sum for
  * every (row, 128 words), and the scored rows of x copied together.
  *
