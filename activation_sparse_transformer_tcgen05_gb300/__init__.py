@@ -16,7 +16,9 @@ from .twell import (TwellBuffers, TwellOverflow, TwellError, load_library, twell
                     OP_FFN_FWD, OP_FFN_BWD, OP_GATED_FWD, EXPORTED_SYMBOLS, DTYPE_BF16, DTYPE_F32, TwellTensorList,
                     twell_layernorm_fwd, twell_layernorm_bwd, twell_layernorm_bwd_workspace_bytes, twell_xent_fwd,
                     twell_xent_fwd_bwd, twell_xent_fwd_workspace_bytes, twell_xent_bwd_workspace_bytes,
-                    twell_grad_clip, twell_grad_clip_workspace_bytes)
+                    twell_grad_clip, twell_grad_clip_workspace_bytes, ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH,
+                    twell_linear_fwd, twell_linear_bwd, twell_linear_bwd_workspace_bytes, twell_dense_gated_ffn_fwd,
+                    twell_dense_gated_ffn_bwd, twell_dense_gated_bwd_workspace_bytes)
 
 __all__ = [
     "TwellBuffers", "TwellOverflow", "TwellError", "load_library", "twell_buf_slots_bound", "twell_check",
@@ -29,4 +31,7 @@ __all__ = [
     "DTYPE_BF16", "DTYPE_F32", "TwellTensorList", "twell_layernorm_fwd", "twell_layernorm_bwd",
     "twell_layernorm_bwd_workspace_bytes", "twell_xent_fwd", "twell_xent_fwd_bwd", "twell_xent_fwd_workspace_bytes",
     "twell_xent_bwd_workspace_bytes", "twell_grad_clip", "twell_grad_clip_workspace_bytes",
+    "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "twell_linear_fwd", "twell_linear_bwd",
+    "twell_linear_bwd_workspace_bytes", "twell_dense_gated_ffn_fwd", "twell_dense_gated_ffn_bwd",
+    "twell_dense_gated_bwd_workspace_bytes",
 ]

@@ -1,0 +1,232 @@
+// twell_linear.cu — linear layer with bias, activation and residual, and its backward.
+//
+//   pre = x W^T + bias, y = act(pre) + res
+//   dpre = dy act'(pre);  dx = dpre W,  dW = dpre^T x,  dbias = column sums of dpre
+//
+// The products are twell_mm.cu's; W is read as it lies, [N, K] or [K, N], in all three.
+// k_linear_dpre forms dpre once for both gradients, rounded to bf16 as the tensor cores'
+// operand (dbias is summed from the fp32 values); without an activation dy itself is the
+// operand, unless its rows do not start on 16-byte boundaries, and this pass only sums.
+#include "activation.cuh"
+#include "common.cuh"
+#include "launch.h"
+#include "mm.h"
+
+namespace twell {
+namespace {
+
+int sms_current()
+{
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) !=
+                                                  cudaSuccess)
+        return 0;
+    return n;
+}
+
+bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+
+constexpr int kMostDim = 1 << 30;
+constexpr int kDpreThreads = 128;
+
+size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
+int64_t padded(int n) { return ((int64_t)n + 63) / 64 * 64; }
+
+// kSumRows rows x (threads * V) columns a block: dpre = dy act'(pre) (pre null: dy) to out, if there is one, and the
+// rows' sums in fp32 to part, if there is one. V = 8: rows of dy, pre and out in 16-byte pieces.
+template <int V>
+__global__ void __launch_bounds__(kDpreThreads)
+    k_linear_dpre(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ pre, int64_t ldpre, int M, int N,
+                  int act, uint16_t* __restrict__ out, int64_t ldout, float* __restrict__ part,
+                  const int32_t* __restrict__ status)
+{
+    if (has_error(status)) return;
+    const int c = ((int)blockIdx.y * kDpreThreads + (int)threadIdx.x) * V, r0 = (int)blockIdx.x * kSumRows;
+    if (c >= N) return;
+    float sum[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    const int rows = min(kSumRows, M - r0);
+    by_activation(pre ? act : TWELL_ACT_NONE, [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+            const size_t row = (size_t)r0 + r;
+            float d[V];
+            if constexpr (V == 8) {
+                const uint4 q = *reinterpret_cast<const uint4*>(dy + row * lddy + c);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                uint32_t z[4] = {0, 0, 0, 0};
+                if (ACT != TWELL_ACT_NONE) {
+                    const uint4 p = *reinterpret_cast<const uint4*>(pre + row * ldpre + c);
+                    z[0] = p.x, z[1] = p.y, z[2] = p.z, z[3] = p.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+                    if (ACT != TWELL_ACT_NONE) {
+                        float da;
+                        activate<ACT>((e & 1) ? bf16_hi(z[e >> 1]) : bf16_lo(z[e >> 1]), &da);
+                        d[e] *= da;
+                    }
+                }
+                if (out)
+                    *reinterpret_cast<uint4*>(out + row * ldout + c) =
+                        make_uint4(cvt_bf16x2(d[0], d[1]), cvt_bf16x2(d[2], d[3]), cvt_bf16x2(d[4], d[5]),
+                                   cvt_bf16x2(d[6], d[7]));
+            } else {
+                d[0] = bf16_to_f32(dy[row * lddy + c]);
+                if (ACT != TWELL_ACT_NONE) {
+                    float da;
+                    activate<ACT>(bf16_to_f32(pre[row * ldpre + c]), &da);
+                    d[0] *= da;
+                }
+                if (out) out[row * ldout + c] = f32_to_bf16_bits(d[0]);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] += d[e];
+        }
+    });
+    if (part) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[(size_t)blockIdx.x * N + c + e] = sum[e];
+    }
+}
+
+bool act_ok(int act) { return act >= TWELL_ACT_NONE && act <= TWELL_ACT_GELU_TANH; }
+
+bool dims_ok(int M, int N, int K, int w_kn)
+{
+    return M >= 0 && N > 0 && K > 0 && K % 8 == 0 && (w_kn == 0 || (w_kn == 1 && N % 8 == 0));
+}
+bool dims_fit(int M, int N, int K) { return M <= kMostDim && N <= kMostDim && K <= kMostDim; }
+
+// Rows of bf16 that the tensor cores' loads can start on.
+bool operand_ok(const void* p, int64_t ld, int width) { return p && aligned(p, 16) && ld >= width && ld % 8 == 0 && ld <= kMostDim; }
+
+}  // namespace
+}  // namespace twell
+
+using namespace twell;
+
+extern "C" twell_status twell_linear_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int w_kn, const float* bias,
+                                         int act, const void* res, int64_t ldres, int M, int N, int K, uint16_t* pre,
+                                         int64_t ldpre, void* y, int64_t ldy, int y_type, int32_t* status, void* stream)
+{
+    if (!dims_ok(M, N, K, w_kn) || !act_ok(act) || (y_type != TWELL_BF16 && y_type != TWELL_F32)) return TWELL_ERR_INVALID_ARG;
+    if (!dims_fit(M, N, K)) return TWELL_ERR_UNSUPPORTED;
+    if (M == 0) return TWELL_OK;
+    const size_t es = y_type == TWELL_F32 ? 4 : 2;
+    if (!operand_ok(x, ldx, K) || !operand_ok(W, w_kn ? N : K, 1) || !y || !status || !aligned(y, es) || ldy < N ||
+        !aligned(bias, 4) || !aligned(status, 4))
+        return TWELL_ERR_INVALID_ARG;
+    if ((res && (ldres < N || !aligned(res, es))) || (pre && (ldpre < N || !aligned(pre, 2)))) return TWELL_ERR_INVALID_ARG;
+    if (y == x || y == W || pre == x || pre == W || (pre && (y == pre || res == pre))) return TWELL_ERR_INVALID_ARG;
+    const int sms = sms_current();
+    if (sms <= 0) return TWELL_ERR_CUDA;
+    MmLinear m{};
+    m.M = M;
+    m.N = N;
+    m.K = K;
+    m.segments = m.problems = 1;
+    m.a[0] = {x, ldx, false};
+    m.b[0] = {W, w_kn ? N : K, w_kn != 0};
+    m.bias = bias;
+    m.act = act;
+    m.res = res;
+    m.ldres = ldres;
+    m.pre = pre;
+    m.ldpre = ldpre;
+    m.out[0] = y;
+    m.ldo = ldy;
+    m.out_f32 = y_type == TWELL_F32;
+    m.status = status;
+    return launch_mm_linear(m, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}
+
+extern "C" size_t twell_linear_bwd_workspace_bytes(int M, int N, int K)
+{
+    if (!dims_ok(M, N, K, 0) || !dims_fit(M, N, K)) return 0;
+    return round256((size_t)M * padded(N) * 2) + round256(((size_t)M + kSumRows - 1) / kSumRows * N * 4) + 256;
+}
+
+extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* W,
+                                         int w_kn, int act, const uint16_t* pre, int64_t ldpre, int M, int N, int K,
+                                         uint16_t* dx, int64_t lddx, void* dW, int dw_type, int accumulate, float* dbias,
+                                         void* ws, size_t ws_bytes, int32_t* status, void* stream)
+{
+    if (!dims_ok(M, N, K, w_kn) || !act_ok(act) || (dw_type != TWELL_BF16 && dw_type != TWELL_F32) ||
+        (accumulate && dw_type != TWELL_F32) || (!dx && !dW && !dbias))
+        return TWELL_ERR_INVALID_ARG;
+    if (!dims_fit(M, N, K)) return TWELL_ERR_UNSUPPORTED;
+    if (!status || !aligned(status, 4) || !aligned(dW, 16) || !aligned(dbias, 4)) return TWELL_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (M == 0) {
+        cudaError_t e = cudaSuccess;
+        if (dW && !accumulate) e = cudaMemsetAsync(dW, 0, (size_t)N * K * (dw_type == TWELL_F32 ? 4 : 2), s);
+        if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, (size_t)N * 4, s);
+        return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+    }
+    if (!dy || lddy < N || !aligned(dy, 2) || (dW && !operand_ok(x, ldx, K)) || (dx && !operand_ok(W, w_kn ? N : K, 1)) ||
+        (dx && (lddx < K || !aligned(dx, 2))))
+        return TWELL_ERR_INVALID_ARG;
+    if (act != TWELL_ACT_NONE && (!pre || ldpre < N || !aligned(pre, 2))) return TWELL_ERR_INVALID_ARG;
+    if ((dx && (dx == dy || dx == x || dx == W || dx == pre)) || (dW && (dW == dy || dW == x || dW == W || dW == pre || dW == dx)))
+        return TWELL_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < twell_linear_bwd_workspace_bytes(M, N, K)) return TWELL_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return TWELL_ERR_INVALID_ARG;
+    const int sms = sms_current();
+    if (sms <= 0) return TWELL_ERR_CUDA;
+
+    if (act == TWELL_ACT_NONE) pre = nullptr;
+    uint16_t* own = static_cast<uint16_t*>(ws);
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + round256((size_t)M * padded(N) * 2));
+    MmOperand dpre{dy, lddy, false};
+    const bool form = (dx || dW) && (pre || !operand_ok(dy, lddy, N));
+    if (form) dpre = {own, padded(N), false};
+    const int blocks = (M + kSumRows - 1) / kSumRows;
+    cudaError_t e = cudaSuccess;
+    if (form || dbias) {
+        const bool vec = N % 8 == 0 && operand_ok(dy, lddy, N) && (!pre || operand_ok(pre, ldpre, N));
+        const int v = vec ? 8 : 1;
+        const int64_t cols = ((int64_t)N + kDpreThreads * v - 1) / (kDpreThreads * v);
+        if (cols > 65535) return TWELL_ERR_UNSUPPORTED;
+        const dim3 grid((unsigned)blocks, (unsigned)cols);
+        count_launches(1);
+        auto kern = vec ? k_linear_dpre<8> : k_linear_dpre<1>;
+        kern<<<grid, kDpreThreads, 0, s>>>(dy, lddy, pre, ldpre, M, N, act, form ? own : nullptr, padded(N),
+                                           dbias ? part : nullptr, status);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && dbias) e = launch_block_sums(part, blocks, N, dbias, status, s);
+    }
+    if (e == cudaSuccess && dx) {
+        MmLinear m{};
+        m.M = M;
+        m.N = K;
+        m.K = N;
+        m.segments = m.problems = 1;
+        m.a[0] = dpre;
+        m.b[0] = {W, w_kn ? N : K, w_kn == 0};  // [K, N]: K-major for this product
+        m.out[0] = dx;
+        m.ldo = lddx;
+        m.status = status;
+        e = launch_mm_linear(m, sms, s);
+    }
+    if (e == cudaSuccess && dW) {
+        MmLinear m{};
+        m.M = w_kn ? K : N;
+        m.N = w_kn ? N : K;
+        m.K = M;
+        m.segments = m.problems = 1;
+        const MmOperand rows{dpre.p, dpre.ld, true}, cols{x, ldx, true};
+        m.a[0] = w_kn ? cols : rows;
+        m.b[0] = w_kn ? rows : cols;
+        m.out[0] = dW;
+        m.ldo = m.N;
+        m.out_f32 = dw_type == TWELL_F32;
+        m.accumulate = accumulate != 0;
+        m.status = status;
+        e = launch_mm_linear(m, sms, s);
+    }
+    return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
+}

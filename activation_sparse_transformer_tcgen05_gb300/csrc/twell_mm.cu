@@ -1,0 +1,824 @@
+// twell_mm.cu — dense products with the linear and gated layers' epilogues.
+//
+// D = A B^T on CTA pairs (tcgen05.mma.cta_group::2, 256 x 256 tiles), bf16 operands
+// by TMA, fp32 accumulators in tensor memory, two of them so that a tile's epilogue
+// runs under the next tile's products. Bound by the tensor cores for hundreds of
+// rows and more.
+//
+//   LINEAR     act(D + bias) + res in bf16 or fp32, the pre-activation kept on demand.
+//              Several products can be added up (segments: the gated layer's
+//              dx = dg Wg + du Wu, one accumulator for both), or several of the same sizes
+//              computed side by side (problems: dWg, dWu, dWd), so that only one launch
+//              ends with partly filled waves of tiles.
+//   GATED      one CTA of the pair brings 128 rows of W_gate, the other 128 of W_up:
+//              a tile's accumulator holds g in its first and u in its last 128 columns,
+//              so the same thread has both, and neither has to be written for h.
+//   GATED_BWD  D = dh; with g and u, dg and du are formed while the next tile is
+//              computed; dh itself is never written.
+//
+// Roles as in twell_gemm.cu: warp 0 loads, warp 1 (even CTA) issues the products, eight
+// warps form the results of 32 rows x 128 columns each and store them through 4 KB of
+// their own shared memory, whole 128-byte pieces of rows at a time.
+#include "activation.cuh"
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "launch.h"
+#include "mm.h"
+
+namespace twell {
+namespace {
+
+enum Epilogue { LINEAR, GATED, GATED_BWD };
+
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kBox = 4096;  // 32 rows x 128 bytes of one epilogue warp
+
+struct Smem {
+    static constexpr int A_BYTES = HALF * BK * 2;
+    static constexpr int STAGE_BYTES = 2 * A_BYTES;
+    static constexpr int BOX_OFF = kStages * STAGE_BYTES;
+    static constexpr int BAR_OFF = BOX_OFF + kEpiWarps * kBox;
+    static constexpr int NBARS = 2 * kStages + 5;
+    static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int TOTAL = MISC_OFF + 16 + 1024;  // + alignment slack
+    static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
+};
+
+// The tensor cores' fp32 sums drop what does not fit, towards zero, at each step of 16 of depth: over 1024
+// by 7 units of 2^-23 of the result, over 4096 by 31 to 70, over 16384 four times that. Results that leave in fp32
+// are therefore summed 1024 at a time and the pieces added up with rounding; for bf16 the loss is a hundredth of
+// the result's own rounding and the tensor cores sum the whole depth.
+constexpr int kPieceBlocks = 16;
+
+struct Maps {
+    CUtensorMap a[kMmParts], b[kMmParts];
+};
+
+struct Args {
+    int rowsA, rowsB, num_kb;  // output rows and columns, 64-deep k-blocks of one segment
+    int segments, problems;
+    int piece;                 // k-blocks that the tensor cores sum by themselves
+    const float* bias;
+    int act;
+    const void* res;
+    int64_t ldres;
+    uint16_t* pre;
+    int64_t ldpre;
+    void* out[kMmParts];
+    int64_t ldo;
+    int out_f32;
+    int accumulate;
+    int vec;                   // bits: out, res, pre have 16-byte pieces (base, row stride and width allow them)
+    // gated
+    uint16_t *g, *u, *h;
+    const uint16_t *g_in, *u_in;
+    float l1;
+    float* part;
+    int32_t* status;
+};
+enum { VEC_OUT = 1, VEC_RES = 2, VEC_PRE = 4 };
+
+__device__ __forceinline__ void fail(int32_t* status, volatile int* abort_flag)
+{
+    set_error(status, TWELL_ERR_TIMEOUT);
+    *abort_flag = 1;
+}
+
+// 32 rows of 128 bytes between a warp's accumulator rows (lane = row) and global memory, where eight lanes share
+// a row. 16-byte pieces are permuted within a row so that both sides touch different banks.
+struct Box {
+    uint8_t* box;
+    int lane;
+    __device__ __forceinline__ uint4* at(int row, int c) const
+    {
+        return reinterpret_cast<uint4*>(box + row * 128 + ((c ^ (row & 7)) << 4));
+    }
+    __device__ __forceinline__ void put(int c, const uint4& v) { *at(lane, c) = v; }
+    __device__ __forceinline__ uint4 get(int c) const { return *at(lane, c); }
+
+    // The box's first `rows` rows and `cols` columns (elements of ES bytes) to rows of `stride` bytes at `to`.
+    template <int ES>
+    __device__ __forceinline__ void store(void* to, size_t stride, int rows, int cols, bool vec)
+    {
+        constexpr int E = 16 / ES;
+        __syncwarp();
+        const int c = lane & 7, r0 = lane >> 3;
+        char* p = static_cast<char*>(to) + r0 * stride + c * 16;
+        if (vec) {
+            if (c * E < cols) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (i * 4 + r0 < rows) *reinterpret_cast<uint4*>(p) = *at(i * 4 + r0, c);
+                    p += 4 * stride;
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const uint4 q = *at(i * 4 + r0, c);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                if (i * 4 + r0 < rows) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (c * E + e < cols) {
+                            if constexpr (ES == 4)
+                                reinterpret_cast<uint32_t*>(p)[e] = w[e];
+                            else
+                                reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e >> 1] >> ((e & 1) * 16));
+                        }
+                }
+                p += 4 * stride;
+            }
+        }
+        __syncwarp();
+    }
+
+    // The same way back; what lies outside is 0.
+    template <int ES>
+    __device__ __forceinline__ void load(const void* from, size_t stride, int rows, int cols, bool vec)
+    {
+        constexpr int E = 16 / ES;
+        const int c = lane & 7, r0 = lane >> 3;
+        const char* p = static_cast<const char*>(from) + r0 * stride + c * 16;
+        if (vec) {
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                q[i] = make_uint4(0, 0, 0, 0);
+                if (i * 4 + r0 < rows && c * E < cols) q[i] = *reinterpret_cast<const uint4*>(p);
+                p += 4 * stride;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) *at(i * 4 + r0, c) = q[i];
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (i * 4 + r0 < rows) {
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (c * E + e < cols) {
+                            if constexpr (ES == 4)
+                                w[e] = reinterpret_cast<const uint32_t*>(p)[e];
+                            else
+                                w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[e] << ((e & 1) * 16);
+                        }
+                }
+                *at(i * 4 + r0, c) = make_uint4(w[0], w[1], w[2], w[3]);
+                p += 4 * stride;
+            }
+        }
+        __syncwarp();
+    }
+
+    // N values of the lane's row as bf16 in the pieces from c0 on.
+    template <int N>
+    __device__ __forceinline__ void put_bf16(const float (&v)[N], int c0 = 0)
+    {
+#pragma unroll
+        for (int c = 0; c < N / 8; ++c) put(c0 + c, pack8(v + c * 8));
+    }
+    static __device__ __forceinline__ uint4 pack8(const float* v)
+    {
+        return make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7]));
+    }
+
+    // Two bf16 matrices of one layout side by side: 32 columns of the first in pieces 0 to 3, of the second in 4 to
+    // 7. `at` is the element of row 0 and column 0, rows have `ld` elements and 16-byte pieces.
+    __device__ __forceinline__ void load_two(const uint16_t* m0, const uint16_t* m1, size_t at, int64_t ld, int rows, int cols)
+    {
+        const int c = lane & 3, r0 = lane >> 2;
+        uint4 q[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool ok = c * 8 < cols && i * 8 + r0 < rows;
+            const size_t o = at + (size_t)(i * 8 + r0) * ld + c * 8;
+            q[i] = ok ? *reinterpret_cast<const uint4*>(m0 + o) : make_uint4(0, 0, 0, 0);
+            q[4 + i] = ok ? *reinterpret_cast<const uint4*>(m1 + o) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            *this->at(i * 8 + r0, c) = q[i];
+            *this->at(i * 8 + r0, 4 + c) = q[4 + i];
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void store_two(uint16_t* m0, uint16_t* m1, size_t at, int64_t ld, int rows, int cols)
+    {
+        __syncwarp();
+        const int c = lane & 3, r0 = lane >> 2;
+        if (c * 8 < cols) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i * 8 + r0 < rows) {
+                    const size_t o = at + (size_t)(i * 8 + r0) * ld + c * 8;
+                    *reinterpret_cast<uint4*>(m0 + o) = *this->at(i * 8 + r0, c);
+                    *reinterpret_cast<uint4*>(m1 + o) = *this->at(i * 8 + r0, 4 + c);
+                }
+            }
+        }
+        __syncwarp();
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[N])
+{
+#pragma unroll
+    for (int ch = 0; ch < N / 32; ++ch) {
+        uint32_t r[32];
+        tmem_ld32_wait(taddr + ch * 32, r);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[ch * 32 + c] = __uint_as_float(r[c]);
+    }
+}
+
+// bias[col .. col + N - 1] (0 past `cols` of them, or without a bias) added to v, by way of the lanes' registers.
+template <int N>
+__device__ __forceinline__ void add_bias(const float* bias, int col, int cols, int lane, float (&v)[N])
+{
+    if (!bias) return;
+#pragma unroll
+    for (int ch = 0; ch < N / 32; ++ch) {
+        const float b = ch * 32 + lane < cols ? bias[col + ch * 32 + lane] : 0.f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[ch * 32 + c] += __shfl_sync(0xffffffffu, b, c);
+    }
+}
+
+// 32 rows x 128 columns from col0 on: bias, activation, residual.
+__device__ __forceinline__ void epi_linear(uint32_t taddr, int row0, int col0, int problem, const Args& a, Box& box)
+{
+    const int rows = a.rowsA - row0;
+#pragma unroll 1
+    for (int ch = 0; ch < 2; ++ch) {
+        const int col = col0 + ch * 64, cols = a.rowsB - col;
+        if (cols <= 0) break;
+        float v[64];
+        read_columns(taddr + ch * 64, v);
+        add_bias(a.bias, col, cols, box.lane, v);
+        if (a.pre) {
+            box.put_bf16(v);
+            box.store<2>(a.pre + (size_t)row0 * a.ldpre + col, (size_t)a.ldpre * 2, rows, cols, a.vec & VEC_PRE);
+        }
+        if (a.act != TWELL_ACT_NONE)
+            by_activation(a.act, [&](auto tag) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c) v[c] = activate<decltype(tag)::value>(v[c]);
+            });
+        if (a.out_f32) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (half * 32 >= cols) break;
+                if (a.res || a.accumulate) {
+                    // (an element of out is read and written by the same lane)
+                    const float* from = static_cast<const float*>(a.accumulate ? a.out[problem] : a.res);
+                    const int64_t ld = a.accumulate ? a.ldo : a.ldres;
+                    box.load<4>(from + (size_t)row0 * ld + col + half * 32, (size_t)ld * 4, rows, cols - half * 32,
+                                a.vec & (a.accumulate ? VEC_OUT : VEC_RES));
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint4 q = box.get(c);
+                        float* w = v + half * 32 + c * 4;
+                        w[0] += __uint_as_float(q.x);
+                        w[1] += __uint_as_float(q.y);
+                        w[2] += __uint_as_float(q.z);
+                        w[3] += __uint_as_float(q.w);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float* w = v + half * 32 + c * 4;
+                    box.put(c, make_uint4(__float_as_uint(w[0]), __float_as_uint(w[1]), __float_as_uint(w[2]),
+                                          __float_as_uint(w[3])));
+                }
+                box.store<4>(static_cast<float*>(a.out[problem]) + (size_t)row0 * a.ldo + col + half * 32, (size_t)a.ldo * 4, rows,
+                             cols - half * 32, a.vec & VEC_OUT);
+            }
+        } else {
+            if (a.res) {
+                box.load<2>(static_cast<const uint16_t*>(a.res) + (size_t)row0 * a.ldres + col, (size_t)a.ldres * 2, rows, cols,
+                            a.vec & VEC_RES);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const uint4 q = box.get(c);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[c * 8 + 2 * e] += bf16_lo(w[e]);
+                        v[c * 8 + 2 * e + 1] += bf16_hi(w[e]);
+                    }
+                }
+            }
+            box.put_bf16(v);
+            box.store<2>(static_cast<uint16_t*>(a.out[problem]) + (size_t)row0 * a.ldo + col, (size_t)a.ldo * 2, rows, cols,
+                         a.vec & VEC_OUT);
+        }
+    }
+}
+
+// 32 rows x 64 hidden units from col on; g at taddr, u 128 columns further.
+__device__ __forceinline__ void epi_gated(uint32_t taddr, int row0, int col, const Args& a, Box& box)
+{
+    const int rows = a.rowsA - row0, cols = a.rowsB - col;
+    uint4 h[8];
+#pragma unroll
+    for (int ch = 0; ch < 2; ++ch) {
+        float g[32], u[32];
+        read_columns(taddr + ch * 32, g);
+        add_bias(a.bias, col + ch * 32, cols - ch * 32, box.lane, g);
+        read_columns(taddr + HALF + ch * 32, u);
+        if (a.g) {
+            box.put_bf16(g);
+            box.put_bf16(u, 4);
+            box.store_two(a.g, a.u, (size_t)row0 * a.ldo + col + ch * 32, a.ldo, rows, cols - ch * 32);
+        }
+        by_activation(a.act, [&](auto tag) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) g[c] = activate<decltype(tag)::value>(g[c]) * u[c];
+        });
+#pragma unroll
+        for (int c = 0; c < 4; ++c) h[ch * 4 + c] = Box::pack8(g + c * 8);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) box.put(c, h[c]);
+    box.store<2>(a.h + (size_t)row0 * a.ldo + col, (size_t)a.ldo * 2, rows, cols, true);
+}
+
+// 32 rows x 128 hidden units from col0 on of dh. Rows and columns outside have g = u = 0 and dh = 0, so dg = du = 0.
+__device__ __forceinline__ void epi_gated_bwd(uint32_t taddr, int row0, int col0, const Args& a, Box& box)
+{
+    const int rows = a.rowsA - row0;
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        const int col = col0 + ch * 32, cols = a.rowsB - col;
+        if (cols <= 0) break;
+        const size_t at = (size_t)row0 * a.ldo + col;
+        box.load_two(a.g_in, a.u_in, at, a.ldo, rows, cols);
+        float dg[32], du[32];
+        read_columns(taddr + ch * 32, du);
+        by_activation(a.act, [&](auto tag) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint4 qg = box.get(c), qu = box.get(4 + c);
+                const uint32_t wg[4] = {qg.x, qg.y, qg.z, qg.w}, wu[4] = {qu.x, qu.y, qu.z, qu.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float g = (e & 1) ? bf16_hi(wg[e >> 1]) : bf16_lo(wg[e >> 1]);
+                    const float u = (e & 1) ? bf16_hi(wu[e >> 1]) : bf16_lo(wu[e >> 1]);
+                    float da;
+                    const float act = activate<decltype(tag)::value>(g, &da);
+                    float dh = du[c * 8 + e];
+                    if (a.l1 != 0.f && act != 0.f && u != 0.f) dh += (act > 0.f) == (u > 0.f) ? a.l1 : -a.l1;
+                    dg[c * 8 + e] = dh * u * da;
+                    du[c * 8 + e] = dh * act;
+                }
+            }
+        });
+        // rounded to bf16 once, as operands of the products that follow; the bias's gradient is summed before that
+        box.put_bf16(dg);
+        box.put_bf16(du, 4);
+        box.store_two(a.g, a.u, at, a.ldo, rows, cols);
+        if (a.part) {
+            transpose_reduce32(dg, box.lane);  // lane u: column u over the 32 rows
+            if (box.lane < cols) a.part[(size_t)(row0 / kSumRows) * a.rowsB + col + box.lane] = dg[0];
+        }
+    }
+}
+
+// 128 accumulator columns of a thread's row added to sum; or sum put in their place.
+__device__ __forceinline__ void add_columns(uint32_t taddr, float (&sum)[128])
+{
+#pragma unroll
+    for (int ch = 0; ch < 8; ++ch) {
+        uint32_t v[16];
+        tmem_ld16_wait(taddr + ch * 16, v);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) sum[ch * 16 + c] += __uint_as_float(v[c]);
+    }
+}
+__device__ __forceinline__ void set_columns(uint32_t taddr, const float (&sum)[128])
+{
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        uint32_t v[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[ch * 32 + c]);
+        tmem_st32(taddr + ch * 32, v);
+    }
+    tmem_st_wait();
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a)
+{
+    using L = Smem;
+    constexpr uint32_t IDESC =
+        idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
+    constexpr uint64_t A_KSTEP = A_MN ? (16u * 128u) >> 4 : 2u;  // descriptor units (16 B) per 16-deep K step
+    constexpr uint64_t B_KSTEP = B_MN ? (16u * 128u) >> 4 : 2u;
+    constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;  // output columns of a tile
+    extern __shared__ uint8_t smem_raw[];
+    // Same offset in both CTAs: the pair's products address the peer's operands with the leader's descriptors.
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile int* skip = reinterpret_cast<volatile int*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        *skip = (leader && has_error(a.status)) ? 1 : 0;
+        *abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(mma_done, 1);
+        fence_mbar_init();
+    }
+    cluster_sync();  // barriers of both CTAs initialised before either uses the other's
+    const int sk = ld_cluster_s32(cluster_addr(const_cast<int*>(skip), 0));
+    cluster_sync();  // the leader's flag has been read before anyone may leave
+    if (sk) return;  // an earlier kernel of this call failed; uniform over the pair
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 2 * PAIR_N);
+        tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {
+        for (int i = 0; i < a.segments * a.problems; ++i) {
+            tma_prefetch_map(&maps.a[i]);
+            tma_prefetch_map(&maps.b[i]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int num_m = (a.rowsA + PAIR_M - 1) / PAIR_M;
+    const int num_n = (a.rowsB + TILE_N - 1) / TILE_N;
+    const int mn_tiles = num_m * num_n;
+    const int num_tiles = mn_tiles * a.problems;
+    const int depth = a.num_kb * a.segments;
+    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer ----
+        if (lane == 0) {
+            const uint32_t full_leader = cluster_addr(full, 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            long long issued = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+                int mb, nb;
+                const int problem = tile / mn_tiles;
+                pair_tile_coords(tile - problem * mn_tiles, num_m, num_n, &mb, &nb);
+                const int ma = mb * PAIR_M + (int)rank * HALF;
+                // GATED: 128 rows of W_gate in the even CTA, the same rows of W_up in the odd one
+                const int nbr = EPI == GATED ? nb * HALF : nb * PAIR_N + (int)rank * HALF;
+                for (int seg = 0; ok && seg < a.segments; ++seg) {
+                    const CUtensorMap* ta = &maps.a[problem + seg];
+                    const CUtensorMap* tb = &maps.b[EPI == GATED ? (int)rank : problem + seg];
+                    for (int kb = 0; kb < a.num_kb; ++kb) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* sa = smem + stage * L::STAGE_BYTES;
+                        if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_BYTES);
+                        const uint32_t fb = full_leader + 8u * (uint32_t)stage;
+                        if (A_MN) {
+                            tma_load_2d_pair(sa, ta, ma, kb * BK, fb);
+                            tma_load_2d_pair(sa + kMnBox * BK * 2, ta, ma + kMnBox, kb * BK, fb);
+                        } else {
+                            tma_load_2d_pair(sa, ta, kb * BK, ma, fb);
+                        }
+                        if (B_MN) {
+                            tma_load_2d_pair(sa + L::A_BYTES, tb, nbr, kb * BK, fb);
+                            tma_load_2d_pair(sa + L::A_BYTES + kMnBox * BK * 2, tb, nbr + kMnBox, kb * BK, fb);
+                        } else {
+                            tma_load_2d_pair(sa + L::A_BYTES, tb, kb * BK, nbr, fb);
+                        }
+                        ++issued;
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            if (!ok) fail(a.status, abort_flag);
+            // The last load issued into each stage must land before the CTA exits: the leader sees it on its full
+            // barrier, the peer on its empty barrier (the leader's products consumed it).
+            for (int s = 0; s < kStages; ++s) {
+                const long long n_s = issued / kStages + (s < issued % kStages ? 1 : 0);
+                if (n_s > 0) mbar_wait(leader ? &full[s] : &empty[s], (uint32_t)((n_s - 1) & 1), nullptr);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------- MMA issuer (even CTA) -----
+        if (leader && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+                for (int kb0 = 0, kb1; ok && kb0 < depth; kb0 = kb1) {
+                    kb1 = min(kb0 + a.piece, depth);
+                    if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PAIR_N);
+                    for (int kb = kb0; kb < kb1; ++kb) {
+                        if (!mbar_wait(&full[stage], phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
+                        const uint64_t adesc = operand_desc(A_MN, sa);
+                        const uint64_t bdesc = operand_desc(B_MN, sa + L::A_BYTES);
+#pragma unroll
+                        for (int k = 0; k < BK / 16; ++k)
+                            umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, ((kb - kb0) | k) != 0);
+                        umma_commit_pair(&empty[stage], 0x3);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    umma_commit_pair(&tfull[acc], 0x3);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                }
+            }
+            if (!ok) fail(a.status, abort_flag);
+            umma_commit_pair(mma_done, 0x1);  // every product issued above has finished once this arrives
+            mbar_wait(mma_done, 0, nullptr);
+        }
+    } else {
+        // --------------------------------------------------- epilogue -----
+        const int q = warp & 3;              // TMEM lane quarter this warp may read
+        const int half = (warp - 2) >> 2;    // its 128 of the accumulator's columns
+        const uint32_t tempty_leader = cluster_addr(tempty, 0);
+        Box box{smem + L::BOX_OFF + (warp - 2) * kBox, lane};
+        const uint32_t lanes_at = tmem_base + ((uint32_t)(32 * q) << 16);
+        const bool pieces = EPI != GATED && depth > a.piece;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+            int mb, nb;
+            const int problem = tile / mn_tiles;
+            pair_tile_coords(tile - problem * mn_tiles, num_m, num_n, &mb, &nb);
+            const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
+            const int col0 = nb * TILE_N + (TILE_N / 2) * half;
+            const bool live = row0 < a.rowsA && col0 < a.rowsB;  // not all past the last row or column
+            ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            if constexpr (EPI != GATED) {
+                if (pieces) {
+                    float sum[128];
+#pragma unroll
+                    for (int k = 0; k < 128; ++k) sum[k] = 0.f;
+                    int done = 0;
+                    while (true) {
+                        const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + 128 * half);
+                        done += a.piece;
+                        if (live) add_columns(at, sum);
+                        if (done >= depth) {
+                            if (live) set_columns(at, sum);
+                            break;
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
+                        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    if (!ok) break;
+                }
+            }
+            if (live) {
+                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N);
+                if constexpr (EPI == LINEAR)
+                    epi_linear(at + 128u * (uint32_t)half, row0, col0, problem, a, box);
+                else if constexpr (EPI == GATED)
+                    epi_gated(at + 64u * (uint32_t)half, row0, col0, a, box);
+                else
+                    epi_gated_bwd(at + 128u * (uint32_t)half, row0, col0, a, box);
+            }
+            tc_fence_before();
+            __syncwarp();
+            // relaxed: it says that tensor memory has been read; a release would wait for the results' stores
+            if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!ok) fail(a.status, abort_flag);
+    }
+
+    // Neither CTA deallocates or exits while the pair's products, loads or arrivals may still touch the other's
+    // tensor or shared memory.
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 2 * PAIR_N);
+    }
+}
+
+__global__ void __launch_bounds__(512) k_block_sums(const float* __restrict__ part, int blocks, int n,
+                                                    float* __restrict__ db, const int32_t* __restrict__ status)
+{
+    __shared__ float sum[16][33];
+    if (has_error(status)) return;
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+    float s = 0.f;
+    if (c < n) {
+#pragma unroll 4
+        for (int b = run; b < blocks; b += 16) s += part[(size_t)b * n + c];
+    }
+    sum[run][threadIdx.x & 31] = s;
+    __syncthreads();
+    if (run == 0 && c < n) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += sum[i][threadIdx.x];
+        db[c] = s;
+    }
+}
+
+// ---------------------------------------------------------------- launches --
+
+bool map_of(CUtensorMap* m, const MmOperand& o, int rows, int K)
+{
+    return o.mn ? make_map_mn(m, o.p, rows, K, (int)o.ld) : make_map(m, o.p, rows, K, HALF, (int)o.ld);
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
+{
+    auto kern = k_mm_pair<EPI, A_MN, B_MN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::TOTAL);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Smem::TOTAL;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // clusters of two that can be resident at once
+    static int known[64] = {0};
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (known[dev] <= 0) {
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorNotSupported;
+        known[dev] = n;
+    }
+    constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;
+    const int64_t tiles =
+        ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + TILE_N - 1) / TILE_N) * a.problems;
+    if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(2 * (unsigned)(tiles < known[dev] ? tiles : known[dev]), 1, 1);
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a);
+}
+
+bool pieces_of_16(const void* p, int64_t ld, int n, int es)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * es % 16 == 0 && (int64_t)n * es % 16 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
+{
+    (void)sms;
+    Maps maps;
+    const int n = m.segments * m.problems;
+    for (int i = 0; i < n; ++i)
+        if (!map_of(&maps.a[i], m.a[i], m.M, m.K) || !map_of(&maps.b[i], m.b[i], m.N, m.K)) return cudaErrorInvalidValue;
+    for (int i = n; i < kMmParts; ++i) maps.a[i] = maps.a[0], maps.b[i] = maps.b[0];
+    Args a{};
+    a.rowsA = m.M;
+    a.rowsB = m.N;
+    a.num_kb = (m.K + BK - 1) / BK;
+    a.segments = m.segments;
+    a.problems = m.problems;
+    a.piece = m.out_f32 ? kPieceBlocks : a.num_kb * a.segments;
+    a.bias = m.bias;
+    a.act = m.act;
+    a.res = m.res;
+    a.ldres = m.ldres;
+    a.pre = m.pre;
+    a.ldpre = m.ldpre;
+    for (int i = 0; i < m.problems; ++i) a.out[i] = m.out[i];
+    a.ldo = m.ldo;
+    a.out_f32 = m.out_f32;
+    a.accumulate = m.accumulate;
+    const int es = m.out_f32 ? 4 : 2;
+    bool out_vec = true;
+    for (int i = 0; i < m.problems; ++i) out_vec = out_vec && pieces_of_16(m.out[i], m.ldo, m.N, es);
+    a.vec = (out_vec ? VEC_OUT : 0) | (m.res && pieces_of_16(m.res, m.ldres, m.N, es) ? VEC_RES : 0) |
+            (m.pre && pieces_of_16(m.pre, m.ldpre, m.N, 2) ? VEC_PRE : 0);
+    a.status = m.status;
+    const bool amn = m.a[0].mn, bmn = m.b[0].mn;
+    if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s);
+    if (amn) return cudaErrorInvalidValue;
+    if (bmn) return run_pair<LINEAR, false, true>(maps, a, s);
+    return run_pair<LINEAR, false, false>(maps, a, s);
+}
+
+cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
+{
+    (void)sms;
+    Maps maps;
+    if (!make_map(&maps.a[0], m.x, m.M, m.K, HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, HALF) ||
+        !make_map(&maps.b[1], m.Wu, m.F, m.K, HALF))
+        return cudaErrorInvalidValue;
+    maps.a[1] = maps.a[2] = maps.a[0];
+    maps.b[2] = maps.b[0];
+    Args a{};
+    a.rowsA = m.M;
+    a.rowsB = m.F;
+    a.num_kb = (m.K + BK - 1) / BK;
+    a.segments = a.problems = 1;
+    a.piece = a.num_kb;
+    a.bias = m.bias;
+    a.act = m.act;
+    a.g = m.g;
+    a.u = m.u;
+    a.h = m.h;
+    a.ldo = m.F;
+    a.status = m.status;
+    return run_pair<GATED, false, false>(maps, a, s);
+}
+
+cudaError_t launch_mm_gated_bwd(const MmGatedBwd& m, int sms, cudaStream_t s)
+{
+    (void)sms;
+    Maps maps;
+    if (!make_map(&maps.a[0], m.dy, m.M, m.K, HALF) || !make_map(&maps.b[0], m.Wd, m.F, m.K, HALF))
+        return cudaErrorInvalidValue;
+    maps.a[1] = maps.a[2] = maps.a[0];
+    maps.b[1] = maps.b[2] = maps.b[0];
+    Args a{};
+    a.rowsA = m.M;
+    a.rowsB = m.F;
+    a.num_kb = (m.K + BK - 1) / BK;
+    a.segments = a.problems = 1;
+    a.piece = m.part ? kPieceBlocks : a.num_kb;
+    a.act = m.act;
+    a.l1 = m.l1;
+    a.g_in = m.g;
+    a.u_in = m.u;
+    a.g = m.dg;
+    a.u = m.du;
+    a.part = m.part;
+    a.ldo = m.F;
+    a.status = m.status;
+    return run_pair<GATED_BWD, false, false>(maps, a, s);
+}
+
+cudaError_t launch_block_sums(const float* part, int blocks, int n, float* db, const int32_t* status, cudaStream_t s)
+{
+    count_launches(1);
+    k_block_sums<<<(unsigned)((n + 31) / 32), 512, 0, s>>>(part, blocks, n, db, status);
+    return cudaGetLastError();
+}
+
+}  // namespace twell

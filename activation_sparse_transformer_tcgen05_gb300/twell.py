@@ -30,10 +30,14 @@ EXPORTED_SYMBOLS = (
     "twell_layernorm_fwd", "twell_layernorm_bwd", "twell_layernorm_bwd_workspace_bytes",
     "twell_xent_fwd", "twell_xent_fwd_bwd", "twell_xent_fwd_workspace_bytes", "twell_xent_bwd_workspace_bytes",
     "twell_grad_clip", "twell_grad_clip_workspace_bytes",
+    "twell_linear_fwd", "twell_linear_bwd", "twell_linear_bwd_workspace_bytes", "twell_dense_gated_ffn_fwd",
+    "twell_dense_gated_ffn_bwd", "twell_dense_gated_bwd_workspace_bytes",
 )
 
 # Element type codes (twell_dtype).
 DTYPE_BF16, DTYPE_F32 = 0, 1
+# Activations (twell_activation).
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = range(5)
 
 # Call sites of twell_set_kernel_timer.
 (SITE_NONE, SITE_UP_GEMM, SITE_SPMM_DOWN, SITE_SDDMM, SITE_DX, SITE_CSC, SITE_WGRAD, SITE_DECODE_TAIL,
@@ -147,6 +151,19 @@ def load_library(path: str | None = None):
     lib.twell_grad_clip_workspace_bytes.argtypes = []
     lib.twell_grad_clip.restype = I32
     lib.twell_grad_clip.argtypes = [TLP, F32, P, P, SZ, P]
+    lib.twell_linear_fwd.restype = I32
+    lib.twell_linear_fwd.argtypes = [P, I64, P, I32, P, I32, P, I64, I32, I32, I32, P, I64, P, I64, I32, P, P]
+    lib.twell_linear_bwd_workspace_bytes.restype = SZ
+    lib.twell_linear_bwd_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.twell_linear_bwd.restype = I32
+    lib.twell_linear_bwd.argtypes = [P, I64, P, I64, P, I32, I32, P, I64, I32, I32, I32, P, I64, P, I32, I32, P, P, SZ, P, P]
+    lib.twell_dense_gated_ffn_fwd.restype = I32
+    lib.twell_dense_gated_ffn_fwd.argtypes = [P, P, P, P, P, I32, P, I32, I32, I32, P, P, P, P, P, P]
+    lib.twell_dense_gated_bwd_workspace_bytes.restype = SZ
+    lib.twell_dense_gated_bwd_workspace_bytes.argtypes = [I32, I32, I32]
+    lib.twell_dense_gated_ffn_bwd.restype = I32
+    lib.twell_dense_gated_ffn_bwd.argtypes = [P, P, P, P, I32, P, P, P, P, F32, I32, I32, I32, P, P, P, P, I32, I32, P, P, SZ, P,
+                                              P]
     lib.twell_check.restype = I32
     lib.twell_check.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
     _lib = lib
@@ -577,6 +594,84 @@ def twell_grad_clip(tensors: TwellTensorList, max_norm: float, norm, ws, stream=
     """norm = the L2 norm over all tensors; outs = tensors * min(1, max_norm / norm)."""
     _check(load_library().twell_grad_clip(tensors.ref, max_norm, _vec(norm, "norm", 1, DTYPE_F32), _ptr(ws, "ws"),
                                           ws.numel() * ws.element_size(), _stream(stream)), "twell_grad_clip")
+
+
+def twell_linear_fwd(x, W, w_kn: bool, bias, act: int, res, pre, y, status, stream=None):
+    """y = act(x W^T + bias) + res; pre = x W^T + bias (kept for the backward). W is [N, K], or [K, N] with w_kn. bias, res and
+    pre may be None; y is bf16 or fp32, res of its type (or y itself)."""
+    if x.dim() != 2 or W.dim() != 2 or y.dim() != 2:
+        raise ValueError("x, W and y must be matrices")
+    M, K = x.shape
+    N = W.shape[1 if w_kn else 0]
+    if W.shape != ((K, N) if w_kn else (N, K)):
+        raise ValueError(f"W must be {'[K, N]' if w_kn else '[N, K]'} with x's width K = {K}, got {list(W.shape)}")
+    ty = _dtype(y, "y")
+    px, ldx = _rows(x, "x", M, K, DTYPE_BF16)
+    pr, ldr = _rows(res, "res", M, N, ty)
+    pp, ldp = _rows(pre, "pre", M, N, DTYPE_BF16)
+    py, ldy = _rows(y, "y", M, N, ty)
+    _check(load_library().twell_linear_fwd(
+        px, ldx, _vec(W, "W", N * K, DTYPE_BF16), int(w_kn), _vec(bias, "bias", N, DTYPE_F32), act, pr, ldr, M, N, K, pp, ldp,
+        py, ldy, ty, _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_linear_fwd")
+
+
+def twell_linear_bwd_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load_library().twell_linear_bwd_workspace_bytes(M, N, K))
+
+
+def twell_linear_bwd(dy, x, W, w_kn: bool, act: int, pre, dx, dW, accumulate: bool, dbias, ws, status, stream=None):
+    """Backward of twell_linear_fwd: dx, dW (in W's layout, bf16 or fp32; accumulate adds to an fp32 one) and dbias, each of
+    which may be None; pre may be None without an activation."""
+    if dy.dim() != 2 or x.dim() != 2 or W.dim() != 2:
+        raise ValueError("dy, x and W must be matrices")
+    M, K = x.shape
+    N = W.shape[1 if w_kn else 0]
+    if W.shape != ((K, N) if w_kn else (N, K)):
+        raise ValueError(f"W must be {'[K, N]' if w_kn else '[N, K]'} with x's width K = {K}, got {list(W.shape)}")
+    if dW is not None and dW.shape != W.shape:
+        raise ValueError(f"dW must have W's shape {list(W.shape)}, got {list(dW.shape)}")
+    tw = _dtype(dW, "dW") if dW is not None else DTYPE_BF16
+    pg, ldg = _rows(dy, "dy", M, N, DTYPE_BF16)
+    px, ldx = _rows(x, "x", M, K, DTYPE_BF16)
+    pp, ldp = _rows(pre, "pre", M, N, DTYPE_BF16)
+    pd, ldd = _rows(dx, "dx", M, K, DTYPE_BF16)
+    _check(load_library().twell_linear_bwd(
+        pg, ldg, px, ldx, _vec(W, "W", N * K, DTYPE_BF16), int(w_kn), act, pp, ldp, M, N, K, pd, ldd, _vec(dW, "dW", N * K, tw),
+        tw, int(accumulate), _vec(dbias, "dbias", N, DTYPE_F32), _ptr(ws, "ws"), ws.numel() * ws.element_size(),
+        _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_linear_bwd")
+
+
+def twell_dense_gated_ffn_fwd(x, W_gate, W_up, b, W_down, act: int, res, g, u, h, y, status, stream=None):
+    """The gated layer densely: h = act(x W_gate^T + b) * (x W_up^T), y = h W_down + res. g and u: the two projections, kept for
+    the backward (or both None); b and res may be None, res may be y."""
+    M, d = x.shape
+    F = W_up.shape[0]
+    _check(load_library().twell_dense_gated_ffn_fwd(
+        _vec(x, "x", M * d, DTYPE_BF16), _vec(W_gate, "W_gate", F * d, DTYPE_BF16), _vec(W_up, "W_up", F * d, DTYPE_BF16),
+        _vec(b, "b", F, DTYPE_F32), _vec(W_down, "W_down", F * d, DTYPE_BF16), act, _vec(res, "res", M * d, DTYPE_BF16), M, d, F,
+        _vec(g, "g", M * F, DTYPE_BF16), _vec(u, "u", M * F, DTYPE_BF16), _vec(h, "h", M * F, DTYPE_BF16),
+        _vec(y, "y", M * d, DTYPE_BF16), _ptr(status, "status", bytes_per_elem=4), _stream(stream)),
+        "twell_dense_gated_ffn_fwd")
+
+
+def twell_dense_gated_bwd_workspace_bytes(M: int, d: int, F: int) -> int:
+    return int(load_library().twell_dense_gated_bwd_workspace_bytes(M, d, F))
+
+
+def twell_dense_gated_ffn_bwd(x, W_gate, W_up, W_down, act: int, g, u, h, dy, l1: float, dx, dW_gate, dW_up, dW_down,
+                              accumulate: bool, db, ws, status, stream=None):
+    """Backward of twell_dense_gated_ffn_fwd with l1 sum |h| added to the loss. dx and db may be None, and the three dW (bf16 or
+    fp32; accumulate adds to fp32 ones) together."""
+    M, d = x.shape
+    F = W_up.shape[0]
+    tw = _dtype(dW_gate, "dW_gate") if dW_gate is not None else DTYPE_BF16
+    _check(load_library().twell_dense_gated_ffn_bwd(
+        _vec(x, "x", M * d, DTYPE_BF16), _vec(W_gate, "W_gate", F * d, DTYPE_BF16), _vec(W_up, "W_up", F * d, DTYPE_BF16),
+        _vec(W_down, "W_down", F * d, DTYPE_BF16), act, _vec(g, "g", M * F, DTYPE_BF16), _vec(u, "u", M * F, DTYPE_BF16),
+        _vec(h, "h", M * F, DTYPE_BF16), _vec(dy, "dy", M * d, DTYPE_BF16), float(l1), M, d, F, _vec(dx, "dx", M * d, DTYPE_BF16),
+        _vec(dW_gate, "dW_gate", F * d, tw), _vec(dW_up, "dW_up", F * d, tw), _vec(dW_down, "dW_down", F * d, tw), tw,
+        int(accumulate), _vec(db, "db", F, DTYPE_F32), _ptr(ws, "ws"), ws.numel() * ws.element_size(),
+        _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_dense_gated_ffn_bwd")
 
 
 def twell_check(status: torch.Tensor, stream=None) -> int:

@@ -467,6 +467,74 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
                              void* stream);
 
 /*
+ * Linear layer with bias, activation and residual, and its backward:
+ *   pre = x W^T + bias, y = act(pre) + res
+ *   dpre = dy act'(pre), dx = dpre W, dW = dpre^T x, dbias = column sums of dpre
+ * x [M, K] bf16; W bf16, [N, K] (w_kn 0) or [K, N] (w_kn 1: x W), densely packed;
+ * bias [N] fp32 or NULL; act a twell_activation; res [M, N] of y's type or NULL;
+ * y [M, N] bf16 or fp32 (y_type); pre [M, N] bf16 or NULL (kept for the backward).
+ * Row strides (ld*) in elements. x: a multiple of 8, 16-byte aligned; y, res, pre,
+ * dy, dx: any that is at least the width, of any alignment (16-byte boundaries are
+ * fastest). M >= 0, N >= 1, K % 8 == 0; with w_kn N % 8 == 0. Limit of this build:
+ * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res; other outputs must not
+ * overlap inputs (the call rejects equal pointers).
+ * Sums are fp32 (fp32 results are added up in rounded pieces of 1024 of depth),
+ * outputs are rounded once.
+ *
+ * twell_linear_bwd: dy [M, N] bf16; pre as the forward kept it (NULL if act is
+ * TWELL_ACT_NONE). dx [M, K] bf16; dW in W's layout, bf16 or fp32 (dw_type), with
+ * accumulate != 0 (fp32 only) added to what is there; dbias [N] fp32. Each of the
+ * three may be NULL, not all. With an activation dpre enters the products rounded
+ * to bf16, like any operand of the tensor cores; dbias sums it in fp32.
+ *   ws: at least twell_linear_bwd_workspace_bytes(M, N, K) bytes, 256-byte aligned.
+ * M = 0: dW and dbias are 0 (dW unchanged with accumulate).
+ * Large batches run on CTA pairs (TWELL_ERR_CUDA if a cluster of two cannot be
+ * launched).
+ */
+enum twell_activation { TWELL_ACT_NONE = 0, TWELL_ACT_RELU = 1, TWELL_ACT_SILU = 2, TWELL_ACT_GELU = 3,
+                        TWELL_ACT_GELU_TANH = 4 };
+twell_status twell_linear_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int w_kn, const float* bias, int act,
+                              const void* res, int64_t ldres, int M, int N, int K, uint16_t* pre, int64_t ldpre,
+                              void* y, int64_t ldy, int y_type, int32_t* status, void* stream);
+size_t twell_linear_bwd_workspace_bytes(int M, int N, int K);
+twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, const uint16_t* W,
+                              int w_kn, int act, const uint16_t* pre, int64_t ldpre, int M, int N, int K, uint16_t* dx,
+                              int64_t lddx, void* dW, int dw_type, int accumulate, float* dbias, void* ws,
+                              size_t ws_bytes, int32_t* status, void* stream);
+
+/*
+ * The gated feed-forward layer computed densely, forward and backward. With act =
+ * TWELL_ACT_RELU it is the layer that twell_ffn_fwd serves sparsely with W_gate.
+ *   g = x W_gate^T + b, u = x W_up^T, h = act(g) u, y = h W_down + res
+ *   L = <dy, y> + l1_coef sum |h|:
+ *   dh = dy W_down^T + l1_coef sign(act(g) u), dg = dh u act'(g), du = dh act(g)
+ *   dx = dg W_gate + du W_up, dW_gate = dg^T x, dW_up = du^T x, dW_down = h^T dy,
+ *   db = column sums of dg
+ * x, y, res, dy, dx [M, d] bf16; W_* [F, d] bf16; b, db [F] fp32 or NULL; g, u, h
+ * [M, F] bf16; res may be NULL, or y itself. The forward writes h, and g and u unless
+ * both are NULL (only a backward reads them); h is formed from the unrounded g and u,
+ * y from h as stored. Everything is densely packed; d, F multiples of 8, M >= 0.
+ * Limit of this build: M, d, F <= 2^30 (TWELL_ERR_UNSUPPORTED).
+ * Backward: dg and du enter the products rounded to bf16, db sums dg in fp32. dW_*
+ * bf16 or fp32 (dw_type), with accumulate != 0 (fp32 only) added to what is there; the
+ * three may all be NULL, and so may dx and db, but not everything.
+ *   ws: at least twell_dense_gated_bwd_workspace_bytes(M, d, F) bytes, 256-byte aligned.
+ * M = 0: dW_* and db are 0 (dW_* unchanged with accumulate). Large batches run on CTA
+ * pairs (TWELL_ERR_CUDA if a cluster of two cannot be launched).
+ */
+twell_status twell_dense_gated_ffn_fwd(const uint16_t* x, const uint16_t* W_gate, const uint16_t* W_up, const float* b,
+                                       const uint16_t* W_down, int act, const uint16_t* res, int M, int d, int F,
+                                       uint16_t* g, uint16_t* u, uint16_t* h, uint16_t* y, int32_t* status,
+                                       void* stream);
+size_t twell_dense_gated_bwd_workspace_bytes(int M, int d, int F);
+twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint16_t* W_gate, const uint16_t* W_up,
+                                       const uint16_t* W_down, int act, const uint16_t* g, const uint16_t* u,
+                                       const uint16_t* h, const uint16_t* dy, float l1_coef, int M, int d, int F,
+                                       uint16_t* dx, void* dW_gate, void* dW_up, void* dW_down, int dw_type,
+                                       int accumulate, float* db, void* ws, size_t ws_bytes, int32_t* status,
+                                       void* stream);
+
+/*
  * twell_set_kernel_timer — measurement hook. While set, every launch of the
  * kernel at call site `site` is bracketed by cudaEventRecord(ev_begin) and
  * cudaEventRecord(ev_end) on the launch's stream; ev_begin/ev_end are
