@@ -18,7 +18,8 @@ from .twell import (TwellBuffers, TwellOverflow, TwellError, load_library, twell
                     twell_xent_fwd_bwd, twell_xent_fwd_workspace_bytes, twell_xent_bwd_workspace_bytes,
                     twell_grad_clip, twell_grad_clip_workspace_bytes, ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH,
                     twell_linear_fwd, twell_linear_bwd, twell_linear_bwd_workspace_bytes, twell_dense_gated_ffn_fwd,
-                    twell_dense_gated_ffn_bwd, twell_dense_gated_bwd_workspace_bytes)
+                    twell_dense_gated_ffn_bwd, twell_dense_gated_bwd_workspace_bytes, TwellAdamWList, twell_adamw,
+                    twell_adamw_values, ADAMW_BLOCK)
 
 __all__ = [
     "TwellBuffers", "TwellOverflow", "TwellError", "load_library", "twell_buf_slots_bound", "twell_check",
@@ -33,5 +34,5 @@ __all__ = [
     "twell_xent_bwd_workspace_bytes", "twell_grad_clip", "twell_grad_clip_workspace_bytes",
     "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "twell_linear_fwd", "twell_linear_bwd",
     "twell_linear_bwd_workspace_bytes", "twell_dense_gated_ffn_fwd", "twell_dense_gated_ffn_bwd",
-    "twell_dense_gated_bwd_workspace_bytes",
+    "twell_dense_gated_bwd_workspace_bytes", "TwellAdamWList", "twell_adamw", "twell_adamw_values", "ADAMW_BLOCK",
 ]

@@ -31,7 +31,7 @@ EXPORTED_SYMBOLS = (
     "twell_xent_fwd", "twell_xent_fwd_bwd", "twell_xent_fwd_workspace_bytes", "twell_xent_bwd_workspace_bytes",
     "twell_grad_clip", "twell_grad_clip_workspace_bytes",
     "twell_linear_fwd", "twell_linear_bwd", "twell_linear_bwd_workspace_bytes", "twell_dense_gated_ffn_fwd",
-    "twell_dense_gated_ffn_bwd", "twell_dense_gated_bwd_workspace_bytes",
+    "twell_dense_gated_ffn_bwd", "twell_dense_gated_bwd_workspace_bytes", "twell_adamw", "twell_adamw_values",
 )
 
 # Element type codes (twell_dtype).
@@ -70,11 +70,19 @@ class _TwellTensorList(ctypes.Structure):
                 ("numel", ctypes.c_void_p), ("type", ctypes.c_void_p)]
 
 
+class _TwellAdamWList(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int32), ("state_bits", ctypes.c_int32)] + [
+        (k, ctypes.c_void_p) for k in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy", "numel", "param_type",
+                                       "grad_type")]
+
+
 _lib = None
 P, I32, I64, SZ, F32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 BUFP = ctypes.POINTER(_TwellBuf)
 OVP = ctypes.POINTER(_TwellOverflow)
 TLP = ctypes.POINTER(_TwellTensorList)
+ALP = ctypes.POINTER(_TwellAdamWList)
+F64, U64 = ctypes.c_double, ctypes.c_uint64
 
 
 def load_library(path: str | None = None):
@@ -164,6 +172,10 @@ def load_library(path: str | None = None):
     lib.twell_dense_gated_ffn_bwd.restype = I32
     lib.twell_dense_gated_ffn_bwd.argtypes = [P, P, P, P, I32, P, P, P, P, F32, I32, I32, I32, P, P, P, P, I32, I32, P, P, SZ, P,
                                               P]
+    lib.twell_adamw.restype = I32
+    lib.twell_adamw.argtypes = [ALP, P, P, F64, F64, F64, F64, P, F32, U64, P]
+    lib.twell_adamw_values.restype = I32
+    lib.twell_adamw_values.argtypes = [ALP, TLP, TLP, P]
     lib.twell_check.restype = I32
     lib.twell_check.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
     _lib = lib
@@ -672,6 +684,73 @@ def twell_dense_gated_ffn_bwd(x, W_gate, W_up, W_down, act: int, g, u, h, dy, l1
         _vec(dW_gate, "dW_gate", F * d, tw), _vec(dW_up, "dW_up", F * d, tw), _vec(dW_down, "dW_down", F * d, tw), tw,
         int(accumulate), _vec(db, "db", F, DTYPE_F32), _ptr(ws, "ws"), ws.numel() * ws.element_size(),
         _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_dense_gated_ffn_bwd")
+
+
+ADAMW_BLOCK = 256  # elements that share a scale of 8-bit states
+
+
+class TwellAdamWList:
+    """Parameters with their gradients and optimiser states (contiguous device tensors) and the C struct naming them, for
+    twell_adamw. m and v: fp32, or uint8 codes with m_scale and v_scale (fp32, one for every ADAMW_BLOCK elements).
+    copies: bf16 tensors that follow fp32 parameters (None, or None in places). Keeps the tensors alive; their memory
+    must stay where it is."""
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None):
+        self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
+        n = len(self.params)
+        eight = m_scale is not None
+        if (v_scale is not None) != eight:
+            raise ValueError("m_scale and v_scale: both or neither")
+        self.m_scale, self.v_scale = (list(m_scale), list(v_scale)) if eight else ([], [])
+        self.copies = [None] * n if copies is None else list(copies)
+        if not (len(self.grads) == len(self.m) == len(self.v) == len(self.copies) == n) or (
+                eight and not (len(self.m_scale) == len(self.v_scale) == n)):
+            raise ValueError(f"{n} parameters, but other lists of another length")
+        state = torch.uint8 if eight else torch.float32
+        for i, p in enumerate(self.params):
+            k = p.numel()
+            _vec(p, f"parameter {i}", k, _dtype(p, f"parameter {i}"))
+            _vec(self.grads[i], f"gradient {i}", k, _dtype(self.grads[i], f"gradient {i}"))
+            for t, what in ((self.m[i], "m"), (self.v[i], "v")):
+                if t.dtype is not state:
+                    raise ValueError(f"{what} {i} must be {state}, got {t.dtype}")
+                _ptr(t, f"{what} {i}", numel=k)
+            for t, what in ((self.m_scale, "m_scale"), (self.v_scale, "v_scale")) if eight else ():
+                _vec(t[i], f"{what} {i}", -(-k // ADAMW_BLOCK), DTYPE_F32)
+            if self.copies[i] is not None:
+                if p.dtype is not torch.float32:
+                    raise ValueError(f"parameter {i} must be fp32 to have a copy")
+                _vec(self.copies[i], f"copy {i}", k, DTYPE_BF16)
+
+        def addresses(ts):
+            return (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])
+
+        self._arrays = [addresses(self.params), addresses(self.grads), addresses(self.m), addresses(self.v),
+                        addresses(self.m_scale) if eight else None, addresses(self.v_scale) if eight else None,
+                        addresses(self.copies), (ctypes.c_int64 * n)(*[p.numel() for p in self.params]),
+                        (ctypes.c_int32 * n)(*[_dtype(p, "parameter") for p in self.params]),
+                        (ctypes.c_int32 * n)(*[_dtype(g, "gradient") for g in self.grads])]
+        self.struct = _TwellAdamWList(n, 8 if eight else 32, *[None if a is None else ctypes.addressof(a) for a in self._arrays])
+
+    @property
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def twell_adamw(tensors: TwellAdamWList, lr, step, beta1: float, beta2: float, eps: float, weight_decay: float, norm,
+                max_norm: float, seed: int, stream=None):
+    """One AdamW step in place. lr (fp32 [1]) and step (int32 [1], 1 for the first) are read on the device; norm (fp32 [1],
+    or None): the gradients count scaled so that it is at most max_norm."""
+    if step.dtype is not torch.int32:
+        raise ValueError(f"step must be int32, got {step.dtype}")
+    _check(load_library().twell_adamw(tensors.ref, _vec(lr, "lr", 1, DTYPE_F32), _ptr(step, "step", numel=1), beta1, beta2, eps,
+                                      weight_decay, _vec(norm, "norm", 1, DTYPE_F32), max_norm, seed & (2 ** 64 - 1),
+                                      _stream(stream)), "twell_adamw")
+
+
+def twell_adamw_values(tensors: TwellAdamWList, m_out: TwellTensorList, v_out: TwellTensorList, stream=None):
+    """The values that 8-bit states stand for, to the outs of two lists (bf16 or fp32)."""
+    _check(load_library().twell_adamw_values(tensors.ref, m_out.ref, v_out.ref, _stream(stream)), "twell_adamw_values")
 
 
 def twell_check(status: torch.Tensor, stream=None) -> int:

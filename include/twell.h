@@ -535,6 +535,54 @@ twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint16_t* W_gate
                                        void* stream);
 
 /*
+ * twell_adamw — one step of Adam with decoupled weight decay over many tensors:
+ *   c = norm > max_norm ? max_norm / norm : 1,  g' = c g
+ *   m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   param -= lr (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay param)
+ * lr [1] fp32 and step [1] int32 (t, 1 for the first step) are read on the device, so
+ * that a captured call follows them; norm [1] fp32 as twell_grad_clip writes it (with
+ * an infinite bound), or NULL: c = 1. Gradients are read only. With a norm that is not
+ * finite, or a step below 1, the call changes nothing. beta1, beta2 in [0, 1), eps > 0, weight_decay >= 0.
+ * The list is a host struct of host arrays (read during the call): n tensors, device
+ * addresses, element counts (>= 0). param and grad bf16 or fp32 (twell_dtype codes);
+ * copy (the array or any entry may be NULL): a bf16 copy of an fp32 param. Tensors are
+ * contiguous and aligned to their element size; no tensor overlaps another.
+ * state_bits 32: m, v [numel] fp32. state_bits 8: m, v [numel] uint8 codes and m_scale,
+ * v_scale [ceil(numel / 256)] fp32, each the power of two that TWELL_ADAMW_BLOCK
+ * consecutive elements share. A code is s eeee fff (m) or eeeee fff (v):
+ *   scale 2^(e - 2^E) (1 + f / 8), or scale 2^(1 - 2^E) f / 8 for e = 0   (E = 4, 5)
+ * All zeros, codes and scales, are the states before the first step. Codes are rounded
+ * up or down so that their mean is the value, and so is a bf16 param; a v above 0 never
+ * becomes 0. The random bits are a function of (seed, step, tensor's place in the list,
+ * element) alone. A block with a value that is not finite has a NaN scale.
+ * Limits of this build: 32768 tensors (TWELL_ERR_UNSUPPORTED).
+ *
+ * twell_adamw_values — the values that 8-bit states stand for, to the out tensors of
+ * two lists (bf16, where every one is exact while it is in range, or fp32) with the
+ * list's element counts: to save, inspect or convert them.
+ */
+#define TWELL_ADAMW_BLOCK 256
+typedef struct twell_adamw_list {
+    int32_t n;
+    int32_t state_bits;
+    void* const* param;
+    const void* const* grad;
+    void* const* m;
+    void* const* v;
+    float* const* m_scale; /* state_bits 8 only, else ignored */
+    float* const* v_scale;
+    void* const* copy;
+    const int64_t* numel;
+    const int32_t* param_type;
+    const int32_t* grad_type;
+} twell_adamw_list;
+twell_status twell_adamw(const twell_adamw_list* list, const float* lr, const int32_t* step, double beta1, double beta2,
+                         double eps, double weight_decay, const float* norm, float max_norm, uint64_t seed,
+                         void* stream);
+twell_status twell_adamw_values(const twell_adamw_list* list, const twell_tensor_list* m_out,
+                                const twell_tensor_list* v_out, void* stream);
+
+/*
  * twell_set_kernel_timer — measurement hook. While set, every launch of the
  * kernel at call site `site` is bracketed by cudaEventRecord(ev_begin) and
  * cudaEventRecord(ev_end) on the launch's stream; ev_begin/ev_end are
