@@ -16,6 +16,11 @@
 //   GATED_BWD  D = dh; with g and u, dg and du are formed while the next tile is
 //              computed; dh itself is never written.
 //
+// Few rows (decode batches): the weights' rows are the tensor cores' 128-row operand and
+// the tokens its columns, so that a tile reads 128 rows of W once, whatever the batch
+// (k_mm_few). Bound by memory: the depth is split over a cluster of CTAs until the whole GPU
+// streams, and the parts are added up through the cluster's shared memory, in order.
+//
 // Roles as in twell_gemm.cu: warp 0 loads, warp 1 (even CTA) issues the products, eight
 // warps form the results of 32 rows x 128 columns each and store them through 4 KB of
 // their own shared memory, whole 128-byte pieces of rows at a time.
@@ -651,6 +656,270 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
     }
 }
 
+// ---------------------------------------------------------------- few rows --
+//
+// One CTA: 128 rows of W (GATED: 64 of W_gate and the same 64 of W_up) x up to BN tokens x one part of the depth; a
+// cluster of `parts` CTAs has the whole depth. Two CTAs share an SM: their set-up and ends overlap, and both rings
+// together keep ~190 KB of W in flight, where 45 KB would cover the memory's latency at its rate.
+//   warp 0  loads, warp 1  tensor memory and products, warps 2-5  parts to shared memory; then all threads add the
+//   parts of their columns up and form the results.
+// An earlier error is only looked at before the results are stored: no CTA may leave its cluster early.
+
+constexpr int kFewThreads = 192;
+constexpr int kFewRows = 128;  // rows of W in a tile
+
+template <int BN>
+struct FewSmem {
+    static constexpr int W_BYTES = kFewRows * BK * 2;
+    static constexpr int X_BYTES = BN * BK * 2;
+    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
+    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 1) * 8;
+    static constexpr int TOTAL = MISC_OFF + 16 + 1024;  // + alignment slack
+    static constexpr int PIECES = BN <= 32 ? 8 : 256 / BN;  // accumulators
+    static constexpr uint32_t TMEM_COLS = PIECES * BN;
+    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs on an SM");
+    static_assert(kFewRows * BN * 4 <= STAGES * STAGE_BYTES, "the parts take the ring's place");
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// Four results of one row, and where they go.
+__device__ __forceinline__ void few_store(void* out, bool f32, size_t at, int left, bool vec, const float (&v)[4])
+{
+    if (vec && left >= 4) {
+        if (f32)
+            *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e >= left) break;
+            if (f32)
+                static_cast<float*>(out)[at + e] = v[e];
+            else
+                static_cast<uint16_t*>(out)[at + e] = f32_to_bf16_bits(v[e]);
+        }
+    }
+}
+
+template <int EPI, int BN, bool W_MN>
+__global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant__ Maps maps, const Args a, int parts, int per)
+{
+    using L = FewSmem<BN>;
+    constexpr uint32_t IDESC = idesc_bf16_f32(kFewRows, BN) | (W_MN ? kIdescAMn : 0u);
+    constexpr uint64_t W_KSTEP = W_MN ? (16u * 128u) >> 4 : 2u;
+    constexpr int COLS = EPI == GATED ? kFewRows / 2 : kFewRows;  // output columns of a tile
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+    uint64_t* empty = full + L::STAGES;
+    uint64_t* done = empty + L::STAGES;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = parts > 1 ? (int)cluster_rank() : 0;
+    const int col0 = (int)(blockIdx.x / (unsigned)parts) * COLS, row0 = (int)blockIdx.y * BN;
+    const int depth = a.num_kb * a.segments;
+    const int kb0 = min(rank * per, depth), kb1 = min(kb0 + per, depth);
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, L::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            const uint64_t once = l2_policy_evict_first();  // W goes by once
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const int seg = kb / a.num_kb, x = (kb - seg * a.num_kb) * BK;
+                uint8_t* sw = smem + stage * L::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
+                if constexpr (EPI == GATED) {
+                    tma_load_2d_hint(sw, &maps.b[0], x, col0, &full[stage], once);
+                    tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[1], x, col0, &full[stage], once);
+                } else if constexpr (W_MN) {
+                    tma_load_2d_hint(sw, &maps.b[seg], col0, x, &full[stage], once);
+                    tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[seg], col0 + kMnBox, x, &full[stage], once);
+                } else {
+                    tma_load_2d_hint(sw, &maps.b[seg], x, col0, &full[stage], once);
+                }
+                tma_load_2d(sw + L::W_BYTES, &maps.a[seg], x, row0, &full[stage]);
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) fail(a.status, abort_flag);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = true;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(&full[stage], phase, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int i = kb - kb0, piece = i / a.piece;
+                const uint32_t d_tmem = tmem_base + (uint32_t)(piece * BN);
+                const uint32_t sw = smem_u32(smem + stage * L::STAGE_BYTES);
+                const uint64_t wdesc = operand_desc(W_MN, sw);
+                const uint64_t xdesc = sw128_kmajor_desc(sw + L::W_BYTES);
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                    umma_bf16(d_tmem, wdesc + W_KSTEP * k, xdesc + 2u * k, IDESC, ((i - piece * a.piece) | k) != 0);
+                umma_commit(&empty[stage]);
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) fail(a.status, abort_flag);
+            umma_commit(done);
+        }
+    }
+    __syncwarp();
+    // Every load has landed when the products that read it are done, so the ring is free from here on. (Loads in
+    // flight after a wait that ran out still land in it: the results are not used then, but the CTA must not end.)
+    bool ok = mbar_wait(done, 0, nullptr);
+    if (!ok) fail(a.status, abort_flag);
+    if (__syncthreads_or(*abort_flag)) {
+        if (threadIdx.x == 0)
+            for (int s = 0; s < L::STAGES; ++s) {
+                mbar_wait(&full[s], 0, nullptr);
+                mbar_wait(&full[s], 1, nullptr);
+            }
+        __syncthreads();
+    }
+    tc_fence_after();
+    float* part = reinterpret_cast<float*>(smem);  // [token][kFewRows]
+    const int tokens = min(BN, a.rowsA - row0);
+    if (warp >= 2) {
+        const int q = warp & 3;
+        const int pieces = (kb1 - kb0 + a.piece - 1) / a.piece;
+        const uint32_t at = tmem_base + ((uint32_t)(32 * q) << 16);
+#pragma unroll 1
+        for (int c0 = 0; c0 < tokens; c0 += 16) {
+            float sum[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum[c] = 0.f;
+            for (int p = 0; p < pieces; ++p) {
+                uint32_t v[16];
+                tmem_ld16_wait(at + (uint32_t)(p * BN + c0), v);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) sum[c] += __uint_as_float(v[c]);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) part[(c0 + c) * kFewRows + 32 * q + lane] = sum[c];
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    if (parts > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+
+    // this CTA's share of the tile's columns, four at a time; parts in the cluster's order
+    const int share = COLS / parts;
+    const int base = rank * share;
+    if (!has_error(a.status)) {
+        for (int i = threadIdx.x; i < tokens * (share / 4); i += kFewThreads) {
+            const int t = i / (share / 4), c = base + (i - t * (share / 4)) * 4;
+            const int col = col0 + c, left = a.rowsB - col;
+            if (left <= 0) continue;
+            float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < parts; ++r) {
+                const float* from = part + t * kFewRows + c;
+                const uint32_t addr = parts > 1 ? cluster_addr(from, (uint32_t)r) : smem_u32(from);
+                const float4 f = ld_cluster_f4(addr);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                if constexpr (EPI == GATED) {
+                    const float4 w = ld_cluster_f4(addr + (kFewRows / 2) * 4);
+                    u[0] += w.x, u[1] += w.y, u[2] += w.z, u[3] += w.w;
+                }
+            }
+            const size_t row = (size_t)row0 + t;
+            if (a.bias) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left) v[e] += a.bias[col + e];
+            }
+            if constexpr (EPI == GATED) {
+                const size_t at = row * a.ldo + col;
+                if (a.g) {
+                    few_store(a.g, false, at, left, true, v);
+                    few_store(a.u, false, at, left, true, u);
+                }
+                by_activation(a.act, [&](auto tag) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]) * u[e];
+                });
+                few_store(a.h, false, at, left, true, v);
+            } else {
+                if (a.pre) few_store(a.pre, false, row * a.ldpre + col, left, a.vec & VEC_PRE, v);
+                if (a.act != TWELL_ACT_NONE)
+                    by_activation(a.act, [&](auto tag) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]);
+                    });
+                if (a.res) {
+                    const size_t at = row * a.ldres + col;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left)
+                            v[e] += a.out_f32 ? static_cast<const float*>(a.res)[at + e]
+                                              : bf16_to_f32(static_cast<const uint16_t*>(a.res)[at + e]);
+                }
+                few_store(a.out[0], a.out_f32, row * a.ldo + col, left, a.vec & VEC_OUT, v);
+            }
+        }
+    }
+    __syncwarp();
+    // no CTA ends while another may still read its part
+    if (parts > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, L::TMEM_COLS);
+    }
+}
+
 __global__ void __launch_bounds__(512) k_block_sums(const float* __restrict__ part, int blocks, int n,
                                                     float* __restrict__ db, const int32_t* __restrict__ status)
 {
@@ -673,9 +942,9 @@ __global__ void __launch_bounds__(512) k_block_sums(const float* __restrict__ pa
 
 // ---------------------------------------------------------------- launches --
 
-bool map_of(CUtensorMap* m, const MmOperand& o, int rows, int K)
+bool map_of(CUtensorMap* m, const MmOperand& o, int rows, int K, int box_rows)
 {
-    return o.mn ? make_map_mn(m, o.p, rows, K, (int)o.ld) : make_map(m, o.p, rows, K, HALF, (int)o.ld);
+    return o.mn ? make_map_mn(m, o.p, rows, K, (int)o.ld) : make_map(m, o.p, rows, K, box_rows, (int)o.ld);
 }
 
 template <int EPI, bool A_MN, bool B_MN>
@@ -718,6 +987,65 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
+// Rows up to which the weights' rows are the tensor cores' 128-row operand.
+constexpr int kFewMost = 128;
+
+// Parts of the depth: as few as keep about one CTA on each SM, and no part shorter than four k-blocks.
+int few_parts(int64_t tiles, int depth, int sms)
+{
+    int parts = 1;
+    while (parts < 8 && tiles * parts < sms && depth / (2 * parts) >= 4) parts *= 2;
+    return parts;
+}
+
+template <int EPI, int BN, bool W_MN>
+cudaError_t run_few(const Maps& maps, Args a, int sms, cudaStream_t s)
+{
+    using L = FewSmem<BN>;
+    auto kern = k_mm_few<EPI, BN, W_MN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+    if (e != cudaSuccess) return e;
+    constexpr int COLS = EPI == GATED ? kFewRows / 2 : kFewRows;
+    const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
+    const int blocks = (a.rowsA + BN - 1) / BN, depth = a.num_kb * a.segments;
+    const int parts = few_parts(tiles * blocks, depth, sms), per = (depth + parts - 1) / parts;
+    if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
+    // fp32 results in pieces of 512 of depth, or as many as there are accumulators for
+    a.piece = per;
+    if (a.out_f32) {
+        const int least = (per + L::PIECES - 1) / L::PIECES;
+        a.piece = least > 8 ? least : 8;
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)parts;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * parts), (unsigned)blocks, 1);
+    cfg.blockDim = dim3(kFewThreads, 1, 1);
+    cfg.dynamicSmemBytes = L::TOTAL;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    count_launches(1);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per);
+}
+
+// Tokens a tile holds for this many rows.
+int few_tokens(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+template <int EPI, bool W_MN>
+cudaError_t run_few_rows(const Maps& maps, const Args& a, int sms, cudaStream_t s)
+{
+    switch (few_tokens(a.rowsA)) {
+        case 16: return run_few<EPI, 16, W_MN>(maps, a, sms, s);
+        case 32: return run_few<EPI, 32, W_MN>(maps, a, sms, s);
+        case 64: return run_few<EPI, 64, W_MN>(maps, a, sms, s);
+        default: return run_few<EPI, 128, W_MN>(maps, a, sms, s);
+    }
+}
+
 bool pieces_of_16(const void* p, int64_t ld, int n, int es)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * es % 16 == 0 && (int64_t)n * es % 16 == 0;
@@ -727,11 +1055,12 @@ bool pieces_of_16(const void* p, int64_t ld, int n, int es)
 
 cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
 {
-    (void)sms;
     Maps maps;
     const int n = m.segments * m.problems;
+    const bool few = m.M <= kFewMost && m.problems == 1 && !m.accumulate && !m.a[0].mn;
     for (int i = 0; i < n; ++i)
-        if (!map_of(&maps.a[i], m.a[i], m.M, m.K) || !map_of(&maps.b[i], m.b[i], m.N, m.K)) return cudaErrorInvalidValue;
+        if (!map_of(&maps.a[i], m.a[i], m.M, m.K, few ? few_tokens(m.M) : HALF) || !map_of(&maps.b[i], m.b[i], m.N, m.K, HALF))
+            return cudaErrorInvalidValue;
     for (int i = n; i < kMmParts; ++i) maps.a[i] = maps.a[0], maps.b[i] = maps.b[0];
     Args a{};
     a.rowsA = m.M;
@@ -757,6 +1086,7 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
             (m.pre && pieces_of_16(m.pre, m.ldpre, m.N, 2) ? VEC_PRE : 0);
     a.status = m.status;
     const bool amn = m.a[0].mn, bmn = m.b[0].mn;
+    if (few) return bmn ? run_few_rows<LINEAR, true>(maps, a, sms, s) : run_few_rows<LINEAR, false>(maps, a, sms, s);
     if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s);
     if (amn) return cudaErrorInvalidValue;
     if (bmn) return run_pair<LINEAR, false, true>(maps, a, s);
@@ -765,10 +1095,11 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
 
 cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
 {
-    (void)sms;
     Maps maps;
-    if (!make_map(&maps.a[0], m.x, m.M, m.K, HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, HALF) ||
-        !make_map(&maps.b[1], m.Wu, m.F, m.K, HALF))
+    const bool few = m.M <= kFewMost;
+    const int w_rows = few ? kFewRows / 2 : HALF;
+    if (!make_map(&maps.a[0], m.x, m.M, m.K, few ? few_tokens(m.M) : HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, w_rows) ||
+        !make_map(&maps.b[1], m.Wu, m.F, m.K, w_rows))
         return cudaErrorInvalidValue;
     maps.a[1] = maps.a[2] = maps.a[0];
     maps.b[2] = maps.b[0];
@@ -785,6 +1116,7 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
     a.h = m.h;
     a.ldo = m.F;
     a.status = m.status;
+    if (few) return run_few_rows<GATED, false>(maps, a, sms, s);
     return run_pair<GATED, false, false>(maps, a, s);
 }
 
