@@ -34,7 +34,7 @@ namespace twell {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 4, kValueBlocksPerSm = 6;
 constexpr int kBlock = TWELL_ADAMW_BLOCK;         // elements that share a scale: one warp's, 8 a lane
 constexpr int kUnit = kBlock * (kThreads / 32);   // elements of one unit of work
 constexpr int kPer = kBlock / 32;
@@ -105,15 +105,27 @@ __device__ __forceinline__ float sqrt_approx(float x)
     return y;
 }
 
-// Place of a lane's element k in its block: four neighbours, or (VEC false) neighbours in neighbouring lanes.
+// (of a normal number below 2^126: eps at least, the root of a float at most)
+__device__ __forceinline__ float reciprocal_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Place of a lane's element k in its block: four neighbours, or (V false) neighbours in neighbouring lanes.
 template <bool V>
 __device__ __forceinline__ int place(int k, int lane)
 {
     return V ? (k >> 2) * 128 + lane * 4 + (k & 3) : k * 32 + lane;
 }
 
+// A lane's elements as pairs, for the instructions that work on two fp32 values at once: with one at a time the pass
+// over 8-bit states is bound by instructions.
+constexpr int kPairs = kPer / 2;
+
 template <bool V>
-__device__ __forceinline__ void load(const void* p, bool f32, int64_t i0, int left, int lane, float (&x)[kPer])
+__device__ __forceinline__ void load(const void* p, bool f32, int64_t i0, int left, int lane, float2 (&x)[kPairs])
 {
     if constexpr (V) {
 #pragma unroll
@@ -121,144 +133,226 @@ __device__ __forceinline__ void load(const void* p, bool f32, int64_t i0, int le
             const int64_t i = i0 + place<true>(k, lane);
             if (f32) {
                 const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-                x[k] = q.x, x[k + 1] = q.y, x[k + 2] = q.z, x[k + 3] = q.w;
+                x[k / 2] = make_float2(q.x, q.y);
+                x[k / 2 + 1] = make_float2(q.z, q.w);
             } else {
                 const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-                x[k] = bf16_lo(q.x), x[k + 1] = bf16_hi(q.x), x[k + 2] = bf16_lo(q.y), x[k + 3] = bf16_hi(q.y);
+                x[k / 2] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+                x[k / 2 + 1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
             }
         }
     } else {
+        float y[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const int i = place<false>(k, lane);
-            x[k] = 0.f;
+            y[k] = 0.f;
             if (i < left)
-                x[k] = f32 ? static_cast<const float*>(p)[i0 + i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i0 + i]);
+                y[k] = f32 ? static_cast<const float*>(p)[i0 + i] : bf16_to_f32(static_cast<const uint16_t*>(p)[i0 + i]);
         }
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) x[k] = make_float2(y[2 * k], y[2 * k + 1]);
     }
 }
 
 template <bool V>
-__device__ __forceinline__ void store(void* p, bool f32, int64_t i0, int left, int lane, const float (&x)[kPer])
+__device__ __forceinline__ void store(void* p, bool f32, int64_t i0, int left, int lane, const float2 (&x)[kPairs])
 {
     if constexpr (V) {
 #pragma unroll
         for (int k = 0; k < kPer; k += 4) {
             const int64_t i = i0 + place<true>(k, lane);
+            const float2 a = x[k / 2], b = x[k / 2 + 1];
             if (f32)
-                *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+                *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a.x, a.y, b.x, b.y);
             else
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-                    make_uint2(cvt_bf16x2(x[k], x[k + 1]), cvt_bf16x2(x[k + 2], x[k + 3]));
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = make_uint2(cvt_bf16x2(a.x, a.y), cvt_bf16x2(b.x, b.y));
         }
     } else {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
             const int i = place<false>(k, lane);
             if (i >= left) continue;
+            const float y = (k & 1) ? x[k / 2].y : x[k / 2].x;
             if (f32)
-                static_cast<float*>(p)[i0 + i] = x[k];
+                static_cast<float*>(p)[i0 + i] = y;
             else
-                static_cast<uint16_t*>(p)[i0 + i] = f32_to_bf16_bits(x[k]);
+                static_cast<uint16_t*>(p)[i0 + i] = f32_to_bf16_bits(y);
+        }
+    }
+}
+
+// Codes of four elements a word, the first in the lowest byte.
+template <bool V>
+__device__ __forceinline__ void load_codes(const void* p, int64_t i0, int left, int lane, uint32_t (&w)[kPer / 4])
+{
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4) {
+        if constexpr (V) {
+            w[k / 4] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + i0 + place<true>(k, lane));
+        } else {
+            w[k / 4] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = place<false>(k + e, lane);
+                if (i < left) w[k / 4] |= (uint32_t) static_cast<const uint8_t*>(p)[i0 + i] << (8 * e);
+            }
         }
     }
 }
 
 template <bool V>
-__device__ __forceinline__ void load_codes(const void* p, int64_t i0, int left, int lane, uint32_t (&x)[kPer])
+__device__ __forceinline__ void store_codes(void* p, int64_t i0, int left, int lane, const uint32_t (&w)[kPer / 4])
+{
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4) {
+        if constexpr (V) {
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i0 + place<true>(k, lane)) = w[k / 4];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = place<false>(k + e, lane);
+                if (i < left) static_cast<uint8_t*>(p)[i0 + i] = (uint8_t)(w[k / 4] >> (8 * e));
+            }
+        }
+    }
+}
+
+// 16 random bits for each of a lane's elements: for the moments m's in the lower and v's in the upper half of a word,
+// two elements' words to one of splitmix64's; for a bf16 parameter four elements' bits. Neighbours of a lane share one.
+template <bool V>
+__device__ __forceinline__ void moment_bits(uint64_t key, int64_t i0, int lane, uint32_t (&r)[kPer])
 {
     if constexpr (V) {
+        const uint64_t at = key + (uint64_t)((i0 + lane * 4) / 2 + 1) * kGamma;
+#pragma unroll
+        for (int k = 0; k < kPer; k += 2) {
+            const uint64_t w = mix(at + (uint64_t)((k >> 2) * 64 + ((k >> 1) & 1)) * kGamma);
+            r[k] = (uint32_t)w;
+            r[k + 1] = (uint32_t)(w >> 32);
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int64_t e = i0 + place<false>(k, lane);
+            r[k] = (uint32_t)(mix(key + (uint64_t)((e >> 1) + 1) * kGamma) >> ((e & 1) * 32));
+        }
+    }
+}
+template <bool V>
+__device__ __forceinline__ void param_bits(uint64_t key, int64_t i0, int lane, uint32_t (&r)[kPer])
+{
+    if constexpr (V) {
+        const uint64_t at = key + (uint64_t)((i0 + lane * 4) / 4 + 1) * kGamma;
 #pragma unroll
         for (int k = 0; k < kPer; k += 4) {
-            const uint32_t q = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + i0 + place<true>(k, lane));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[k + e] = (q >> (8 * e)) & 255u;
+            const uint64_t w = mix(at + (uint64_t)((k >> 2) * 32) * kGamma);
+            r[k] = (uint32_t)w & 0xffffu;
+            r[k + 1] = (uint32_t)w >> 16;
+            r[k + 2] = (uint32_t)(w >> 32) & 0xffffu;
+            r[k + 3] = (uint32_t)(w >> 48);
         }
     } else {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int i = place<false>(k, lane);
-            x[k] = i < left ? static_cast<const uint8_t*>(p)[i0 + i] : 0u;
+            const int64_t e = i0 + place<false>(k, lane);
+            r[k] = (uint32_t)(mix(key + (uint64_t)((e >> 2) + 1) * kGamma) >> ((e & 3) * 16)) & 0xffffu;
         }
     }
 }
 
-template <bool V>
-__device__ __forceinline__ void store_codes(void* p, int64_t i0, int left, int lane, const uint32_t (&x)[kPer])
-{
-    if constexpr (V) {
-#pragma unroll
-        for (int k = 0; k < kPer; k += 4)
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + i0 + place<true>(k, lane)) =
-                x[k] | x[k + 1] << 8 | x[k + 2] << 16 | x[k + 3] << 24;
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int i = place<false>(k, lane);
-            if (i < left) static_cast<uint8_t*>(p)[i0 + i] = (uint8_t)x[k];
-        }
-    }
-}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// Powers of two that a code and its value lie apart: 2^(127 - 2^E) times the scale. One multiplication as long as their
+// product is a normal number, two (rounded the same) for scales above 2^(2^E).
+template <int E>
+constexpr float kUp = E == kMBits ? 0x1p+111f : 0x1p+95f;
 
 // The values of codes with E exponent bits under `scale`.
 template <int E>
-__device__ __forceinline__ void decode(const uint32_t (&code)[kPer], float scale, float (&x)[kPer])
+__device__ __forceinline__ void decode(const uint32_t (&w)[kPer / 4], float scale, float2 (&x)[kPairs])
 {
-    const float up = __uint_as_float((uint32_t)(254 - (1 << E)) << 23);  // 2^(127 - 2^E)
+    const bool large = scale > (E == kMBits ? 0x1p+16f : 0x1p+32f);
+    const float2 f = both(large ? kUp<E> : scale * kUp<E>);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const uint32_t size = E == kMBits ? code[k] & 127u : code[k];
-        const float y = __fmul_rn(__fmul_rn(__uint_as_float(size << 20), up), scale);
-        x[k] = E == kMBits && (code[k] & 128u) ? -y : y;
+    for (int k = 0; k < kPer; k += 2) {
+        float y[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // the byte at the top, then 4 bits down: exponent and fraction where fp32 has them, m's sign at its place
+            const uint32_t top = w[k / 4] << (24 - 8 * ((k + e) & 3));
+            y[e] = __uint_as_float(E == kMBits ? (uint32_t)((int32_t)top >> 4) & 0x87f00000u : (top >> 4) & 0x0ff00000u);
+        }
+        x[k / 2] = __fmul2_rn(make_float2(y[0], y[1]), f);
+        if (large) x[k / 2] = __fmul2_rn(x[k / 2], both(scale));
     }
 }
 
 // Codes of a block's values and their scale (the same in all lanes), rounded by 16 random bits each. A block with a
-// value that is not finite has NaN as its scale, and all its values are NaN.
+// value that is not finite, or above 15/16 2^127, has NaN as its scale, and all its values are NaN.
 template <int E>
-__device__ __forceinline__ float encode(const float (&x)[kPer], const uint32_t (&random)[kPer], uint32_t (&code)[kPer])
+__device__ __forceinline__ float encode(const float2 (&x)[kPairs], const uint32_t (&random)[kPer], uint32_t (&w)[kPer / 4])
 {
     uint32_t top = 0;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    uint32_t up = (top >> 23) + 1 + ((top & 0x7fffffu) > 0x700000u ? 1u : 0u);
-    up = min(up, 254u);
-    const float scale = top == 0 ? 0.f : top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __uint_as_float(up << 23);
-    // 1 / scale: 2^(127 - up), below fp32's normal numbers for up = 254
-    const float inv = top == 0 ? 0.f : up == 254u ? __uint_as_float(0x400000u) : __uint_as_float((254u - up) << 23);
-    const float down = E == kMBits ? 0x1p-111f : 0x1p-95f;  // 2^(2^E - 127)
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const float z = __fmul_rn(__fmul_rn(fabsf(x[k]), inv), down);
-        uint32_t q = (__float_as_uint(z) + (random[k] << 4)) >> 20;
-        q = min(q, (8u << E) - 1u);
-        if (E == kMBits)
-            q |= (__float_as_uint(x[k]) >> 24) & 128u;
-        else if (q == 0 && x[k] > 0.f)
-            q = 1;
-        code[k] = q;
+    for (int k = 0; k < kPairs; ++k) {
+        const uint32_t a = __float_as_uint(x[k].x), b = __float_as_uint(x[k].y);
+        top = max(top, max(E == kMBits ? a & 0x7fffffffu : a, E == kMBits ? b & 0x7fffffffu : b));
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const uint32_t up = (top >> 23) + 1 + ((top & 0x7fffffu) > 0x700000u ? 1u : 0u);
+    const float scale = top == 0 ? 0.f : up > 254u ? __uint_as_float(0x7fc00000u) : __uint_as_float(up << 23);
+    // 2^(127 - up) 2^(2^E - 127), the second factor for itself where the product is below fp32's normal numbers
+    constexpr uint32_t sum = 127u + (1u << E);
+    const bool large = up > sum - 1u;
+    const float2 f = both(__uint_as_float(large ? (up >= 254u ? 0x400000u : (254u - up) << 23) : (sum - up) << 23));
+    uint32_t least = 0xffffffffu, t[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; k += 2) {
+        float2 z = __fmul2_rn(x[k / 2], f);
+        if (large) z = __fmul2_rn(z, both(1.f / kUp<E>));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // Rounded up or down by the bits below the code: at most 15/16 of the scale, so never past the largest
+            // code. Four bits up, the code is the top byte, m's sign (which the shift takes away) its first bit.
+            const uint32_t bits = __float_as_uint(e ? z.y : z.x), r = random[k + e];
+            t[k + e] = (bits + (E == kMBits ? r & 0xffffu : r >> 16) * 16u) << 4;
+            if (E == kMBits)
+                t[k + e] |= __float_as_uint(e ? x[k / 2].y : x[k / 2].x) & 0x80000000u;
+            else
+                least = min(least, t[k + e]);
+        }
+    }
+    if (E != kMBits && least < 1u << 24) {  // a code of 0: only 0 has it
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (t[k] < 1u << 24 && ((k & 1) ? x[k / 2].y : x[k / 2].x) > 0.f) t[k] = 1u << 24;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; k += 4)
+        w[k / 4] = __byte_perm(__byte_perm(t[k], t[k + 1], 0x0073), __byte_perm(t[k + 2], t[k + 3], 0x0073), 0x5410);
     return scale;
 }
 
 struct Scalars {
-    float c, lr, by_m, by_v;
+    float c, rate, decay, root;  // rate = lr / (1 - b1^t), decay so that rate decay = lr wd, root = 1 / sqrt(1 - b2^t)
     uint64_t base;
     int skip;
 };
 
-// A block's elements of one tensor.
-template <bool V, bool BITS8>
+// A block's elements of one tensor. `moments`, `params`: keys of its random bits.
+// PF, GF: parameter and gradient are fp32 (as template arguments: with both kinds of loads behind a branch each waited for
+// the one before).
+template <bool V, bool BITS8, bool PF, bool GF>
 __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void* v, float* ms, float* vs, uint16_t* copy,
-                                           int flags, int64_t i0, int left, int lane, const Hyper& h, const Scalars& s,
-                                           uint64_t key)
+                                           int64_t i0, int left, int lane, const Hyper& h, const Scalars& s,
+                                           uint64_t moments, uint64_t params)
 {
-    float x[kPer], grad[kPer], mom[kPer], var[kPer];
-    load<V>(p, flags & P_F32, i0, left, lane, x);
-    load<V>(g, flags & G_F32, i0, left, lane, grad);
+    float2 x[kPairs], grad[kPairs], mom[kPairs], var[kPairs];
+    load<V>(p, PF, i0, left, lane, x);
+    load<V>(g, GF, i0, left, lane, grad);
     if constexpr (BITS8) {
-        uint32_t cm[kPer], cv[kPer];
+        uint32_t cm[kPer / 4], cv[kPer / 4];
         load_codes<V>(m, i0, left, lane, cm);
         load_codes<V>(v, i0, left, lane, cv);
         const float sm = ms[i0 / kBlock], sv = vs[i0 / kBlock];
@@ -269,42 +363,37 @@ __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void
         load<V>(v, true, i0, left, lane, var);
     }
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const float gs = __fmul_rn(grad[k], s.c);
-        mom[k] = __fadd_rn(__fmul_rn(h.b1, mom[k]), __fmul_rn(h.rest1, gs));
-        var[k] = __fadd_rn(__fmul_rn(h.b2, var[k]), __fmul_rn(h.rest2, __fmul_rn(gs, gs)));
-        const float to = __fdividef(mom[k] * s.by_m, sqrt_approx(var[k] * s.by_v) + h.eps);
-        x[k] -= s.lr * fmaf(h.decay, x[k], to);
+    for (int k = 0; k < kPairs; ++k) {
+        // each operation rounded for itself: what the codes are formed of is the same bits in any order of compilation
+        const float2 gs = __fmul2_rn(grad[k], both(s.c));
+        mom[k] = __fadd2_rn(__fmul2_rn(both(h.b1), mom[k]), __fmul2_rn(both(h.rest1), gs));
+        var[k] = __fadd2_rn(__fmul2_rn(both(h.b2), var[k]), __fmul2_rn(both(h.rest2), __fmul2_rn(gs, gs)));
+        const float2 under = __ffma2_rn(make_float2(sqrt_approx(var[k].x), sqrt_approx(var[k].y)), both(s.root), both(h.eps));
+        const float2 to = __fmul2_rn(mom[k], make_float2(reciprocal_approx(under.x), reciprocal_approx(under.y)));
+        x[k] = __ffma2_rn(both(-s.rate), __ffma2_rn(both(s.decay), x[k], to), x[k]);
     }
-    if (flags & P_F32) {
+    if (PF) {
         store<V>(p, true, i0, left, lane, x);
         if (copy) store<V>(copy, false, i0, left, lane, x);
     } else {
         // 16 random bits each: most steps are smaller than half a unit of bf16
-        const uint64_t pkey = mix(key + kGamma);
+        uint32_t r[kPer];
+        param_bits<V>(params, i0, lane, r);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int64_t e = i0 + place<V>(k, lane);
-            const uint32_t r = (uint32_t)(mix(pkey + (uint64_t)((e >> 2) + 1) * kGamma) >> ((e & 3) * 16)) & 0xffffu;
-            const uint32_t bits = __float_as_uint(x[k]);
+            float& y = (k & 1) ? x[k / 2].y : x[k / 2].x;
+            const uint32_t bits = __float_as_uint(y);
             // (not into infinity's or NaN's bits)
-            x[k] = __uint_as_float((bits & 0x7f800000u) == 0x7f800000u ? bits : (bits + r) & 0xffff0000u);
+            y = __uint_as_float((bits & 0x7f800000u) == 0x7f800000u ? bits : (bits + r[k]) & 0xffff0000u);
         }
         store<V>(p, false, i0, left, lane, x);
     }
     if constexpr (BITS8) {
-        const uint64_t mkey = mix(key);
-        uint32_t rm[kPer], rv[kPer], code[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-            const int64_t e = i0 + place<V>(k, lane);
-            const uint32_t w = (uint32_t)(mix(mkey + (uint64_t)((e >> 1) + 1) * kGamma) >> ((e & 1) * 32));
-            rm[k] = w & 0xffffu;
-            rv[k] = w >> 16;
-        }
-        const float sm = encode<kMBits>(mom, rm, code);
+        uint32_t r[kPer], code[kPer / 4];
+        moment_bits<V>(moments, i0, lane, r);
+        const float sm = encode<kMBits>(mom, r, code);
         store_codes<V>(m, i0, left, lane, code);
-        const float sv = encode<kVBits>(var, rv, code);
+        const float sv = encode<kVBits>(var, r, code);
         store_codes<V>(v, i0, left, lane, code);
         if (lane == 0) {
             ms[i0 / kBlock] = sm;
@@ -316,6 +405,24 @@ __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void
     }
 }
 
+// f(whole pieces, parameter in fp32, gradient in fp32) as types.
+template <class F>
+__device__ __forceinline__ void by_types(int flags, bool whole, F f)
+{
+    const std::true_type yes{};
+    const std::false_type no{};
+    switch (flags & (whole ? VEC | P_F32 | G_F32 : P_F32 | G_F32)) {
+        case VEC | P_F32 | G_F32: f(yes, yes, yes); break;
+        case VEC | P_F32: f(yes, yes, no); break;
+        case VEC | G_F32: f(yes, no, yes); break;
+        case VEC: f(yes, no, no); break;
+        case P_F32 | G_F32: f(no, yes, yes); break;
+        case P_F32: f(no, yes, no); break;
+        case G_F32: f(no, no, yes); break;
+        default: f(no, no, no); break;
+    }
+}
+
 template <int CAP, bool BITS8>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_constant__ Table<CAP> t, const Hyper h)
 {
@@ -323,12 +430,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
     if (threadIdx.x == 0) {
         Scalars s;
         const float norm = h.norm ? *h.norm : 0.f;
-        s.c = norm > h.max_norm ? __fdiv_rn(h.max_norm, norm) : 1.f;
-        s.lr = *h.lr;
         const int step = *h.step;
         s.skip = !(fabsf(norm) < INFINITY) || step < 1;
-        s.by_m = __fdiv_rn(1.f, one_minus_power(h.log_b1, step));
-        s.by_v = __fdiv_rn(1.f, one_minus_power(h.log_b2, step));
+        s.c = norm > h.max_norm ? __fdiv_rn(h.max_norm, norm) : 1.f;
+        const float rest = one_minus_power(h.log_b1, step);
+        s.rate = __fdiv_rn(*h.lr, rest);
+        s.decay = h.decay * rest;
+        s.root = rsqrtf(one_minus_power(h.log_b2, step));
         s.base = mix(h.seed + (uint64_t)(int64_t)step * kGamma);
         shared = s;
     }
@@ -337,26 +445,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
     if (s.skip) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
-    int k = u0 < u1 ? t.find(u0) : 0;
+    int k = u0 < u1 ? t.find(u0) - 1 : 0, next = u0;
+    uint64_t moments = 0, params = 0;
     for (int u = u0; u < u1; ++u) {
-        while (u >= t.first[k + 1]) ++k;
+        if (u >= next) {  // the next tensor (none is empty), or the first
+            ++k;
+            next = t.first[k + 1];
+            const uint64_t key = s.base + (uint64_t)(2 * (int64_t)t.id[k] + 1) * kGamma;
+            if (BITS8) moments = mix(key);
+            params = mix(key + kGamma);
+        }
         const int64_t i0 = (int64_t)(u - t.first[k]) * kUnit + warp * kBlock;
         const int64_t rest = t.numel[k] - i0;
         if (rest <= 0) continue;
         const int left = (int)min((int64_t)kBlock, rest);
-        const uint64_t key = s.base + (uint64_t)(2 * (int64_t)t.id[k] + 1) * kGamma;
-        if (left == kBlock && (t.flags[k] & VEC))
-            step_block<true, BITS8>(t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], t.flags[k], i0, left, lane, h, s,
-                                    key);
-        else
-            step_block<false, BITS8>(t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], t.flags[k], i0, left, lane, h,
-                                     s, key);
+        by_types(t.flags[k], left == kBlock, [&](auto v, auto pf, auto gf) {
+            step_block<decltype(v)::value, BITS8, decltype(pf)::value, decltype(gf)::value>(
+                t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], i0, left, lane, h, s, moments, params);
+        });
     }
 }
 
 // The values that 8-bit states stand for: m to p's tensor of the table, v to g's.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw_values(const __grid_constant__ Table<CAP> t)
+__global__ void __launch_bounds__(kThreads, kValueBlocksPerSm) k_adamw_values(const __grid_constant__ Table<CAP> t)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
@@ -368,10 +480,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw_values(const _
         if (rest <= 0) continue;
         const int left = (int)min((int64_t)kBlock, rest);
         const int flags = t.flags[k];
-        auto both = [&](auto tag) {
+        auto block = [&](auto tag) {
             constexpr bool V = decltype(tag)::value;
-            uint32_t cm[kPer], cv[kPer];
-            float x[kPer];
+            uint32_t cm[kPer / 4], cv[kPer / 4];
+            float2 x[kPairs];
             load_codes<V>(t.m[k], i0, left, lane, cm);
             load_codes<V>(t.v[k], i0, left, lane, cv);
             const float sm = t.ms[k][i0 / kBlock], sv = t.vs[k][i0 / kBlock];
@@ -381,9 +493,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw_values(const _
             store<V>(const_cast<void*>(t.g[k]), flags & G_F32, i0, left, lane, x);
         };
         if (left == kBlock && (flags & VEC))
-            both(std::true_type{});
+            block(std::true_type{});
         else
-            both(std::false_type{});
+            block(std::false_type{});
     }
 }
 
@@ -430,7 +542,7 @@ twell_status check_list(const twell_adamw_list* l)
 
 // f(table, blocks) for the list's tensors, CAP of them a launch. p and g of entry i: of(i, &p, &g, &flags).
 template <int CAP, class Of, class F>
-twell_status by_tables(const twell_adamw_list* l, int sms, Of of, F f)
+twell_status by_tables(const twell_adamw_list* l, int most, Of of, F f)
 {
     int next = 0;
     while (next < l->n) {
@@ -461,7 +573,6 @@ twell_status by_tables(const twell_adamw_list* l, int sms, Of of, F f)
         }
         if (t.n == 0) break;
         t.first[t.n] = (int32_t)units;
-        const int most = sms * kBlocksPerSm;
         count_launches(1);
         f(t, (int)(units < most ? units : most));
         if (cudaGetLastError() != cudaSuccess) return TWELL_ERR_CUDA;
@@ -482,7 +593,7 @@ extern "C" twell_status twell_adamw(const twell_adamw_list* list, const float* l
     if (ok != TWELL_OK) return ok;
     if (!lr || !step || !aligned(lr, 4) || !aligned(step, 4) || !aligned(norm, 4) || !(beta1 >= 0.0 && beta1 < 1.0) ||
         !(beta2 >= 0.0 && beta2 < 1.0) || !(eps > 0.0 && eps < INFINITY) || !(weight_decay >= 0.0 && weight_decay < INFINITY) ||
-        !((float)eps > 0.f) || (norm && !(max_norm >= 0.f)))
+        !((float)eps >= 0x1p-126f) || (norm && !(max_norm >= 0.f)))
         return TWELL_ERR_INVALID_ARG;
     if (list->n == 0) return TWELL_OK;
     const int sms = sms_current();
@@ -510,13 +621,13 @@ extern "C" twell_status twell_adamw(const twell_adamw_list* list, const float* l
         *flags = (uint8_t)((list->param_type[i] == TWELL_F32 ? P_F32 : 0) | (list->grad_type[i] == TWELL_F32 ? G_F32 : 0));
     };
     if (list->n <= kSmallTable)
-        return by_tables<kSmallTable>(list, sms, of, [&](const Table<kSmallTable>& t, int blocks) {
+        return by_tables<kSmallTable>(list, sms * kBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) {
             if (eight)
                 k_adamw<kSmallTable, true><<<blocks, kThreads, 0, s>>>(t, h);
             else
                 k_adamw<kSmallTable, false><<<blocks, kThreads, 0, s>>>(t, h);
         });
-    return by_tables<kTable>(list, sms, of, [&](const Table<kTable>& t, int blocks) {
+    return by_tables<kTable>(list, sms * kBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) {
         if (eight)
             k_adamw<kTable, true><<<blocks, kThreads, 0, s>>>(t, h);
         else
@@ -548,10 +659,10 @@ extern "C" twell_status twell_adamw_values(const twell_adamw_list* list, const t
         *flags = (uint8_t)((m_out->type[i] == TWELL_F32 ? P_F32 : 0) | (v_out->type[i] == TWELL_F32 ? G_F32 : 0));
     };
     if (list->n <= kSmallTable)
-        return by_tables<kSmallTable>(list, sms, of, [&](const Table<kSmallTable>& t, int blocks) {
+        return by_tables<kSmallTable>(list, sms * kValueBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) {
             k_adamw_values<kSmallTable><<<blocks, kThreads, 0, s>>>(t);
         });
-    return by_tables<kTable>(list, sms, of, [&](const Table<kTable>& t, int blocks) {
+    return by_tables<kTable>(list, sms * kValueBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) {
         k_adamw_values<kTable><<<blocks, kThreads, 0, s>>>(t);
     });
 }

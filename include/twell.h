@@ -542,7 +542,7 @@ twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint16_t* W_gate
  * lr [1] fp32 and step [1] int32 (t, 1 for the first step) are read on the device, so
  * that a captured call follows them; norm [1] fp32 as twell_grad_clip writes it (with
  * an infinite bound), or NULL: c = 1. Gradients are read only. With a norm that is not
- * finite, or a step below 1, the call changes nothing. beta1, beta2 in [0, 1), eps > 0, weight_decay >= 0.
+ * finite, or a step below 1, the call changes nothing. beta1, beta2 in [0, 1), eps >= 2^-126, weight_decay >= 0.
  * The list is a host struct of host arrays (read during the call): n tensors, device
  * addresses, element counts (>= 0). param and grad bf16 or fp32 (twell_dtype codes);
  * copy (the array or any entry may be NULL): a bf16 copy of an fp32 param. Tensors are
@@ -554,7 +554,7 @@ twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint16_t* W_gate
  * All zeros, codes and scales, are the states before the first step. Codes are rounded
  * up or down so that their mean is the value, and so is a bf16 param; a v above 0 never
  * becomes 0. The random bits are a function of (seed, step, tensor's place in the list,
- * element) alone. A block with a value that is not finite has a NaN scale.
+ * element) alone. A block with a value that is not finite, or above 15/16 2^127, has a NaN scale.
  * Limits of this build: 32768 tensors (TWELL_ERR_UNSUPPORTED).
  *
  * twell_adamw_values — the values that 8-bit states stand for, to the out tensors of
