@@ -33,6 +33,8 @@ struct MmLinear {
     int64_t ldo;
     bool out_f32;
     bool accumulate;         // out += (fp32 only; no res)
+    bool after_gated;        // the stream's launch before is launch_mm_gated's: it does not write W, so that W may be
+                             //   loaded while it still runs
     int32_t* status;
 };
 cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s);

@@ -81,6 +81,7 @@ extern "C" twell_status twell_dense_gated_ffn_fwd(const uint16_t* x, const uint1
     down.ldres = d;
     down.out[0] = y;
     down.ldo = d;
+    down.after_gated = true;
     down.status = status;
     if (e == cudaSuccess) e = launch_mm_linear(down, sms, s);
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;

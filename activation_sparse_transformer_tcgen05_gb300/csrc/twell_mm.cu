@@ -81,6 +81,7 @@ struct Args {
     const uint16_t *g_in, *u_in;
     float l1;
     float* part;
+    int early;                 // few rows: W does not come from the launch before, and may be loaded before that has ended
     int32_t* status;
 };
 enum { VEC_OUT = 1, VEC_RES = 2, VEC_PRE = 4 };
@@ -253,16 +254,18 @@ __device__ __forceinline__ void add_bias(const float* bias, int col, int cols, i
     }
 }
 
-// 32 rows x 128 columns from col0 on: bias, activation, residual.
-__device__ __forceinline__ void epi_linear(uint32_t taddr, int row0, int col0, int problem, const Args& a, Box& box)
+// 32 rows x `width` columns from col0 on: bias, activation, residual. read(offset, v): 64 sums of the lane's row from
+// col0 + offset on (those past the width may be anything).
+template <class Read>
+__device__ __forceinline__ void epi_linear(Read read, int width, int row0, int col0, int problem, const Args& a, Box& box)
 {
     const int rows = a.rowsA - row0;
 #pragma unroll 1
-    for (int ch = 0; ch < 2; ++ch) {
-        const int col = col0 + ch * 64, cols = a.rowsB - col;
+    for (int ch = 0; ch * 64 < width; ++ch) {
+        const int col = col0 + ch * 64, cols = min(a.rowsB - col, width - ch * 64);
         if (cols <= 0) break;
         float v[64];
-        read_columns(taddr + ch * 64, v);
+        read(ch * 64, v);
         add_bias(a.bias, col, cols, box.lane, v);
         if (a.pre) {
             box.put_bf16(v);
@@ -416,9 +419,41 @@ __device__ __forceinline__ void set_columns(uint32_t taddr, const float (&sum)[1
     tmem_st_wait();
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a)
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
 {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// LINEAR with few tiles: the pairs of a cluster have a part of the depth of one tile each. Every pair finishes its share
+// of the tile's columns: its own sums stay in tensor memory, the others' go to shared memory, in the place of the
+// operands' ring, and are read from there by the pair that needs them; parts are added in order. (4096 x 4096, 512 rows:
+// 25 us in one part, 20 in two; 1024 x 4096, 256 rows: 24 us in one, 18 in two, 16 in four.)
+// Four columns of a row lie together, then the rows, then the next four columns: a warp's 16-byte accesses touch 512
+// bytes in a row. (Rows apart, each lane's piece crossed the cluster by itself: 5 us more for each part.)
+__device__ __forceinline__ float* part_row(uint8_t* smem, int share, int owner, int row)
+{
+    return reinterpret_cast<float*>(smem) + (size_t)owner * HALF * share + row * 4;
+}
+
+// 32 sums of a row from the tile's column c0 on, for the pair that finishes them.
+__device__ __forceinline__ void put_part(uint8_t* smem, int share, int my_part, int row, int c0, const float* v)
+{
+    const int owner = c0 / share;
+    if (owner == my_part) return;
+    float4* to = reinterpret_cast<float4*>(part_row(smem, share, owner, row) + (c0 - owner * share) * HALF);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) to[c * HALF] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a, int parts_arg, int per)
+{
+    const int parts = EPI == LINEAR ? parts_arg : 1;
     using L = Smem;
     constexpr uint32_t IDESC =
         idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
@@ -438,10 +473,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
     volatile int* skip = reinterpret_cast<volatile int*>(tmem_slot + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t crank = cluster_rank(), rank = crank & 1u, lead = crank & ~1u;  // rank in the pair, its even CTA
+    const int my_part = (int)(crank >> 1);
+    const uint16_t both_ctas = (uint16_t)(3u << lead);
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        *skip = (leader && has_error(a.status)) ? 1 : 0;
+        *skip = (crank == 0 && has_error(a.status)) ? 1 : 0;
         *abort_flag = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -457,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
     cluster_sync();  // barriers of both CTAs initialised before either uses the other's
     const int sk = ld_cluster_s32(cluster_addr(const_cast<int*>(skip), 0));
     cluster_sync();  // the leader's flag has been read before anyone may leave
-    if (sk) return;  // an earlier kernel of this call failed; uniform over the pair
+    if (sk) return;  // an earlier kernel of this call failed; uniform over the cluster
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 2 * PAIR_N);
         tmem_relinquish_pair();
@@ -477,13 +514,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
     const int num_n = (a.rowsB + TILE_N - 1) / TILE_N;
     const int mn_tiles = num_m * num_n;
     const int num_tiles = mn_tiles * a.problems;
-    const int depth = a.num_kb * a.segments;
-    const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+    const int whole = a.num_kb * a.segments;
+    const int k0 = parts > 1 ? min(my_part * per, whole) : 0, k1 = parts > 1 ? min(k0 + per, whole) : whole;
+    const int depth = k1 - k0;  // of this pair
+    const int pair = (int)blockIdx.x / (2 * parts), num_pairs = (int)gridDim.x / (2 * parts);  // (in parts: one tile each)
+    Box box{smem + L::BOX_OFF + (warp >= 2 ? warp - 2 : 0) * kBox, lane};
+    int last_acc = 0;
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer ----
         if (lane == 0) {
-            const uint32_t full_leader = cluster_addr(full, 0);
+            const uint32_t full_leader = cluster_addr(full, lead);
             int stage = 0;
             uint32_t phase = 0;
             long long issued = 0;
@@ -495,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
                 const int ma = mb * PAIR_M + (int)rank * HALF;
                 // GATED: 128 rows of W_gate in the even CTA, the same rows of W_up in the odd one
                 const int nbr = EPI == GATED ? nb * HALF : nb * PAIR_N + (int)rank * HALF;
-                for (int seg = 0; ok && seg < a.segments; ++seg) {
+                for (int k = k0; ok && k < k1;) {
+                    const int seg = k / a.num_kb, end = min(k1, (seg + 1) * a.num_kb) - seg * a.num_kb;
                     const CUtensorMap* ta = &maps.a[problem + seg];
                     const CUtensorMap* tb = &maps.b[EPI == GATED ? (int)rank : problem + seg];
-                    for (int kb = 0; kb < a.num_kb; ++kb) {
+                    for (int kb = k - seg * a.num_kb; kb < end; ++kb, ++k) {
                         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
                             ok = false;
                             break;
@@ -563,28 +605,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
                             umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, ((kb - kb0) | k) != 0);
-                        umma_commit_pair(&empty[stage], 0x3);
+                        umma_commit_pair(&empty[stage], both_ctas);
                         if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!ok) break;
-                    umma_commit_pair(&tfull[acc], 0x3);
+                    umma_commit_pair(&tfull[acc], both_ctas);
                     acc ^= 1;
                     if (acc == 0) acc_phase ^= 1u;
                 }
             }
             if (!ok) fail(a.status, abort_flag);
-            umma_commit_pair(mma_done, 0x1);  // every product issued above has finished once this arrives
+            umma_commit_pair(mma_done, (uint16_t)(1u << lead));  // every product issued above has finished once this arrives
             mbar_wait(mma_done, 0, nullptr);
         }
     } else {
         // --------------------------------------------------- epilogue -----
         const int q = warp & 3;              // TMEM lane quarter this warp may read
         const int half = (warp - 2) >> 2;    // its 128 of the accumulator's columns
-        const uint32_t tempty_leader = cluster_addr(tempty, 0);
-        Box box{smem + L::BOX_OFF + (warp - 2) * kBox, lane};
+        const uint32_t tempty_leader = cluster_addr(tempty, lead);
         const uint32_t lanes_at = tmem_base + ((uint32_t)(32 * q) << 16);
         const bool pieces = EPI != GATED && depth > a.piece;
         int acc = 0;
@@ -626,10 +667,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
                     if (!ok) break;
                 }
             }
-            if (live) {
+            if (EPI == LINEAR && parts > 1) {
+                // (the pair's products are done: its ring is free)
+                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N);
+                last_acc = acc;
+                const int share = PAIR_N / parts;
+#pragma unroll 1
+                for (int c0 = 128 * half; c0 < 128 * half + 128; c0 += 32) {
+                    if (c0 / share == my_part) continue;
+                    float v[32];
+                    read_columns(at + (uint32_t)c0, v);
+                    put_part(smem, share, my_part, 32 * q + lane, c0, v);
+                }
+            } else if (live) {
                 const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N);
                 if constexpr (EPI == LINEAR)
-                    epi_linear(at + 128u * (uint32_t)half, row0, col0, problem, a, box);
+                    epi_linear([&](int c, float (&v)[64]) { read_columns(at + (uint32_t)(128 * half + c), v); }, 128, row0, col0,
+                               problem, a, box);
                 else if constexpr (EPI == GATED)
                     epi_gated(at + 64u * (uint32_t)half, row0, col0, a, box);
                 else
@@ -645,8 +699,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
         if (!ok) fail(a.status, abort_flag);
     }
 
+    if constexpr (EPI == LINEAR) {
+        if (parts > 1) {
+            __syncwarp();
+            tc_fence_before();
+            cluster_sync();
+            tc_fence_after();
+            if (warp >= 2 && !has_error(a.status)) {  // (a wait that ran out has left a part undefined)
+                const int q = warp & 3, half = (warp - 2) >> 2;
+                int mb, nb;
+                const int problem = pair / mn_tiles;
+                pair_tile_coords(pair - problem * mn_tiles, num_m, num_n, &mb, &nb);
+                const int share = PAIR_N / parts, width = share / 2;  // 64 or 32 columns of a warp
+                const int first = my_part * share + half * width;
+                const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q, col0 = nb * PAIR_N + first;
+                const uint32_t own = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(last_acc * PAIR_N + first);
+                if (row0 < a.rowsA && col0 < a.rowsB)
+                    epi_linear(
+                        [&](int c0, float (&v)[64]) {
+                            const float* mine = part_row(smem, share, my_part, 32 * q + lane) + (half * width + c0) * HALF;
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) v[c] = 0.f;
+#pragma unroll 1
+                            for (int p = 0; p < parts; ++p) {
+                                const uint32_t at = cluster_addr(mine, (uint32_t)(2 * p) + rank);
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if (h * 32 >= width) break;
+                                    float w[32];
+                                    if (p == my_part) {
+                                        read_columns(own + (uint32_t)(c0 + h * 32), w);
+                                    } else {
+#pragma unroll
+                                        for (int c = 0; c < 8; ++c) {
+                                            const float4 f = ld_cluster_f4(at + (uint32_t)((h * 32 + c * 4) * HALF * 4));
+                                            w[4 * c] = f.x, w[4 * c + 1] = f.y, w[4 * c + 2] = f.z, w[4 * c + 3] = f.w;
+                                        }
+                                    }
+#pragma unroll
+                                    for (int c = 0; c < 32; ++c) v[h * 32 + c] += w[c];
+                                }
+                            }
+                        },
+                        width, row0, col0, problem, a, box);
+            }
+        }
+    }
+
     // Neither CTA deallocates or exits while the pair's products, loads or arrivals may still touch the other's
-    // tensor or shared memory.
+    // tensor or shared memory, or the cluster's CTAs read its part.
     __syncwarp();
     tc_fence_before();
     cluster_sync();
@@ -659,44 +760,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
 // ---------------------------------------------------------------- few rows --
 //
 // One CTA: 128 rows of W (GATED: 64 of W_gate and the same 64 of W_up) x up to BN tokens x one part of the depth; a
-// cluster of `parts` CTAs has the whole depth. Two CTAs share an SM: their set-up and ends overlap, and both rings
-// together keep ~190 KB of W in flight, where 45 KB would cover the memory's latency at its rate.
+// cluster of `parts` CTAs has the whole depth. Two or three CTAs share an SM: set-up and ends overlap
+// with the others' loads.
 //   warp 0  loads, warp 1  tensor memory and products, warps 2-5  parts to shared memory; then all threads add the
 //   parts of their columns up and form the results.
 // An earlier error is only looked at before the results are stored: no CTA may leave its cluster early.
 
+// Lets the stream's next launch start if it waits for this one's end by itself (launch_wait).
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 constexpr int kFewThreads = 192;
 constexpr int kFewRows = 128;  // rows of W in a tile
 
+// Shared memory of a CTA: a ring of `stages`, then the barriers.
 template <int BN>
 struct FewSmem {
     static constexpr int W_BYTES = kFewRows * BK * 2;
-    static constexpr int X_BYTES = BN * BK * 2;
-    static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int STAGES = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
-    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
-    static constexpr int MISC_OFF = BAR_OFF + (2 * STAGES + 1) * 8;
-    static constexpr int TOTAL = MISC_OFF + 16 + 1024;  // + alignment slack
-    static constexpr int PIECES = BN <= 32 ? 8 : 256 / BN;  // accumulators
-    static constexpr uint32_t TMEM_COLS = PIECES * BN;
-    static_assert(2 * (TOTAL + 1024) <= 228 * 1024, "two CTAs on an SM");
-    static_assert(kFewRows * BN * 4 <= STAGES * STAGE_BYTES, "the parts take the ring's place");
+    static constexpr int STAGE_BYTES = W_BYTES + BN * BK * 2;
+    static constexpr int MOST = 5;  // stages
+    static constexpr int total(int stages) { return stages * STAGE_BYTES + (2 * MOST + 5) * 8 + 16 + 1024; }  // + alignment slack
+    // Two or three CTAs on an SM (each with 1 KB of the system's)
+    static constexpr int TWO = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
+    static constexpr int THREE = BN == 16 ? 4 : BN <= 64 ? 3 : 2;
+    // Accumulators. Up to 64 tokens: a second one for results in pieces, which the epilogue's threads add up in
+    // registers while the next piece is formed; with 128 (too many for registers) each piece has its own.
+    static constexpr bool DRAINED = BN <= 64;
+    static_assert(TWO <= MOST && 2 * (total(TWO) + 1024) <= 228 * 1024 && 3 * (total(THREE) + 1024) <= 228 * 1024, "the SM's");
+    static_assert(kFewRows * BN * 4 <= THREE * STAGE_BYTES, "the parts take the ring's place");
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr)
+// Four results of one row: neighbours, in one piece (VEC), or `apart` columns from one another, of which those with
+// col + e apart < n exist.
+template <bool VEC>
+__device__ __forceinline__ void few_store(void* out, bool f32, size_t at, int apart, int left, const float (&v)[4])
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Four results of one row, and where they go.
-__device__ __forceinline__ void few_store(void* out, bool f32, size_t at, int left, bool vec, const float (&v)[4])
-{
-    if (vec && left >= 4) {
+    if constexpr (VEC) {
         if (f32)
             *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(v[0], v[1], v[2], v[3]);
         else
@@ -704,17 +803,128 @@ __device__ __forceinline__ void few_store(void* out, bool f32, size_t at, int le
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if (e >= left) break;
+            if (e * apart >= left) break;
             if (f32)
-                static_cast<float*>(out)[at + e] = v[e];
+                static_cast<float*>(out)[at + e * apart] = v[e];
             else
-                static_cast<uint16_t*>(out)[at + e] = f32_to_bf16_bits(v[e]);
+                static_cast<uint16_t*>(out)[at + e * apart] = f32_to_bf16_bits(v[e]);
         }
     }
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// A CTA's share of its tile's results (`share` columns from `base` on, `tokens` rows), four a thread: neighbours where
+// everything lies on 16-byte boundaries, else a quarter of the share apart, so that lanes store neighbours.
+template <int EPI, bool VEC>
+__device__ __forceinline__ void few_finish(const float* part, int parts, int base, int share, int tokens, int row0, int col0,
+                                           const Args& a)
+{
+    const int per_row = share / 4, apart = VEC ? 1 : per_row;
+    for (int i = threadIdx.x; i < tokens * per_row; i += kFewThreads) {
+        const int t = i / per_row, c = base + (i - t * per_row) * (VEC ? 4 : 1), col = col0 + c;
+        const int left = a.rowsB - col;
+        if (left <= 0) continue;
+        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+        const float* from = part + t * kFewRows + c;
+        for (int r = 0; r < parts; ++r) {
+            const uint32_t addr = parts > 1 ? cluster_addr(from, (uint32_t)r) : smem_u32(from);
+            if constexpr (VEC) {
+                const float4 f = ld_cluster_f4(addr);
+                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
+                if constexpr (EPI == GATED) {
+                    const float4 w = ld_cluster_f4(addr + (kFewRows / 2) * 4);
+                    u[0] += w.x, u[1] += w.y, u[2] += w.z, u[3] += w.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += ld_cluster_f32(addr + (uint32_t)(e * apart * 4));
+            }
+        }
+        const size_t row = (size_t)row0 + t;
+        if (a.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (VEC || e * apart < left) v[e] += a.bias[col + e * apart];
+        }
+        if constexpr (EPI == GATED) {
+            const size_t at = row * a.ldo + col;
+            if (a.g) {
+                few_store<true>(a.g, false, at, 1, left, v);
+                few_store<true>(a.u, false, at, 1, left, u);
+            }
+            by_activation(a.act, [&](auto tag) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]) * u[e];
+            });
+            few_store<true>(a.h, false, at, 1, left, v);
+        } else {
+            if (a.pre) few_store<VEC>(a.pre, false, row * a.ldpre + col, apart, left, v);
+            if (a.act != TWELL_ACT_NONE)
+                by_activation(a.act, [&](auto tag) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]);
+                });
+            if (a.res) {
+                const size_t at = row * a.ldres + col;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (VEC || e * apart < left)
+                        v[e] += a.out_f32 ? static_cast<const float*>(a.res)[at + e * apart]
+                                          : bf16_to_f32(static_cast<const uint16_t*>(a.res)[at + e * apart]);
+            }
+            few_store<VEC>(a.out[0], a.out_f32, row * a.ldo + col, apart, left, v);
+        }
+    }
+}
+
+// The whole depth in one CTA (LINEAR): 16 tokens' results of a column, stored by the thread that has them in its
+// tensor memory lane. A warp's lanes are neighbouring columns of one row.
+__device__ __forceinline__ void few_direct(float (&v)[16], int tokens, size_t row, int col, float bias, const Args& a)
+{
+#pragma unroll
+    for (int c = 0; c < 16; ++c) v[c] += bias;
+    if (a.pre) {
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < tokens) a.pre[(row + c) * a.ldpre + col] = f32_to_bf16_bits(v[c]);
+    }
+    if (a.act != TWELL_ACT_NONE)
+        by_activation(a.act, [&](auto tag) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = activate<decltype(tag)::value>(v[c]);
+        });
+    if (a.out_f32) {
+        float* out = static_cast<float*>(a.out[0]);
+        if (a.res) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (c < tokens) v[c] += static_cast<const float*>(a.res)[(row + c) * a.ldres + col];
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < tokens) out[(row + c) * a.ldo + col] = v[c];
+    } else {
+        uint16_t* out = static_cast<uint16_t*>(a.out[0]);
+        if (a.res) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                if (c < tokens) v[c] += bf16_to_f32(static_cast<const uint16_t*>(a.res)[(row + c) * a.ldres + col]);
+        }
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < tokens) out[(row + c) * a.ldo + col] = f32_to_bf16_bits(v[c]);
+    }
+}
+
 template <int EPI, int BN, bool W_MN>
-__global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant__ Maps maps, const Args a, int parts, int per)
+__global__ void __launch_bounds__(kFewThreads, 3)
+    k_mm_few(const __grid_constant__ Maps maps, const Args a, int parts, int per, int stages, uint32_t tmem_cols)
 {
     using L = FewSmem<BN>;
     constexpr uint32_t IDESC = idesc_bf16_f32(kFewRows, BN) | (W_MN ? kIdescAMn : 0u);
@@ -722,28 +932,61 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
     constexpr int COLS = EPI == GATED ? kFewRows / 2 : kFewRows;  // output columns of a tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
-    uint64_t* empty = full + L::STAGES;
-    uint64_t* done = empty + L::STAGES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + stages * L::STAGE_BYTES);
+    uint64_t* empty = full + L::MOST;
+    uint64_t* done = empty + L::MOST;
+    uint64_t* tfull = done + 1;
+    uint64_t* tempty = tfull + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (EPI == GATED) launch_next();
     const int rank = parts > 1 ? (int)cluster_rank() : 0;
     const int col0 = (int)(blockIdx.x / (unsigned)parts) * COLS, row0 = (int)blockIdx.y * BN;
     const int depth = a.num_kb * a.segments;
     const int kb0 = min(rank * per, depth), kb1 = min(kb0 + per, depth);
+    const uint64_t once = l2_policy_evict_first();  // W goes by once
+    auto load_w = [&](int kb, int at) {
+        const int seg = kb / a.num_kb, x = (kb - seg * a.num_kb) * BK;
+        uint8_t* sw = smem + at * L::STAGE_BYTES;
+        mbar_arrive_expect_tx(&full[at], L::STAGE_BYTES);
+        if constexpr (EPI == GATED) {
+            tma_load_2d_hint(sw, &maps.b[0], x, col0, &full[at], once);
+            tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[1], x, col0, &full[at], once);
+        } else if constexpr (W_MN) {
+            tma_load_2d_hint(sw, &maps.b[seg], col0, x, &full[at], once);
+            tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[seg], col0 + kMnBox, x, &full[at], once);
+        } else {
+            tma_load_2d_hint(sw, &maps.b[seg], x, col0, &full[at], once);
+        }
+    };
+    auto load_x = [&](int kb, int at) {
+        const int seg = kb / a.num_kb;
+        tma_load_2d(smem + at * L::STAGE_BYTES + L::W_BYTES, &maps.a[seg], (kb - seg * a.num_kb) * BK, row0, &full[at]);
+    };
+    const int pieces = (kb1 - kb0 + a.piece - 1) / a.piece;
+    const bool drain = L::DRAINED && pieces > 1;
+    const int ahead = min(kb1 - kb0, stages);  // the ring's first round, which needs no wait
     if (threadIdx.x == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < L::STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
         fence_mbar_init();
+        // under way before the others are set up; the tokens' rows when the launch before has ended
+        for (int i = 0; i < ahead; ++i) load_w(kb0 + i, i);
+        if (!a.early)
+            for (int i = 0; i < ahead; ++i) load_x(kb0 + i, i);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, L::TMEM_COLS);
+        tmem_alloc(tmem_slot, tmem_cols);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -754,28 +997,20 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
-            const uint64_t once = l2_policy_evict_first();  // W goes by once
+            if (a.early) {
+                launch_wait();
+                for (int i = 0; i < ahead; ++i) load_x(kb0 + i, i);
+            }
             int stage = 0;
             uint32_t phase = 0;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag)) {
+            for (int kb = kb0 + ahead; kb < kb1; ++kb) {  // (ahead = stages, or nothing is left)
+                if (!mbar_wait(&empty[stage], phase, abort_flag)) {
                     ok = false;
                     break;
                 }
-                const int seg = kb / a.num_kb, x = (kb - seg * a.num_kb) * BK;
-                uint8_t* sw = smem + stage * L::STAGE_BYTES;
-                mbar_arrive_expect_tx(&full[stage], L::STAGE_BYTES);
-                if constexpr (EPI == GATED) {
-                    tma_load_2d_hint(sw, &maps.b[0], x, col0, &full[stage], once);
-                    tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[1], x, col0, &full[stage], once);
-                } else if constexpr (W_MN) {
-                    tma_load_2d_hint(sw, &maps.b[seg], col0, x, &full[stage], once);
-                    tma_load_2d_hint(sw + L::W_BYTES / 2, &maps.b[seg], col0 + kMnBox, x, &full[stage], once);
-                } else {
-                    tma_load_2d_hint(sw, &maps.b[seg], x, col0, &full[stage], once);
-                }
-                tma_load_2d(sw + L::W_BYTES, &maps.a[seg], x, row0, &full[stage]);
-                if (++stage == L::STAGES) {
+                load_w(kb, stage);
+                load_x(kb, stage);
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -793,16 +1028,25 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
                     break;
                 }
                 tc_fence_after();
-                const int i = kb - kb0, piece = i / a.piece;
-                const uint32_t d_tmem = tmem_base + (uint32_t)(piece * BN);
+                const int i = kb - kb0, piece = i / a.piece, in_piece = i - piece * a.piece;
+                const int acc = drain ? piece & 1 : piece;
+                if (drain && in_piece == 0 && piece >= 2) {  // its last sums have been read
+                    if (!mbar_wait(&tempty[acc], (uint32_t)((piece >> 1) & 1) ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
                 const uint32_t sw = smem_u32(smem + stage * L::STAGE_BYTES);
                 const uint64_t wdesc = operand_desc(W_MN, sw);
                 const uint64_t xdesc = sw128_kmajor_desc(sw + L::W_BYTES);
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k)
-                    umma_bf16(d_tmem, wdesc + W_KSTEP * k, xdesc + 2u * k, IDESC, ((i - piece * a.piece) | k) != 0);
+                    umma_bf16(d_tmem, wdesc + W_KSTEP * k, xdesc + 2u * k, IDESC, (in_piece | k) != 0);
                 umma_commit(&empty[stage]);
-                if (++stage == L::STAGES) {
+                if (drain && (in_piece == a.piece - 1 || kb == kb1 - 1)) umma_commit(&tfull[acc]);
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -811,14 +1055,37 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
             umma_commit(done);
         }
     }
+    const uint32_t lanes_at = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16);
+    float sum[L::DRAINED ? BN : 1];
+    if constexpr (L::DRAINED) {
+        if (warp >= 2 && drain) {
+#pragma unroll
+            for (int c = 0; c < BN; ++c) sum[c] = 0.f;
+            for (int p = 0; p < pieces; ++p) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&tfull[p & 1], (uint32_t)(p >> 1) & 1u, abort_flag))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c0 = 0; c0 < BN; c0 += 16) {
+                    uint32_t v[16];
+                    tmem_ld16_wait(lanes_at + (uint32_t)((p & 1) * BN + c0), v);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) sum[c0 + c] += __uint_as_float(v[c]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[p & 1]);
+            }
+        }
+    }
     __syncwarp();
+    if (a.early) launch_wait();  // nothing of the launch before is read, and nothing written, ahead of this
     // Every load has landed when the products that read it are done, so the ring is free from here on. (Loads in
     // flight after a wait that ran out still land in it: the results are not used then, but the CTA must not end.)
     bool ok = mbar_wait(done, 0, nullptr);
     if (!ok) fail(a.status, abort_flag);
     if (__syncthreads_or(*abort_flag)) {
         if (threadIdx.x == 0)
-            for (int s = 0; s < L::STAGES; ++s) {
+            for (int s = 0; s < stages; ++s) {
                 mbar_wait(&full[s], 0, nullptr);
                 mbar_wait(&full[s], 1, nullptr);
             }
@@ -826,24 +1093,45 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
     }
     tc_fence_after();
     float* part = reinterpret_cast<float*>(smem);  // [token][kFewRows]
+    const bool direct = EPI == LINEAR && parts == 1;
     const int tokens = min(BN, a.rowsA - row0);
     if (warp >= 2) {
-        const int q = warp & 3;
-        const int pieces = (kb1 - kb0 + a.piece - 1) / a.piece;
-        const uint32_t at = tmem_base + ((uint32_t)(32 * q) << 16);
-#pragma unroll 1
-        for (int c0 = 0; c0 < tokens; c0 += 16) {
-            float sum[16];
+        const int row = 32 * (warp & 3) + lane, col = col0 + row;
+        const bool failed = direct && has_error(a.status);
+        const float bias = direct && a.bias && col < a.rowsB ? a.bias[col] : 0.f;
+        auto put16 = [&](int c0, float (&v)[16]) {
+            if (direct) {
+                if (col < a.rowsB && !failed) few_direct(v, tokens - c0, (size_t)row0 + c0, col, bias, a);
+            } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) sum[c] = 0.f;
-            for (int p = 0; p < pieces; ++p) {
-                uint32_t v[16];
-                tmem_ld16_wait(at + (uint32_t)(p * BN + c0), v);
-#pragma unroll
-                for (int c = 0; c < 16; ++c) sum[c] += __uint_as_float(v[c]);
+                for (int c = 0; c < 16; ++c) part[(c0 + c) * kFewRows + row] = v[c];
             }
+        };
+        if (drain) {
+            if constexpr (L::DRAINED) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) part[(c0 + c) * kFewRows + 32 * q + lane] = sum[c];
+                for (int c0 = 0; c0 < BN; c0 += 16) {
+                    if (c0 >= tokens) break;
+                    float v[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] = sum[c0 + c];
+                    put16(c0, v);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int c0 = 0; c0 < tokens; c0 += 16) {
+                float v[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = 0.f;
+                for (int p = 0; p < pieces; ++p) {
+                    uint32_t w[16];
+                    tmem_ld16_wait(lanes_at + (uint32_t)(p * BN + c0), w);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) v[c] += __uint_as_float(w[c]);
+                }
+                put16(c0, v);
+            }
         }
         tc_fence_before();
     }
@@ -853,60 +1141,14 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
     else
         __syncthreads();
 
-    // this CTA's share of the tile's columns, four at a time; parts in the cluster's order
+    // this CTA's share of the tile's columns; parts in the cluster's order
     const int share = COLS / parts;
     const int base = rank * share;
-    if (!has_error(a.status)) {
-        for (int i = threadIdx.x; i < tokens * (share / 4); i += kFewThreads) {
-            const int t = i / (share / 4), c = base + (i - t * (share / 4)) * 4;
-            const int col = col0 + c, left = a.rowsB - col;
-            if (left <= 0) continue;
-            float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = 0; r < parts; ++r) {
-                const float* from = part + t * kFewRows + c;
-                const uint32_t addr = parts > 1 ? cluster_addr(from, (uint32_t)r) : smem_u32(from);
-                const float4 f = ld_cluster_f4(addr);
-                v[0] += f.x, v[1] += f.y, v[2] += f.z, v[3] += f.w;
-                if constexpr (EPI == GATED) {
-                    const float4 w = ld_cluster_f4(addr + (kFewRows / 2) * 4);
-                    u[0] += w.x, u[1] += w.y, u[2] += w.z, u[3] += w.w;
-                }
-            }
-            const size_t row = (size_t)row0 + t;
-            if (a.bias) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (e < left) v[e] += a.bias[col + e];
-            }
-            if constexpr (EPI == GATED) {
-                const size_t at = row * a.ldo + col;
-                if (a.g) {
-                    few_store(a.g, false, at, left, true, v);
-                    few_store(a.u, false, at, left, true, u);
-                }
-                by_activation(a.act, [&](auto tag) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]) * u[e];
-                });
-                few_store(a.h, false, at, left, true, v);
-            } else {
-                if (a.pre) few_store(a.pre, false, row * a.ldpre + col, left, a.vec & VEC_PRE, v);
-                if (a.act != TWELL_ACT_NONE)
-                    by_activation(a.act, [&](auto tag) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]);
-                    });
-                if (a.res) {
-                    const size_t at = row * a.ldres + col;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < left)
-                            v[e] += a.out_f32 ? static_cast<const float*>(a.res)[at + e]
-                                              : bf16_to_f32(static_cast<const uint16_t*>(a.res)[at + e]);
-                }
-                few_store(a.out[0], a.out_f32, row * a.ldo + col, left, a.vec & VEC_OUT, v);
-            }
-        }
+    if (!direct && !has_error(a.status)) {
+        if (EPI == GATED || (a.vec & VEC_OUT && (!a.pre || a.vec & VEC_PRE)))
+            few_finish<EPI, true>(part, parts, base, share, tokens, row0, col0, a);
+        else
+            few_finish<EPI, false>(part, parts, base, share, tokens, row0, col0, a);
     }
     __syncwarp();
     // no CTA ends while another may still read its part
@@ -916,7 +1158,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) k_mm_few(const __grid_constant
         __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, L::TMEM_COLS);
+        tmem_dealloc(tmem_base, tmem_cols);
     }
 }
 
@@ -965,26 +1207,40 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // clusters of two that can be resident at once
-    static int known[64] = {0};
+    // clusters of 2, 4 and 8 CTAs that can be resident at once
+    static int known[64][3] = {{0}};
     int dev = 0;
     e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (known[dev] <= 0) {
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
-        if (e != cudaSuccess) return e;
-        if (n <= 0) return cudaErrorNotSupported;
-        known[dev] = n;
+    if (known[dev][0] <= 0) {
+        for (int i = 2; i >= 0; --i) {  // (the first entry last: it says that all are known)
+            if (i > 0 && EPI != LINEAR) continue;
+            int n = 0;
+            attr[0].val.clusterDim.x = 2u << i;
+            cfg.gridDim = dim3(2u << i, 1, 1);
+            e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+            if (e != cudaSuccess && i == 0) return e;
+            if (e != cudaSuccess) (void)cudaGetLastError();
+            if (n <= 0 && i == 0) return cudaErrorNotSupported;
+            known[dev][i] = e == cudaSuccess ? n : 0;
+        }
     }
     constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;
     const int64_t tiles =
         ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + TILE_N - 1) / TILE_N) * a.problems;
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    cfg.gridDim = dim3(2 * (unsigned)(tiles < known[dev] ? tiles : known[dev]), 1, 1);
+    // Few tiles: the depth in as many parts as run at once, if none is shorter than 12 k-blocks (joining takes about
+    // 2.5 us for each part more, as long as 9 k-blocks); so no part is empty.
+    const int depth = a.num_kb * a.segments;
+    int parts = 1;
+    for (int i = 1; i <= 2; ++i)
+        if (EPI == LINEAR && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
+    const int per = (depth + parts - 1) / parts;
+    attr[0].val.clusterDim.x = 2u * (unsigned)parts;
+    cfg.gridDim = dim3(2u * (unsigned)parts * (unsigned)(parts > 1 || tiles < known[dev][0] ? tiles : known[dev][0]), 1, 1);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kern, maps, a);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per);
 }
 
 // Rows up to which the weights' rows are the tensor cores' 128-row operand.
@@ -1003,33 +1259,39 @@ cudaError_t run_few(const Maps& maps, Args a, int sms, cudaStream_t s)
 {
     using L = FewSmem<BN>;
     auto kern = k_mm_few<EPI, BN, W_MN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::TOTAL);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::total(L::MOST));
     if (e != cudaSuccess) return e;
     constexpr int COLS = EPI == GATED ? kFewRows / 2 : kFewRows;
     const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
     const int blocks = (a.rowsA + BN - 1) / BN, depth = a.num_kb * a.segments;
     const int parts = few_parts(tiles * blocks, depth, sms), per = (depth + parts - 1) / parts;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
-    // fp32 results in pieces of 512 of depth, or as many as there are accumulators for
+    // fp32 results in pieces of 512 of depth (2 to 3 units lost in each), or two of any length
     a.piece = per;
-    if (a.out_f32) {
-        const int least = (per + L::PIECES - 1) / L::PIECES;
-        a.piece = least > 8 ? least : 8;
-    }
-    cudaLaunchAttribute attr[1];
+    if (a.out_f32) a.piece = L::DRAINED || (per + 1) / 2 < 8 ? 8 : (per + 1) / 2;
+    const int held = per > a.piece ? 2 : 1;  // accumulators
+    uint32_t cols = 32;
+    while (cols < (uint32_t)(held * BN)) cols *= 2;
+    // More CTAs than two on each SM: a third one there, with shorter rings, if tensor memory has room. (64 rows x 50000 x
+    // 2048: 46 us with two, 38.5 with three; the gated layer's 224 tiles of 4096 x 14336 58 us with long rings, 61.)
+    const bool three = tiles * parts * blocks > 2 * sms && 3 * cols <= 512;
+    const int stages = three ? L::THREE : L::TWO;
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)parts;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * parts), (unsigned)blocks, 1);
     cfg.blockDim = dim3(kFewThreads, 1, 1);
-    cfg.dynamicSmemBytes = L::TOTAL;
+    cfg.dynamicSmemBytes = (size_t)L::total(stages);
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.early ? 2 : 1;
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per);
+    return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per, stages, cols);
 }
 
 // Tokens a tile holds for this many rows.
@@ -1084,6 +1346,7 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     for (int i = 0; i < m.problems; ++i) out_vec = out_vec && pieces_of_16(m.out[i], m.ldo, m.N, es);
     a.vec = (out_vec ? VEC_OUT : 0) | (m.res && pieces_of_16(m.res, m.ldres, m.N, es) ? VEC_RES : 0) |
             (m.pre && pieces_of_16(m.pre, m.ldpre, m.N, 2) ? VEC_PRE : 0);
+    a.early = few && m.after_gated;
     a.status = m.status;
     const bool amn = m.a[0].mn, bmn = m.b[0].mn;
     if (few) return bmn ? run_few_rows<LINEAR, true>(maps, a, sms, s) : run_few_rows<LINEAR, false>(maps, a, sms, s);
