@@ -2,40 +2,66 @@
 //
 //   relu       max(z, 0), derivative [z > 0] (NaN counts as inactive, as in the packed layer)
 //   silu       z s(z), s(z) = 1 / (1 + e^-z)
-//   gelu       z P(z), P the normal distribution function = (1 + erf(z / sqrt 2)) / 2
+//   gelu       z P(z), P the normal distribution function; derivative P(z) + z e^(-z^2 / 2) / sqrt(2 pi)
 //   gelu_tanh  z (1 + tanh i) / 2 = z s(2 i), i = sqrt(2 / pi) (z + 0.044715 z^3)
 // All in fp32. The exponential and the quotient are the fast ones: within 4e-7 of
-// the value for |z| < 6, where s matters, a hundredth of a bf16 rounding.
+// the value for |z| < 6, where s matters, a hundredth of a bf16 rounding. P's tail is
+// Hastings' rational approximation (Abramowitz and Stegun, 7.1.26), within 8e-8: a
+// polynomial in 1 / (1 + p |z| / sqrt 2) times the e^(-z^2 / 2) that the derivative
+// needs anyway. (With erff the epilogue of the backward's first product was longer than
+// the product itself: 777 x 1000 x 2696 37 us.)
 #pragma once
 
 #include "common.cuh"
 
 namespace twell {
 
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// (of 1 to infinity)
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// act(z); da: act'(z).
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 exp2_pair(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+__device__ __forceinline__ float2 reciprocal_pair(float2 x) { return make_float2(reciprocal(x.x), reciprocal(x.y)); }
+
+// act(z) of two values, for the instructions that work on two at once (half the instructions of the epilogues, and of
+// the pass over dy and the pre-activations); da: act'(z).
 template <int ACT>
-__device__ __forceinline__ float activate(float z, float* da = nullptr)
+__device__ __forceinline__ float2 activate(float2 z, float2* da = nullptr)
 {
     if constexpr (ACT == TWELL_ACT_RELU) {
-        if (da) *da = z > 0.f ? 1.f : 0.f;
-        return z > 0.f ? z : 0.f;
+        if (da) *da = make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+        return make_float2(z.x > 0.f ? z.x : 0.f, z.y > 0.f ? z.y : 0.f);
     } else if constexpr (ACT == TWELL_ACT_SILU) {
-        const float s = logistic(z);
-        if (da) *da = s * fmaf(z, 1.f - s, 1.f);
-        return z * s;
+        const float2 s = reciprocal_pair(__fadd2_rn(exp2_pair(__fmul2_rn(z, pair(-1.44269504f))), pair(1.f)));
+        if (da) *da = __fmul2_rn(s, __ffma2_rn(z, __ffma2_rn(s, pair(-1.f), pair(1.f)), pair(1.f)));
+        return __fmul2_rn(z, s);
     } else if constexpr (ACT == TWELL_ACT_GELU) {
-        const float p = fmaf(0.5f, erff(z * 0.70710678f), 0.5f);
-        if (da) *da = fmaf(z * 0.39894228f, __expf(-0.5f * z * z), p);
-        return z * p;
+        const float2 e = exp2_pair(__fmul2_rn(__fmul2_rn(z, z), pair(-0.72134752f)));  // e^(-z^2 / 2)
+        const float2 t = reciprocal_pair(__ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), pair(0.23164189f), pair(1.f)));
+        float2 q = __ffma2_rn(t, pair(0.530702714f), pair(-0.726576013f));  // half of Hastings' coefficients
+        q = __ffma2_rn(t, q, pair(0.710706871f));
+        q = __ffma2_rn(t, q, pair(-0.142248368f));
+        q = __fmul2_rn(__fmul2_rn(__ffma2_rn(t, q, pair(0.127414796f)), t), e);
+        const float2 o = __ffma2_rn(q, pair(-1.f), pair(1.f));
+        const float2 p = make_float2(z.x < 0.f ? q.x : o.x, z.y < 0.f ? q.y : o.y);
+        if (da) *da = __ffma2_rn(__fmul2_rn(z, pair(0.39894228f)), e, p);
+        return __fmul2_rn(z, p);
     } else if constexpr (ACT == TWELL_ACT_GELU_TANH) {
-        const float k2 = 1.59576912f;  // 2 sqrt(2 / pi)
-        const float s = logistic(k2 * fmaf(0.044715f * z * z, z, z));
-        if (da) *da = fmaf(z * s * (1.f - s), k2 * fmaf(0.134145f * z, z, 1.f), s);
-        return z * s;
+        const float k = 1.59576912f;  // 2 sqrt(2 / pi)
+        const float2 z2 = __fmul2_rn(z, z);
+        const float2 i = __fmul2_rn(__ffma2_rn(z2, pair(-1.44269504f * k * 0.044715f), pair(-1.44269504f * k)), z);
+        const float2 s = reciprocal_pair(__fadd2_rn(exp2_pair(i), pair(1.f))), zs = __fmul2_rn(z, s);
+        if (da)
+            *da = __ffma2_rn(__fmul2_rn(zs, __ffma2_rn(s, pair(-1.f), pair(1.f))),
+                             __ffma2_rn(z2, pair(k * 0.134145f), pair(k)), s);
+        return zs;
     } else {
-        if (da) *da = 1.f;
+        if (da) *da = pair(1.f);
         return z;
     }
 }

@@ -62,13 +62,15 @@ __global__ void __launch_bounds__(kDpreThreads)
                     z[0] = p.x, z[1] = p.y, z[2] = p.z, z[3] = p.w;
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    d[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+                for (int e = 0; e < 8; e += 2) {
+                    float2 g = make_float2(bf16_lo(w[e >> 1]), bf16_hi(w[e >> 1]));
                     if (ACT != TWELL_ACT_NONE) {
-                        float da;
-                        activate<ACT>((e & 1) ? bf16_hi(z[e >> 1]) : bf16_lo(z[e >> 1]), &da);
-                        d[e] *= da;
+                        float2 da;
+                        activate<ACT>(make_float2(bf16_lo(z[e >> 1]), bf16_hi(z[e >> 1])), &da);
+                        g = __fmul2_rn(g, da);
                     }
+                    d[e] = g.x;
+                    d[e + 1] = g.y;
                 }
                 if (out)
                     *reinterpret_cast<uint4*>(out + row * ldout + c) =
@@ -77,9 +79,9 @@ __global__ void __launch_bounds__(kDpreThreads)
             } else {
                 d[0] = bf16_to_f32(dy[row * lddy + c]);
                 if (ACT != TWELL_ACT_NONE) {
-                    float da;
-                    activate<ACT>(bf16_to_f32(pre[row * ldpre + c]), &da);
-                    d[0] *= da;
+                    float2 da;
+                    activate<ACT>(pair(bf16_to_f32(pre[row * ldpre + c])), &da);
+                    d[0] *= da.x;
                 }
                 if (out) out[row * ldout + c] = f32_to_bf16_bits(d[0]);
             }

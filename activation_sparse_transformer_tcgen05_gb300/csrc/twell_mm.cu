@@ -21,9 +21,9 @@
 // (k_mm_few). Bound by memory: the depth is split over a cluster of CTAs until the whole GPU
 // streams, and the parts are added up through the cluster's shared memory, in order.
 //
-// Roles as in twell_gemm.cu: warp 0 loads, warp 1 (even CTA) issues the products, eight
-// warps form the results of 32 rows x 128 columns each and store them through 4 KB of
-// their own shared memory, whole 128-byte pieces of rows at a time.
+// Roles as in twell_gemm.cu: warp 0 loads, warp 1 (even CTA) issues the products, 8 or 16
+// warps form the results of 32 rows x 128 or 64 columns each and store them through 4 KB of
+// their own shared memory, whole pieces of rows at a time.
 #include "activation.cuh"
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -35,17 +35,22 @@ namespace {
 
 enum Epilogue { LINEAR, GATED, GATED_BWD };
 
-constexpr int kStages = 6;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kBox = 4096;  // 32 rows x 128 bytes of one epilogue warp
 
+// GATED_BWD's results take the longest to form (two matrices in, two out, column sums): 16 warps of 64 columns, and a
+// ring one stage shorter for their boxes. With eight of 128 the epilogue took longer than a tile's products (8192 x 4096 x
+// 14336 807 us; with 16, and g and u asked for early, 700).
+template <int EPI>
 struct Smem {
+    static constexpr int STAGES = EPI == GATED_BWD ? 5 : 6;
+    static constexpr int WARPS = EPI == GATED_BWD ? 16 : 8;    // of the epilogue
+    static constexpr int COLS = EPI == LINEAR ? 128 : 64;      // output columns of one of them
+    static constexpr int THREADS = 64 + 32 * WARPS;
     static constexpr int A_BYTES = HALF * BK * 2;
     static constexpr int STAGE_BYTES = 2 * A_BYTES;
-    static constexpr int BOX_OFF = kStages * STAGE_BYTES;
-    static constexpr int BAR_OFF = BOX_OFF + kEpiWarps * kBox;
-    static constexpr int NBARS = 2 * kStages + 5;
+    static constexpr int BOX_OFF = STAGES * STAGE_BYTES;
+    static constexpr int BAR_OFF = BOX_OFF + WARPS * kBox;
+    static constexpr int NBARS = 2 * STAGES + 5;
     static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
     static constexpr int TOTAL = MISC_OFF + 16 + 1024;  // + alignment slack
     static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
@@ -99,7 +104,8 @@ struct Box {
     int lane;
     __device__ __forceinline__ uint4* at(int row, int c) const
     {
-        return reinterpret_cast<uint4*>(box + row * 128 + ((c ^ (row & 7)) << 4));
+        // (eight rows' same piece, two rows' same four and one row's eight each touch all banks)
+        return reinterpret_cast<uint4*>(box + row * 128 + ((c ^ ((row & 1) << 2 | (row >> 1 & 3))) << 4));
     }
     __device__ __forceinline__ void put(int c, const uint4& v) { *at(lane, c) = v; }
     __device__ __forceinline__ uint4 get(int c) const { return *at(lane, c); }
@@ -192,25 +198,7 @@ struct Box {
     }
 
     // Two bf16 matrices of one layout side by side: 32 columns of the first in pieces 0 to 3, of the second in 4 to
-    // 7. `at` is the element of row 0 and column 0, rows have `ld` elements and 16-byte pieces.
-    __device__ __forceinline__ void load_two(const uint16_t* m0, const uint16_t* m1, size_t at, int64_t ld, int rows, int cols)
-    {
-        const int c = lane & 3, r0 = lane >> 2;
-        uint4 q[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool ok = c * 8 < cols && i * 8 + r0 < rows;
-            const size_t o = at + (size_t)(i * 8 + r0) * ld + c * 8;
-            q[i] = ok ? *reinterpret_cast<const uint4*>(m0 + o) : make_uint4(0, 0, 0, 0);
-            q[4 + i] = ok ? *reinterpret_cast<const uint4*>(m1 + o) : make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            *this->at(i * 8 + r0, c) = q[i];
-            *this->at(i * 8 + r0, 4 + c) = q[4 + i];
-        }
-        __syncwarp();
-    }
+    // 7. `at` is the element of row 0 and column 0, rows have `ld` elements and lie on 16-byte boundaries.
     __device__ __forceinline__ void store_two(uint16_t* m0, uint16_t* m1, size_t at, int64_t ld, int rows, int cols)
     {
         __syncwarp();
@@ -238,6 +226,17 @@ __device__ __forceinline__ void read_columns(uint32_t taddr, float (&v)[N])
         tmem_ld32_wait(taddr + ch * 32, r);
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[ch * 32 + c] = __uint_as_float(r[c]);
+    }
+}
+
+template <int ACT, int N>
+__device__ __forceinline__ void activate_all(float (&v)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+        const float2 y = activate<ACT>(make_float2(v[c], v[c + 1]));
+        v[c] = y.x;
+        v[c + 1] = y.y;
     }
 }
 
@@ -273,8 +272,7 @@ __device__ __forceinline__ void epi_linear(Read read, int width, int row0, int c
         }
         if (a.act != TWELL_ACT_NONE)
             by_activation(a.act, [&](auto tag) {
-#pragma unroll
-                for (int c = 0; c < 64; ++c) v[c] = activate<decltype(tag)::value>(v[c]);
+                activate_all<decltype(tag)::value>(v);
             });
         if (a.out_f32) {
 #pragma unroll
@@ -345,7 +343,11 @@ __device__ __forceinline__ void epi_gated(uint32_t taddr, int row0, int col, con
         }
         by_activation(a.act, [&](auto tag) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) g[c] = activate<decltype(tag)::value>(g[c]) * u[c];
+            for (int c = 0; c < 32; c += 2) {
+                const float2 h = __fmul2_rn(activate<decltype(tag)::value>(make_float2(g[c], g[c + 1])), make_float2(u[c], u[c + 1]));
+                g[c] = h.x;
+                g[c + 1] = h.y;
+            }
         });
 #pragma unroll
         for (int c = 0; c < 4; ++c) h[ch * 4 + c] = Box::pack8(g + c * 8);
@@ -355,62 +357,133 @@ __device__ __forceinline__ void epi_gated(uint32_t taddr, int row0, int col, con
     box.store<2>(a.h + (size_t)row0 * a.ldo + col, (size_t)a.ldo * 2, rows, cols, true);
 }
 
-// 32 rows x 128 hidden units from col0 on of dh. Rows and columns outside have g = u = 0 and dh = 0, so dg = du = 0.
-__device__ __forceinline__ void epi_gated_bwd(uint32_t taddr, int row0, int col0, const Args& a, Box& box)
+// GATED_BWD: g and u come into a warp's shared memory by asynchronous copies, 16 columns of both at a time, while the 16
+// columns before are worked on (those of the next tile too): two halves of a box, each 32 rows of 64 bytes (g's two
+// pieces, then u's), which dg and du take the place of on their way out. (Loaded when their turn came, they were two
+// fifths of the epilogue: 8192 x 512 x 14336 337 us, 201 without.)
+struct HalfBox {
+    uint8_t* box;
+    int lane;
+    __device__ __forceinline__ uint4* at(int half, int row, int c) const
+    {
+        // (eight rows' same piece and two rows' all four touch all banks)
+        return reinterpret_cast<uint4*>(box + half * 2048 + row * 64 + ((c ^ (row >> 1 & 3)) << 4));
+    }
+    // Lane's place in a matrix for rows i * 8 + lane / 4: pieces 0 and 1 are the first matrix's, 2 and 3 the second's.
+    __device__ __forceinline__ int piece() const { return lane & 3; }
+
+    // Asks for rows row0 .. row0 + 31 and columns col .. col + 15; what lies outside becomes 0.
+    __device__ __forceinline__ void fetch(int half, int row0, int col, const Args& a) const
+    {
+        const int c = piece(), r0 = lane >> 2;
+        const uint16_t* m = c < 2 ? a.g_in : a.u_in;
+        const int mc = col + (c & 1) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + i * 8 + r0;
+            const bool ok = row < a.rowsA && mc < a.rowsB;
+            const uint16_t* from = ok ? m + (size_t)row * a.ldo + mc : m;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(half, i * 8 + r0, c))), "l"(from),
+                         "r"(ok ? 16 : 0)
+                         : "memory");
+        }
+    }
+    __device__ __forceinline__ void store(int half, int row0, int col, const Args& a) const
+    {
+        const int c = piece(), r0 = lane >> 2;
+        uint16_t* m = c < 2 ? a.g : a.u;
+        const int mc = col + (c & 1) * 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = row0 + i * 8 + r0;
+            if (row < a.rowsA && mc < a.rowsB) *reinterpret_cast<uint4*>(m + (size_t)row * a.ldo + mc) = *at(half, i * 8 + r0, c);
+        }
+    }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last group have landed.
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// l1 with the sign of act u, 0 where either is 0.
+__device__ __forceinline__ float l1_term(float l1, float act, float u)
 {
-    const int rows = a.rowsA - row0;
+    const uint32_t sign = (__float_as_uint(act) ^ __float_as_uint(u)) & 0x80000000u;
+    return act != 0.f && u != 0.f ? __uint_as_float(__float_as_uint(l1) ^ sign) : 0.f;
+}
+
+// 32 rows x 64 hidden units from col0 on of dh, the first 16 columns of g and u already asked for. next_row0, next_col0:
+// where the next tile's begin (next_row0 < 0: there is none). Rows and columns outside have g = u = 0 and dh = 0, so
+// dg = du = 0.
+__device__ __forceinline__ void epi_gated_bwd(uint32_t taddr, int row0, int col0, int next_row0, int next_col0, const Args& a,
+                                              const HalfBox& box)
+{
 #pragma unroll 1
     for (int ch = 0; ch < 4; ++ch) {
-        const int col = col0 + ch * 32, cols = a.rowsB - col;
-        if (cols <= 0) break;
-        const size_t at = (size_t)row0 * a.ldo + col;
-        box.load_two(a.g_in, a.u_in, at, a.ldo, rows, cols);
-        float dg[32], du[32];
-        read_columns(taddr + ch * 32, du);
+        const int col = col0 + ch * 16, half = ch & 1, lane = box.lane;
+        if (ch < 3)
+            box.fetch(half ^ 1, row0, col + 16, a);
+        else if (next_row0 >= 0)
+            box.fetch(half ^ 1, next_row0, next_col0, a);
+        copies_commit();
+        uint32_t dh[16];
+        tmem_ld16_wait(taddr + ch * 16, dh);
+        copies_wait();
+        __syncwarp();
+        float dg[16];
         by_activation(a.act, [&](auto tag) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint4 qg = box.get(c), qu = box.get(4 + c);
+            for (int c = 0; c < 2; ++c) {
+                const uint4 qg = *box.at(half, lane, c), qu = *box.at(half, lane, 2 + c);
                 const uint32_t wg[4] = {qg.x, qg.y, qg.z, qg.w}, wu[4] = {qu.x, qu.y, qu.z, qu.w};
+                float du[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float g = (e & 1) ? bf16_hi(wg[e >> 1]) : bf16_lo(wg[e >> 1]);
-                    const float u = (e & 1) ? bf16_hi(wu[e >> 1]) : bf16_lo(wu[e >> 1]);
-                    float da;
-                    const float act = activate<decltype(tag)::value>(g, &da);
-                    float dh = du[c * 8 + e];
-                    if (a.l1 != 0.f && act != 0.f && u != 0.f) dh += (act > 0.f) == (u > 0.f) ? a.l1 : -a.l1;
-                    dg[c * 8 + e] = dh * u * da;
-                    du[c * 8 + e] = dh * act;
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 g = make_float2(bf16_lo(wg[e >> 1]), bf16_hi(wg[e >> 1]));
+                    const float2 u = make_float2(bf16_lo(wu[e >> 1]), bf16_hi(wu[e >> 1]));
+                    float2 da, d = make_float2(__uint_as_float(dh[c * 8 + e]), __uint_as_float(dh[c * 8 + e + 1]));
+                    const float2 act = activate<decltype(tag)::value>(g, &da);
+                    if (a.l1 != 0.f) {
+                        d.x += l1_term(a.l1, act.x, u.x);
+                        d.y += l1_term(a.l1, act.y, u.y);
+                    }
+                    const float2 by_g = __fmul2_rn(__fmul2_rn(d, u), da), by_u = __fmul2_rn(d, act);
+                    dg[c * 8 + e] = by_g.x;
+                    dg[c * 8 + e + 1] = by_g.y;
+                    du[e] = by_u.x;
+                    du[e + 1] = by_u.y;
                 }
+                // rounded to bf16 once, as operands of the products that follow; the bias's gradient is summed before
+                *box.at(half, lane, c) = Box::pack8(dg + c * 8);
+                *box.at(half, lane, 2 + c) = Box::pack8(du);
             }
         });
-        // rounded to bf16 once, as operands of the products that follow; the bias's gradient is summed before that
-        box.put_bf16(dg);
-        box.put_bf16(du, 4);
-        box.store_two(a.g, a.u, at, a.ldo, rows, cols);
-        if (a.part) {
-            transpose_reduce32(dg, box.lane);  // lane u: column u over the 32 rows
-            if (box.lane < cols) a.part[(size_t)(row0 / kSumRows) * a.rowsB + col + box.lane] = dg[0];
+        __syncwarp();
+        box.store(half, row0, col, a);
+        if (a.part && row0 < a.rowsA) {
+            transpose_reduce16(dg, lane);  // lane u: column u over the 32 rows
+            if (lane < 16 && col + lane < a.rowsB) a.part[(size_t)(row0 / kSumRows) * a.rowsB + col + lane] = dg[0];
         }
+        __syncwarp();
     }
 }
 
-// 128 accumulator columns of a thread's row added to sum; or sum put in their place.
-__device__ __forceinline__ void add_columns(uint32_t taddr, float (&sum)[128])
+// N accumulator columns of a thread's row added to sum; or sum put in their place.
+template <int N>
+__device__ __forceinline__ void add_columns(uint32_t taddr, float (&sum)[N])
 {
 #pragma unroll
-    for (int ch = 0; ch < 8; ++ch) {
+    for (int ch = 0; ch < N / 16; ++ch) {
         uint32_t v[16];
         tmem_ld16_wait(taddr + ch * 16, v);
 #pragma unroll
         for (int c = 0; c < 16; ++c) sum[ch * 16 + c] += __uint_as_float(v[c]);
     }
 }
-__device__ __forceinline__ void set_columns(uint32_t taddr, const float (&sum)[128])
+template <int N>
+__device__ __forceinline__ void set_columns(uint32_t taddr, const float (&sum)[N])
 {
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
+    for (int ch = 0; ch < N / 32; ++ch) {
         uint32_t v[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[ch * 32 + c]);
@@ -451,10 +524,11 @@ __device__ __forceinline__ void put_part(uint8_t* smem, int share, int my_part, 
 }
 
 template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a, int parts_arg, int per)
+__global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a, int parts_arg, int per)
 {
     const int parts = EPI == LINEAR ? parts_arg : 1;
-    using L = Smem;
+    using L = Smem<EPI>;
+    constexpr int kStages = L::STAGES;
     constexpr uint32_t IDESC =
         idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
     constexpr uint64_t A_KSTEP = A_MN ? (16u * 128u) >> 4 : 2u;  // descriptor units (16 B) per 16-deep K step
@@ -486,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 2 * kEpiWarps);
+            mbar_init(&tempty[i], 2 * L::WARPS);
         }
         mbar_init(mma_done, 1);
         fence_mbar_init();
@@ -624,10 +698,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
     } else {
         // --------------------------------------------------- epilogue -----
         const int q = warp & 3;              // TMEM lane quarter this warp may read
-        const int half = (warp - 2) >> 2;    // its 128 of the accumulator's columns
+        const int slice = (warp - 2) >> 2;   // its columns of the accumulator
         const uint32_t tempty_leader = cluster_addr(tempty, lead);
         const uint32_t lanes_at = tmem_base + ((uint32_t)(32 * q) << 16);
         const bool pieces = EPI != GATED && depth > a.piece;
+        if (EPI == GATED_BWD && pair < num_tiles) {
+            int mb, nb;
+            pair_tile_coords(pair, num_m, num_n, &mb, &nb);
+            HalfBox{box.box, lane}.fetch(0, mb * PAIR_M + (int)rank * HALF + 32 * q, nb * TILE_N + L::COLS * slice, a);
+            copies_commit();
+        }
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
@@ -636,19 +716,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
             const int problem = tile / mn_tiles;
             pair_tile_coords(tile - problem * mn_tiles, num_m, num_n, &mb, &nb);
             const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
-            const int col0 = nb * TILE_N + (TILE_N / 2) * half;
+            const int col0 = nb * TILE_N + L::COLS * slice;
             const bool live = row0 < a.rowsA && col0 < a.rowsB;  // not all past the last row or column
             ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
             if (!ok) break;
             tc_fence_after();
             if constexpr (EPI != GATED) {
                 if (pieces) {
-                    float sum[128];
+                    float sum[L::COLS];
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) sum[k] = 0.f;
+                    for (int k = 0; k < L::COLS; ++k) sum[k] = 0.f;
                     int done = 0;
                     while (true) {
-                        const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + 128 * half);
+                        const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
                         done += a.piece;
                         if (live) add_columns(at, sum);
                         if (done >= depth) {
@@ -673,21 +753,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
                 last_acc = acc;
                 const int share = PAIR_N / parts;
 #pragma unroll 1
-                for (int c0 = 128 * half; c0 < 128 * half + 128; c0 += 32) {
+                for (int c0 = L::COLS * slice; c0 < L::COLS * (slice + 1); c0 += 32) {
                     if (c0 / share == my_part) continue;
                     float v[32];
                     read_columns(at + (uint32_t)c0, v);
                     put_part(smem, share, my_part, 32 * q + lane, c0, v);
                 }
-            } else if (live) {
-                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N);
+            } else if (live || EPI == GATED_BWD) {  // (there also to ask for what comes next)
+                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
                 if constexpr (EPI == LINEAR)
-                    epi_linear([&](int c, float (&v)[64]) { read_columns(at + (uint32_t)(128 * half + c), v); }, 128, row0, col0,
-                               problem, a, box);
+                    epi_linear([&](int c, float (&v)[64]) { read_columns(at + (uint32_t)c, v); }, L::COLS, row0, col0, problem, a,
+                               box);
                 else if constexpr (EPI == GATED)
-                    epi_gated(at + 64u * (uint32_t)half, row0, col0, a, box);
-                else
-                    epi_gated_bwd(at + 128u * (uint32_t)half, row0, col0, a, box);
+                    epi_gated(at, row0, col0, a, box);
+                else {
+                    int next_row0 = -1, next_col0 = 0;
+                    if (tile + num_pairs < num_tiles) {
+                        pair_tile_coords(tile + num_pairs, num_m, num_n, &mb, &nb);
+                        next_row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
+                        next_col0 = nb * TILE_N + L::COLS * slice;
+                    }
+                    epi_gated_bwd(at, row0, col0, next_row0, next_col0, a, HalfBox{box.box, lane});
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -697,6 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_mm_pair(const __grid_constant__
             if (acc == 0) acc_phase ^= 1u;
         }
         if (!ok) fail(a.status, abort_flag);
+        if (EPI == GATED_BWD) asm volatile("cp.async.wait_all;" ::: "memory");  // (copies may be left after a wait that ran out)
     }
 
     if constexpr (EPI == LINEAR) {
@@ -859,16 +947,16 @@ __device__ __forceinline__ void few_finish(const float* part, int parts, int bas
                 few_store<true>(a.u, false, at, 1, left, u);
             }
             by_activation(a.act, [&](auto tag) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]) * u[e];
+                activate_all<decltype(tag)::value>(v);
             });
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= u[e];
             few_store<true>(a.h, false, at, 1, left, v);
         } else {
             if (a.pre) few_store<VEC>(a.pre, false, row * a.ldpre + col, apart, left, v);
             if (a.act != TWELL_ACT_NONE)
                 by_activation(a.act, [&](auto tag) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = activate<decltype(tag)::value>(v[e]);
+                    activate_all<decltype(tag)::value>(v);
                 });
             if (a.res) {
                 const size_t at = row * a.ldres + col;
@@ -896,8 +984,7 @@ __device__ __forceinline__ void few_direct(float (&v)[16], int tokens, size_t ro
     }
     if (a.act != TWELL_ACT_NONE)
         by_activation(a.act, [&](auto tag) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = activate<decltype(tag)::value>(v[c]);
+            activate_all<decltype(tag)::value>(v);
         });
     if (a.out_f32) {
         float* out = static_cast<float*>(a.out[0]);
@@ -1193,7 +1280,7 @@ template <int EPI, bool A_MN, bool B_MN>
 cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
 {
     auto kern = k_mm_pair<EPI, A_MN, B_MN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::TOTAL);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1202,8 +1289,8 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = Smem::TOTAL;
+    cfg.blockDim = dim3(Smem<EPI>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Smem<EPI>::TOTAL;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
