@@ -44,7 +44,7 @@ constexpr int kMBits = 4, kVBits = 5;             // exponent bits of the codes
 
 constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
-enum { P_F32 = 1, G_F32 = 2, VEC = 4 };
+enum { P_F32 = 1, G_F32 = 2, VEC = 4 };  // VEC: everything lies on 16-byte boundaries (copies on 8)
 
 template <int CAP>
 struct Table {
@@ -341,24 +341,62 @@ struct Scalars {
 };
 
 // A block's elements of one tensor. `moments`, `params`: keys of its random bits.
+// 8-bit states of fp32 parameters: a warp's next block comes into shared memory by asynchronous copies while the present
+// one is worked on (134 M elements: 457 us with loads when their turn came, now 410). bf16 parameters move too few bytes
+// for that: their pass is bound by instructions, and the copies cost more of them (446 instead of 387 us).
+struct Staged {
+    uint4 p[kBlock / 4], g[kBlock / 4], m[kBlock / 16], v[kBlock / 16];  // parameters, fp32 or bf16 gradients, codes
+};
+
+__device__ __forceinline__ void copy16(void* to, const void* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+// Asks for a whole block of a tensor whose addresses allow 16-byte pieces.
+__device__ __forceinline__ void stage(Staged& s, const void* p, const void* g, const void* m, const void* v, int flags, int64_t i0,
+                                      int lane)
+{
+    const int gs = flags & G_F32 ? 4 : 2;
+    const char* pp = static_cast<const char*>(p) + i0 * 4;
+    const char* gg = static_cast<const char*>(g) + i0 * gs;
+    copy16(&s.p[lane], pp + lane * 16);
+    copy16(&s.p[32 + lane], pp + 512 + lane * 16);
+    copy16(&s.g[lane], gg + lane * 16);
+    if (gs == 4) copy16(&s.g[32 + lane], gg + 512 + lane * 16);
+    const int half = lane & 15;
+    if (lane < 16)
+        copy16(&s.m[half], static_cast<const char*>(m) + i0 + half * 16);
+    else
+        copy16(&s.v[half], static_cast<const char*>(v) + i0 + half * 16);
+}
+
 // PF, GF: parameter and gradient are fp32 (as template arguments: with both kinds of loads behind a branch each waited for
 // the one before).
 template <bool V, bool BITS8, bool PF, bool GF>
 __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void* v, float* ms, float* vs, uint16_t* copy,
                                            int64_t i0, int left, int lane, const Hyper& h, const Scalars& s,
-                                           uint64_t moments, uint64_t params)
+                                           uint64_t moments, uint64_t params, const Staged& staged, float2 scales)
 {
     float2 x[kPairs], grad[kPairs], mom[kPairs], var[kPairs];
-    load<V>(p, PF, i0, left, lane, x);
-    load<V>(g, GF, i0, left, lane, grad);
     if constexpr (BITS8) {
         uint32_t cm[kPer / 4], cv[kPer / 4];
-        load_codes<V>(m, i0, left, lane, cm);
-        load_codes<V>(v, i0, left, lane, cv);
-        const float sm = ms[i0 / kBlock], sv = vs[i0 / kBlock];
-        decode<kMBits>(cm, sm, mom);
-        decode<kVBits>(cv, sv, var);
+        if constexpr (V && PF) {
+            load<V>(staged.p, PF, 0, left, lane, x);
+            load<V>(staged.g, GF, 0, left, lane, grad);
+            load_codes<V>(staged.m, 0, left, lane, cm);
+            load_codes<V>(staged.v, 0, left, lane, cv);
+        } else {
+            load<V>(p, PF, i0, left, lane, x);
+            load<V>(g, GF, i0, left, lane, grad);
+            load_codes<V>(m, i0, left, lane, cm);
+            load_codes<V>(v, i0, left, lane, cv);
+        }
+        decode<kMBits>(cm, scales.x, mom);
+        decode<kVBits>(cv, scales.y, var);
     } else {
+        load<V>(p, PF, i0, left, lane, x);
+        load<V>(g, GF, i0, left, lane, grad);
         load<V>(m, true, i0, left, lane, mom);
         load<V>(v, true, i0, left, lane, var);
     }
@@ -447,6 +485,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
     int k = u0 < u1 ? t.find(u0) - 1 : 0, next = u0;
     uint64_t moments = 0, params = 0;
+    __shared__ Staged ring[BITS8 ? kThreads / 32 : 1][2];
+    bool ready = false;  // this block has been asked for
+    int at = 0;          // its place in the ring
+    float2 scales = make_float2(0.f, 0.f), next_scales = scales;
     for (int u = u0; u < u1; ++u) {
         if (u >= next) {  // the next tensor (none is empty), or the first
             ++k;
@@ -459,10 +501,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
         const int64_t rest = t.numel[k] - i0;
         if (rest <= 0) continue;
         const int left = (int)min((int64_t)kBlock, rest);
+        if constexpr (BITS8) {
+            scales = ready ? next_scales : make_float2(t.ms[k][i0 / kBlock], t.vs[k][i0 / kBlock]);
+            if (left == kBlock && (t.flags[k] & VEC) && (t.flags[k] & P_F32)) {
+                if (!ready) stage(ring[warp][at], t.p[k], t.g[k], t.m[k], t.v[k], t.flags[k], i0, lane);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                ready = u + 1 < min(u1, next) && rest >= kUnit + kBlock;
+                if (ready) {
+                    stage(ring[warp][at ^ 1], t.p[k], t.g[k], t.m[k], t.v[k], t.flags[k], i0 + kUnit, lane);
+                    const int64_t b = i0 / kBlock + kUnit / kBlock;
+                    next_scales = make_float2(t.ms[k][b], t.vs[k][b]);
+                }
+                asm volatile("cp.async.commit_group;\n cp.async.wait_group 1;" ::: "memory");
+                __syncwarp();
+            } else {
+                ready = false;
+            }
+        }
         by_types(t.flags[k], left == kBlock, [&](auto v, auto pf, auto gf) {
             step_block<decltype(v)::value, BITS8, decltype(pf)::value, decltype(gf)::value>(
-                t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], i0, left, lane, h, s, moments, params);
+                t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], i0, left, lane, h, s, moments, params,
+                ring[BITS8 ? warp : 0][at], scales);
         });
+        at ^= 1;
+        if (BITS8) __syncwarp();  // the ring's other half may be filled again
     }
 }
 
@@ -562,10 +624,7 @@ twell_status by_tables(const twell_adamw_list* l, int most, Of of, F f)
                 t.numel[i] = n;
                 t.first[i] = (int32_t)units;
                 t.id[i] = next;
-                // 16-byte pieces of fp32, 8 of bf16, 4 of codes
-                const size_t ss = l->state_bits == 8 ? 4 : 16;
-                if (aligned(t.p[i], t.flags[i] & P_F32 ? 16 : 8) && aligned(t.g[i], t.flags[i] & G_F32 ? 16 : 8) &&
-                    aligned(t.m[i], ss) && aligned(t.v[i], ss) && aligned(t.copy[i], 8))
+                if (aligned(t.p[i], 16) && aligned(t.g[i], 16) && aligned(t.m[i], 16) && aligned(t.v[i], 16) && aligned(t.copy[i], 8))
                     t.flags[i] |= VEC;
                 units += more;
             }

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kDpreThreads)
     const int rows = min(kSumRows, M - r0);
     by_activation(pre ? act : TWELL_ACT_NONE, [&](auto tag) {
         constexpr int ACT = decltype(tag)::value;
-#pragma unroll 4
+#pragma unroll 2  // (more at once: fewer threads on an SM; sums of 8192 x 16384: 1 105 us, 2 103, 4 140, 8 152)
         for (int r = 0; r < rows; ++r) {
             const size_t row = (size_t)r0 + r;
             float d[V];
