@@ -48,6 +48,7 @@ enum { P_F32 = 1, G_F32 = 2, VEC = 4 };  // VEC: everything lies on 16-byte boun
 
 template <int CAP>
 struct Table {
+    static constexpr int kCap = CAP;
     void* p[CAP];
     const void* g[CAP];
     void* m[CAP];
@@ -85,6 +86,7 @@ struct Hyper {
     float b1, b2, rest1, rest2;  // rest = 1 - b, rounded once
     float log_b1, log_b2;
     float eps, decay;
+    float one;  // 1
     uint64_t seed;
 };
 
@@ -263,6 +265,11 @@ __device__ __forceinline__ void param_bits(uint64_t key, int64_t i0, int lane, u
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
+// a + b for pairs, rounded, where a is a rounded product. As a 1 + b with a 1 that the compiler does not know: sums of
+// products, the instructions with explicit rounding too, were joined to fused multiply-additions where they work on
+// pairs, and a code next to a border then was another one than single operations give (one in 5 million).
+__device__ __forceinline__ float2 add_rounded(float2 a, float one, float2 b) { return __ffma2_rn(a, both(one), b); }
+
 // Powers of two that a code and its value lie apart: 2^(127 - 2^E) times the scale. One multiplication as long as their
 // product is a normal number, two (rounded the same) for scales above 2^(2^E).
 template <int E>
@@ -342,8 +349,8 @@ struct Scalars {
 
 // A block's elements of one tensor. `moments`, `params`: keys of its random bits.
 // 8-bit states of fp32 parameters: a warp's next block comes into shared memory by asynchronous copies while the present
-// one is worked on (134 M elements: 457 us with loads when their turn came, now 410). bf16 parameters move too few bytes
-// for that: their pass is bound by instructions, and the copies cost more of them (446 instead of 387 us).
+// one is worked on (134 M elements: 457 us with loads when their turn came, now 406). bf16 parameters move too few bytes
+// for that: their pass is bound by instructions, and the copies cost more of them.
 struct Staged {
     uint4 p[kBlock / 4], g[kBlock / 4], m[kBlock / 16], v[kBlock / 16];  // parameters, fp32 or bf16 gradients, codes
 };
@@ -373,7 +380,7 @@ __device__ __forceinline__ void stage(Staged& s, const void* p, const void* g, c
 
 // PF, GF: parameter and gradient are fp32 (as template arguments: with both kinds of loads behind a branch each waited for
 // the one before).
-template <bool V, bool BITS8, bool PF, bool GF>
+template <bool V, bool BITS8, bool STAGED, bool PF, bool GF>
 __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void* v, float* ms, float* vs, uint16_t* copy,
                                            int64_t i0, int left, int lane, const Hyper& h, const Scalars& s,
                                            uint64_t moments, uint64_t params, const Staged& staged, float2 scales)
@@ -381,7 +388,7 @@ __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void
     float2 x[kPairs], grad[kPairs], mom[kPairs], var[kPairs];
     if constexpr (BITS8) {
         uint32_t cm[kPer / 4], cv[kPer / 4];
-        if constexpr (V && PF) {
+        if constexpr (V && STAGED && PF) {
             load<V>(staged.p, PF, 0, left, lane, x);
             load<V>(staged.g, GF, 0, left, lane, grad);
             load_codes<V>(staged.m, 0, left, lane, cm);
@@ -402,10 +409,10 @@ __device__ __forceinline__ void step_block(void* p, const void* g, void* m, void
     }
 #pragma unroll
     for (int k = 0; k < kPairs; ++k) {
-        // each operation rounded for itself: what the codes are formed of is the same bits in any order of compilation
+        // each operation of the moments rounded for itself: the codes are formed of them
         const float2 gs = __fmul2_rn(grad[k], both(s.c));
-        mom[k] = __fadd2_rn(__fmul2_rn(both(h.b1), mom[k]), __fmul2_rn(both(h.rest1), gs));
-        var[k] = __fadd2_rn(__fmul2_rn(both(h.b2), var[k]), __fmul2_rn(both(h.rest2), __fmul2_rn(gs, gs)));
+        mom[k] = add_rounded(__fmul2_rn(both(h.b1), mom[k]), h.one, __fmul2_rn(both(h.rest1), gs));
+        var[k] = add_rounded(__fmul2_rn(both(h.b2), var[k]), h.one, __fmul2_rn(both(h.rest2), __fmul2_rn(gs, gs)));
         const float2 under = __ffma2_rn(make_float2(sqrt_approx(var[k].x), sqrt_approx(var[k].y)), both(s.root), both(h.eps));
         const float2 to = __fmul2_rn(mom[k], make_float2(reciprocal_approx(under.x), reciprocal_approx(under.y)));
         x[k] = __ffma2_rn(both(-s.rate), __ffma2_rn(both(s.decay), x[k], to), x[k]);
@@ -461,7 +468,9 @@ __device__ __forceinline__ void by_types(int flags, bool whole, F f)
     }
 }
 
-template <int CAP, bool BITS8>
+// STAGED: 8-bit states, some parameters in fp32. (Without any the ring's shared memory would only take the first-level
+// cache away: bf16 parameters 441 instead of 387 us.)
+template <int CAP, bool BITS8, bool STAGED>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_constant__ Table<CAP> t, const Hyper h)
 {
     __shared__ Scalars shared;
@@ -470,7 +479,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
         const float norm = h.norm ? *h.norm : 0.f;
         const int step = *h.step;
         s.skip = !(fabsf(norm) < INFINITY) || step < 1;
-        s.c = norm > h.max_norm ? __fdiv_rn(h.max_norm, norm) : 1.f;
+        // max_norm (1 / norm), as tensor libraries divide a number by a tensor, so that their operations give the same
+        // codes to the bit (divided where 1 / norm would pass fp32's range)
+        s.c = norm <= h.max_norm ? 1.f : norm > 0x1p-126f ? __fmul_rn(h.max_norm, __frcp_rn(norm)) : __fdiv_rn(h.max_norm, norm);
         const float rest = one_minus_power(h.log_b1, step);
         s.rate = __fdiv_rn(*h.lr, rest);
         s.decay = h.decay * rest;
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
     int k = u0 < u1 ? t.find(u0) - 1 : 0, next = u0;
     uint64_t moments = 0, params = 0;
-    __shared__ Staged ring[BITS8 ? kThreads / 32 : 1][2];
+    __shared__ Staged ring[STAGED ? kThreads / 32 : 1][2];
     bool ready = false;  // this block has been asked for
     int at = 0;          // its place in the ring
     float2 scales = make_float2(0.f, 0.f), next_scales = scales;
@@ -503,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
         const int left = (int)min((int64_t)kBlock, rest);
         if constexpr (BITS8) {
             scales = ready ? next_scales : make_float2(t.ms[k][i0 / kBlock], t.vs[k][i0 / kBlock]);
-            if (left == kBlock && (t.flags[k] & VEC) && (t.flags[k] & P_F32)) {
+            if (STAGED && left == kBlock && (t.flags[k] & VEC) && (t.flags[k] & P_F32)) {
                 if (!ready) stage(ring[warp][at], t.p[k], t.g[k], t.m[k], t.v[k], t.flags[k], i0, lane);
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 ready = u + 1 < min(u1, next) && rest >= kUnit + kBlock;
@@ -519,12 +530,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
             }
         }
         by_types(t.flags[k], left == kBlock, [&](auto v, auto pf, auto gf) {
-            step_block<decltype(v)::value, BITS8, decltype(pf)::value, decltype(gf)::value>(
+            step_block<decltype(v)::value, BITS8, STAGED, decltype(pf)::value, decltype(gf)::value>(
                 t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], i0, left, lane, h, s, moments, params,
-                ring[BITS8 ? warp : 0][at], scales);
+                ring[STAGED ? warp : 0][at], scales);
         });
         at ^= 1;
-        if (BITS8) __syncwarp();  // the ring's other half may be filled again
+        if (STAGED) __syncwarp();  // the ring's other half may be filled again
     }
 }
 
@@ -670,6 +681,7 @@ extern "C" twell_status twell_adamw(const twell_adamw_list* list, const float* l
     h.log_b2 = (float)log(beta2);
     h.eps = (float)eps;
     h.decay = (float)weight_decay;
+    h.one = 1.f;
     h.seed = seed;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool eight = list->state_bits == 8;
@@ -679,19 +691,20 @@ extern "C" twell_status twell_adamw(const twell_adamw_list* list, const float* l
         *copy = list->copy ? static_cast<uint16_t*>(list->copy[i]) : nullptr;
         *flags = (uint8_t)((list->param_type[i] == TWELL_F32 ? P_F32 : 0) | (list->grad_type[i] == TWELL_F32 ? G_F32 : 0));
     };
-    if (list->n <= kSmallTable)
-        return by_tables<kSmallTable>(list, sms * kBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) {
-            if (eight)
-                k_adamw<kSmallTable, true><<<blocks, kThreads, 0, s>>>(t, h);
-            else
-                k_adamw<kSmallTable, false><<<blocks, kThreads, 0, s>>>(t, h);
-        });
-    return by_tables<kTable>(list, sms * kBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) {
-        if (eight)
-            k_adamw<kTable, true><<<blocks, kThreads, 0, s>>>(t, h);
+    bool any_f32 = false;
+    for (int i = 0; i < list->n; ++i) any_f32 = any_f32 || (list->numel[i] > 0 && list->param_type[i] == TWELL_F32);
+    auto launch = [&](auto table, int blocks) {  // (by value: the parameters of the launch)
+        constexpr int CAP = decltype(table)::kCap;
+        if (!eight)
+            k_adamw<CAP, false, false><<<blocks, kThreads, 0, s>>>(table, h);
+        else if (any_f32)
+            k_adamw<CAP, true, true><<<blocks, kThreads, 0, s>>>(table, h);
         else
-            k_adamw<kTable, false><<<blocks, kThreads, 0, s>>>(t, h);
-    });
+            k_adamw<CAP, true, false><<<blocks, kThreads, 0, s>>>(table, h);
+    };
+    if (list->n <= kSmallTable)
+        return by_tables<kSmallTable>(list, sms * kBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) { launch(t, blocks); });
+    return by_tables<kTable>(list, sms * kBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) { launch(t, blocks); });
 }
 
 extern "C" twell_status twell_adamw_values(const twell_adamw_list* list, const twell_tensor_list* m_out,

@@ -1028,7 +1028,6 @@ __global__ void __launch_bounds__(kFewThreads, 3)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (EPI == GATED) launch_next();
     const int rank = parts > 1 ? (int)cluster_rank() : 0;
     const int col0 = (int)(blockIdx.x / (unsigned)parts) * COLS, row0 = (int)blockIdx.y * BN;
     const int depth = a.num_kb * a.segments;
@@ -1080,6 +1079,7 @@ __global__ void __launch_bounds__(kFewThreads, 3)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    if (EPI == GATED) launch_next();  // (this launch has its tensor memory: the next one's cannot come first)
 
     if (warp == 0) {
         if (lane == 0) {

@@ -473,7 +473,7 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * x [M, K] bf16; W bf16, [N, K] (w_kn 0) or [K, N] (w_kn 1: x W), densely packed;
  * bias [N] fp32 or NULL; act a twell_activation; res [M, N] of y's type or NULL;
  * y [M, N] bf16 or fp32 (y_type); pre [M, N] bf16 or NULL (kept for the backward).
- * Row strides (ld*) in elements. x: a multiple of 8, 16-byte aligned; y, res, pre,
+ * Row strides (ld*) in elements. x: a multiple of 8, <= 2^30, 16-byte aligned; y, res, pre,
  * dy, dx: any that is at least the width, of any alignment (16-byte boundaries are
  * fastest). M >= 0, N >= 1, K % 8 == 0; with w_kn N % 8 == 0. Limit of this build:
  * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res; other outputs must not

@@ -155,6 +155,32 @@ def test_first_steps_from_nothing(bits):
         _check(pr, 1e9, wd=0.0)
 
 
+@pytest.mark.parametrize("scale", [1e-13, 1e6, 1e12, 1e17])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_of_any_magnitude(scale, bits):
+    """Scales of codes far from 1, where a factor of the conversion leaves fp32's range and takes two steps."""
+    pr = Problem([3000, 255], bits=bits, first=True)
+    for g in pr.g:
+        g.mul_(scale)
+    pr.norm.fill_(math.sqrt(sum(float((t.double() ** 2).sum()) for t in pr.g)))
+    for t in (1, 2, 3):
+        pr.step.fill_(t)
+        _check(pr, 0.5 * float(pr.norm), wd=0.0)
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF, BF), (F32, BF)], ids=["f32", "bf16", "f32_bf16"])
+def test_moments_are_single_rounded_operations(types):
+    """With 32-bit states, m and v as torch's operations give them, to the bit (the 8-bit codes are formed of them)."""
+    pr = Problem([70_000, 1001], *types)
+    want = []
+    c = torch.where(pr.norm > 0.01, 0.01 / pr.norm, 1.0)
+    for g, m, v in zip(pr.g, pr.m, pr.v):
+        gs = g.float() * c
+        want.append((B1 * m + (1 - B1) * gs, B2 * v + (1 - B2) * (gs * gs)))
+    pr.run(0.01)
+    assert all(torch.equal(m, a) and torch.equal(v, b) for m, v, (a, b) in zip(pr.m, pr.v, want))
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_late_steps_without_a_norm(bits):
     pr = Problem([3000], bits=bits)
