@@ -908,17 +908,35 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr)
 }
 
 // A CTA's share of its tile's results (`share` columns from `base` on, `tokens` rows), four a thread: neighbours where
-// everything lies on 16-byte boundaries, else a quarter of the share apart, so that lanes store neighbours.
+// everything lies on 16-byte boundaries, else a quarter of the share apart, so that lanes store neighbours. A thread keeps
+// its columns (their number divides the threads). (Four rows at once were slower: 128 x 4096 x 4096 21 us instead of 17.)
 template <int EPI, bool VEC>
 __device__ __forceinline__ void few_finish(const float* part, int parts, int base, int share, int tokens, int row0, int col0,
                                            const Args& a)
 {
-    const int per_row = share / 4, apart = VEC ? 1 : per_row;
-    for (int i = threadIdx.x; i < tokens * per_row; i += kFewThreads) {
-        const int t = i / per_row, c = base + (i - t * per_row) * (VEC ? 4 : 1), col = col0 + c;
-        const int left = a.rowsB - col;
-        if (left <= 0) continue;
-        float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+    const int per_row = share / 4, apart = VEC ? 1 : per_row, step = kFewThreads / per_row;
+    const int c = base + (int)threadIdx.x % per_row * (VEC ? 4 : 1), col = col0 + c, left = a.rowsB - col;
+    if (left <= 0) return;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.bias) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (VEC || e * apart < left) bias[e] = a.bias[col + e * apart];
+    }
+#pragma unroll 1
+    for (int t = (int)threadIdx.x / per_row; t < tokens; t += step) {
+        const size_t row = (size_t)row0 + t;
+        float v[4], u[4] = {0.f, 0.f, 0.f, 0.f}, res[4] = {0.f, 0.f, 0.f, 0.f};
+        if (EPI == LINEAR && a.res) {
+            const size_t at = row * a.ldres + col;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (VEC || e * apart < left)
+                    res[e] = a.out_f32 ? static_cast<const float*>(a.res)[at + e * apart]
+                                       : bf16_to_f32(static_cast<const uint16_t*>(a.res)[at + e * apart]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = bias[e];
         const float* from = part + t * kFewRows + c;
         for (int r = 0; r < parts; ++r) {
             const uint32_t addr = parts > 1 ? cluster_addr(from, (uint32_t)r) : smem_u32(from);
@@ -934,46 +952,41 @@ __device__ __forceinline__ void few_finish(const float* part, int parts, int bas
                 for (int e = 0; e < 4; ++e) v[e] += ld_cluster_f32(addr + (uint32_t)(e * apart * 4));
             }
         }
-        const size_t row = (size_t)row0 + t;
-        if (a.bias) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (VEC || e * apart < left) v[e] += a.bias[col + e * apart];
-        }
         if constexpr (EPI == GATED) {
             const size_t at = row * a.ldo + col;
             if (a.g) {
                 few_store<true>(a.g, false, at, 1, left, v);
                 few_store<true>(a.u, false, at, 1, left, u);
             }
-            by_activation(a.act, [&](auto tag) {
-                activate_all<decltype(tag)::value>(v);
-            });
+            by_activation(a.act, [&](auto tag) { activate_all<decltype(tag)::value>(v); });
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] *= u[e];
             few_store<true>(a.h, false, at, 1, left, v);
         } else {
             if (a.pre) few_store<VEC>(a.pre, false, row * a.ldpre + col, apart, left, v);
-            if (a.act != TWELL_ACT_NONE)
-                by_activation(a.act, [&](auto tag) {
-                    activate_all<decltype(tag)::value>(v);
-                });
-            if (a.res) {
-                const size_t at = row * a.ldres + col;
+            if (a.act != TWELL_ACT_NONE) by_activation(a.act, [&](auto tag) { activate_all<decltype(tag)::value>(v); });
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (VEC || e * apart < left)
-                        v[e] += a.out_f32 ? static_cast<const float*>(a.res)[at + e * apart]
-                                          : bf16_to_f32(static_cast<const uint16_t*>(a.res)[at + e * apart]);
-            }
+            for (int e = 0; e < 4; ++e) v[e] += res[e];
             few_store<VEC>(a.out[0], a.out_f32, row * a.ldo + col, apart, left, v);
         }
     }
 }
 
 // The whole depth in one CTA (LINEAR): 16 tokens' results of a column, stored by the thread that has them in its
-// tensor memory lane. A warp's lanes are neighbouring columns of one row.
-__device__ __forceinline__ void few_direct(float (&v)[16], int tokens, size_t row, int col, float bias, const Args& a)
+// tensor memory lane. A warp's lanes are neighbouring columns of one row. The residual's values are asked for before
+// the sums are ready, or while the 16 tokens before are worked on.
+__device__ __forceinline__ void few_residual(float (&r)[16], int tokens, size_t row, int col, const Args& a)
+{
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+        r[c] = 0.f;
+        if (c < tokens)
+            r[c] = a.out_f32 ? static_cast<const float*>(a.res)[(row + c) * a.ldres + col]
+                             : bf16_to_f32(static_cast<const uint16_t*>(a.res)[(row + c) * a.ldres + col]);
+    }
+}
+__device__ __forceinline__ void few_direct(float (&v)[16], const float (&res)[16], int tokens, size_t row, int col, float bias,
+                                           const Args& a)
 {
 #pragma unroll
     for (int c = 0; c < 16; ++c) v[c] += bias;
@@ -983,29 +996,18 @@ __device__ __forceinline__ void few_direct(float (&v)[16], int tokens, size_t ro
             if (c < tokens) a.pre[(row + c) * a.ldpre + col] = f32_to_bf16_bits(v[c]);
     }
     if (a.act != TWELL_ACT_NONE)
-        by_activation(a.act, [&](auto tag) {
-            activate_all<decltype(tag)::value>(v);
-        });
-    if (a.out_f32) {
-        float* out = static_cast<float*>(a.out[0]);
-        if (a.res) {
+        by_activation(a.act, [&](auto tag) { activate_all<decltype(tag)::value>(v); });
+    if (a.res) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                if (c < tokens) v[c] += static_cast<const float*>(a.res)[(row + c) * a.ldres + col];
-        }
+        for (int c = 0; c < 16; ++c) v[c] += res[c];
+    }
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-            if (c < tokens) out[(row + c) * a.ldo + col] = v[c];
-    } else {
-        uint16_t* out = static_cast<uint16_t*>(a.out[0]);
-        if (a.res) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c)
-                if (c < tokens) v[c] += bf16_to_f32(static_cast<const uint16_t*>(a.res)[(row + c) * a.ldres + col]);
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-            if (c < tokens) out[(row + c) * a.ldo + col] = f32_to_bf16_bits(v[c]);
+    for (int c = 0; c < 16; ++c) {
+        if (c >= tokens) break;
+        if (a.out_f32)
+            static_cast<float*>(a.out[0])[(row + c) * a.ldo + col] = v[c];
+        else
+            static_cast<uint16_t*>(a.out[0])[(row + c) * a.ldo + col] = f32_to_bf16_bits(v[c]);
     }
 }
 
@@ -1186,9 +1188,16 @@ __global__ void __launch_bounds__(kFewThreads, 3)
         const int row = 32 * (warp & 3) + lane, col = col0 + row;
         const bool failed = direct && has_error(a.status);
         const float bias = direct && a.bias && col < a.rowsB ? a.bias[col] : 0.f;
+        const bool with_res = direct && a.res && col < a.rowsB;
+        float res[16];
+        if (with_res) few_residual(res, tokens, (size_t)row0, col, a);
         auto put16 = [&](int c0, float (&v)[16]) {
             if (direct) {
-                if (col < a.rowsB && !failed) few_direct(v, tokens - c0, (size_t)row0 + c0, col, bias, a);
+                float now[16];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) now[c] = res[c];
+                if (with_res && c0 + 16 < tokens) few_residual(res, tokens - c0 - 16, (size_t)row0 + c0 + 16, col, a);
+                if (col < a.rowsB && !failed) few_direct(v, now, tokens - c0, (size_t)row0 + c0, col, bias, a);
             } else {
 #pragma unroll
                 for (int c = 0; c < 16; ++c) part[(c0 + c) * kFewRows + row] = v[c];
