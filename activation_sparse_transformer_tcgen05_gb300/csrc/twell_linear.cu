@@ -32,66 +32,81 @@ constexpr int kDpreThreads = 128;
 size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 int64_t padded(int n) { return ((int64_t)n + 63) / 64 * 64; }
 
-// kSumRows rows x (threads * V) columns a block: dpre = dy act'(pre) (pre null: dy) to out, if there is one, and the
-// rows' sums in fp32 to part, if there is one. V = 8: rows of dy, pre and out in 16-byte pieces.
-template <int V>
+// kSumRows rows a block: dpre = dy act'(pre) (pre null: dy) to out, if there is one, and the rows' sums in fp32 to part,
+// if there is one. V = 8: rows of dy, pre and out in 16-byte pieces. Narrow matrices: `split` threads share a column's
+// rows (each every split-th) and their sums are added in order (3789 x 16: 32 rows in a row took 25 us).
+template <int V, bool SPLIT>
 __global__ void __launch_bounds__(kDpreThreads)
     k_linear_dpre(const uint16_t* __restrict__ dy, int64_t lddy, const uint16_t* __restrict__ pre, int64_t ldpre, int M, int N,
-                  int act, uint16_t* __restrict__ out, int64_t ldout, float* __restrict__ part,
+                  int act, uint16_t* __restrict__ out, int64_t ldout, float* __restrict__ part, int split_arg, int col0,
                   const int32_t* __restrict__ status)
 {
     if (has_error(status)) return;
+    __shared__ float shared[V][SPLIT ? kDpreThreads : 1];
+    const int split = SPLIT ? split_arg : 1;
     const int r0 = (int)blockIdx.x * kSumRows, rows = min(kSumRows, M - r0);
-    for (int64_t c = ((int64_t)blockIdx.y * kDpreThreads + threadIdx.x) * V; c < N; c += (int64_t)gridDim.y * kDpreThreads * V) {
-        float sum[V];
+    const int wide = kDpreThreads / split, first = (int)threadIdx.x / wide;  // threads across, this one's first row
+    const int c = col0 + ((int)blockIdx.y * wide + (int)threadIdx.x % wide) * V;
+    if (!SPLIT && c >= N) return;
+    float sum[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] = 0.f;
-        by_activation(pre ? act : TWELL_ACT_NONE, [&](auto tag) {
-            constexpr int ACT = decltype(tag)::value;
+    for (int e = 0; e < V; ++e) sum[e] = 0.f;
+    if (c < N) by_activation(pre ? act : TWELL_ACT_NONE, [&](auto tag) {
+        constexpr int ACT = decltype(tag)::value;
 #pragma unroll 2  // (more at once: fewer threads on an SM; sums of 8192 x 16384: 1 105 us, 2 103, 4 140, 8 152)
-            for (int r = 0; r < rows; ++r) {
-                const size_t row = (size_t)r0 + r;
-                float d[V];
-                if constexpr (V == 8) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(dy + row * lddy + c);
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-                    uint32_t z[4] = {0, 0, 0, 0};
-                    if (ACT != TWELL_ACT_NONE) {
-                        const uint4 p = *reinterpret_cast<const uint4*>(pre + row * ldpre + c);
-                        z[0] = p.x, z[1] = p.y, z[2] = p.z, z[3] = p.w;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        float2 g = make_float2(bf16_lo(w[e >> 1]), bf16_hi(w[e >> 1]));
-                        if (ACT != TWELL_ACT_NONE) {
-                            float2 da;
-                            activate<ACT>(make_float2(bf16_lo(z[e >> 1]), bf16_hi(z[e >> 1])), &da);
-                            g = __fmul2_rn(g, da);
-                        }
-                        d[e] = g.x;
-                        d[e + 1] = g.y;
-                    }
-                    if (out)
-                        *reinterpret_cast<uint4*>(out + row * ldout + c) =
-                            make_uint4(cvt_bf16x2(d[0], d[1]), cvt_bf16x2(d[2], d[3]), cvt_bf16x2(d[4], d[5]),
-                                       cvt_bf16x2(d[6], d[7]));
-                } else {
-                    d[0] = bf16_to_f32(dy[row * lddy + c]);
-                    if (ACT != TWELL_ACT_NONE) {
-                        float2 da;
-                        activate<ACT>(pair(bf16_to_f32(pre[row * ldpre + c])), &da);
-                        d[0] *= da.x;
-                    }
-                    if (out) out[row * ldout + c] = f32_to_bf16_bits(d[0]);
+        for (int r = SPLIT ? first : 0; r < rows; r += split) {
+            const size_t row = (size_t)r0 + r;
+            float d[V];
+            if constexpr (V == 8) {
+                const uint4 q = *reinterpret_cast<const uint4*>(dy + row * lddy + c);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+                uint32_t z[4] = {0, 0, 0, 0};
+                if (ACT != TWELL_ACT_NONE) {
+                    const uint4 p = *reinterpret_cast<const uint4*>(pre + row * ldpre + c);
+                    z[0] = p.x, z[1] = p.y, z[2] = p.z, z[3] = p.w;
                 }
 #pragma unroll
-                for (int e = 0; e < V; ++e) sum[e] += d[e];
+                for (int e = 0; e < 8; e += 2) {
+                    float2 g = make_float2(bf16_lo(w[e >> 1]), bf16_hi(w[e >> 1]));
+                    if (ACT != TWELL_ACT_NONE) {
+                        float2 da;
+                        activate<ACT>(make_float2(bf16_lo(z[e >> 1]), bf16_hi(z[e >> 1])), &da);
+                        g = __fmul2_rn(g, da);
+                    }
+                    d[e] = g.x;
+                    d[e + 1] = g.y;
+                }
+                if (out)
+                    *reinterpret_cast<uint4*>(out + row * ldout + c) =
+                        make_uint4(cvt_bf16x2(d[0], d[1]), cvt_bf16x2(d[2], d[3]), cvt_bf16x2(d[4], d[5]),
+                                   cvt_bf16x2(d[6], d[7]));
+            } else {
+                d[0] = bf16_to_f32(dy[row * lddy + c]);
+                if (ACT != TWELL_ACT_NONE) {
+                    float2 da;
+                    activate<ACT>(pair(bf16_to_f32(pre[row * ldpre + c])), &da);
+                    d[0] *= da.x;
+                }
+                if (out) out[row * ldout + c] = f32_to_bf16_bits(d[0]);
             }
-        });
-        if (part) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) part[(size_t)blockIdx.x * N + c + e] = sum[e];
+            for (int e = 0; e < V; ++e) sum[e] += d[e];
         }
+    });
+    if (SPLIT && part) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) shared[e][threadIdx.x] = sum[e];
+        __syncthreads();
+        if (first == 0) {
+            for (int k = 1; k < split; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) sum[e] += shared[e][threadIdx.x + k * wide];
+        }
+    }
+    if (part && first == 0 && c < N) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[(size_t)blockIdx.x * N + c + e] = sum[e];
     }
 }
 
@@ -191,13 +206,19 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
     if (form || dbias) {
         const bool vec = N % 8 == 0 && operand_ok(dy, lddy, N) && (!pre || operand_ok(pre, ldpre, N));
         const int v = vec ? 8 : 1;
-        const int64_t cols = ((int64_t)N + kDpreThreads * v - 1) / (kDpreThreads * v);
-        const dim3 grid((unsigned)blocks, (unsigned)(cols < 65535 ? cols : 65535));
-        count_launches(1);
-        auto kern = vec ? k_linear_dpre<8> : k_linear_dpre<1>;
-        kern<<<grid, kDpreThreads, 0, s>>>(dy, lddy, pre, ldpre, M, N, act, form ? own : nullptr, padded(N),
-                                           dbias ? part : nullptr, status);
-        e = cudaGetLastError();
+        int split = 1;
+        while (split < kSumRows && (int64_t)N * 2 * split <= (int64_t)kDpreThreads * v) split *= 2;
+        const int wide = kDpreThreads / split;
+        auto kern = vec ? (split > 1 ? k_linear_dpre<8, true> : k_linear_dpre<8, false>)
+                        : (split > 1 ? k_linear_dpre<1, true> : k_linear_dpre<1, false>);
+        // (a launch has at most 65535 blocks across)
+        for (int64_t c = 0; c < N && e == cudaSuccess; c += 65535ll * wide * v) {
+            const int64_t across = (N - c + wide * v - 1) / (wide * v);
+            count_launches(1);
+            kern<<<dim3((unsigned)blocks, (unsigned)(across < 65535 ? across : 65535)), kDpreThreads, 0, s>>>(
+                dy, lddy, pre, ldpre, M, N, act, form ? own : nullptr, padded(N), dbias ? part : nullptr, split, (int)c, status);
+            e = cudaGetLastError();
+        }
         if (e == cudaSuccess && dbias) e = launch_block_sums(part, blocks, N, dbias, status, s);
     }
     if (e == cudaSuccess && dx) {

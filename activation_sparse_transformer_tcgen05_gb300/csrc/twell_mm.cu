@@ -1339,19 +1339,48 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per);
 }
 
-// Rows up to which the weights' rows are the tensor cores' 128-row operand.
-constexpr int kFewMost = 128;
+// Few rows: up to this many always, up to kFewTry where an estimate says so.
+constexpr int kFewMost = 128, kFewTry = 1024;
 
-// Parts of the depth: as few as keep about one CTA on each SM, and no part shorter than four k-blocks.
-int few_parts(int64_t tiles, int depth, int sms)
+// How k_mm_few would work on `rows` rows and `tiles` tiles of output columns.
+struct FewPlan {
+    int tokens, blocks, parts, per;  // of a tile, blocks of them, parts of the depth, k-blocks of one
+    float us;                        // about
+};
+
+FewPlan few_plan(int rows, int64_t tiles, int depth, bool f32, int sms)
 {
-    int parts = 1;
-    while (parts < 8 && tiles * parts < sms && depth / (2 * parts) >= 4) parts *= 2;
-    return parts;
+    FewPlan p{};
+    p.tokens = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    while (true) {
+        p.blocks = (rows + p.tokens - 1) / p.tokens;
+        // parts of the depth: as few as keep about one CTA on each SM, and none shorter than four k-blocks
+        p.parts = 1;
+        while (p.parts < 8 && tiles * p.blocks * p.parts < sms && depth / (2 * p.parts) >= 4) p.parts *= 2;
+        p.per = (depth + p.parts - 1) / p.parts;
+        // (fp32 results in pieces of at most 1024 of depth: with 128 tokens there are two accumulators for them)
+        if (p.tokens < 128 || !f32 || p.per <= 32) break;
+        p.tokens = 64;
+    }
+    const float ctas = (float)(tiles * p.blocks * p.parts), slots = 2.f * (float)sms;
+    const float at_once = ctas < slots ? ctas : slots;
+    // a k-block takes 0.2 us by itself, 0.55 where two CTAs share each SM (256 to 512 rows x 128 to 4096 x 512 to 14336)
+    const float each = 0.0018f * at_once;
+    p.us = 9.5f + ceilf(ctas / slots) * (float)p.per * (each > 0.2f ? each : 0.2f);
+    return p;
+}
+
+// The same of the CTA pairs' kernel, whose k-blocks of 256 x 256 take 0.275 us: its parts are 2.5 us each (run_pair).
+float pair_us(int64_t rows, int64_t cols, int depth, int sms)
+{
+    const int64_t tiles = (rows + PAIR_M - 1) / PAIR_M * ((cols + PAIR_N - 1) / PAIR_N), pairs = sms / 2;
+    const int parts = tiles <= 15 && depth >= 48 ? 4 : tiles <= 36 && depth >= 24 ? 2 : 1;
+    const float waves = parts > 1 ? 1.f : (float)((tiles + pairs - 1) / pairs);
+    return 6.6f + (parts == 4 ? 5.f : parts == 2 ? 2.5f : 0.f) + waves * (float)((depth + parts - 1) / parts) * 0.275f;
 }
 
 template <int EPI, int BN, bool W_MN>
-cudaError_t run_few(const Maps& maps, Args a, int sms, cudaStream_t s)
+cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cudaStream_t s)
 {
     using L = FewSmem<BN>;
     auto kern = k_mm_few<EPI, BN, W_MN>;
@@ -1359,10 +1388,9 @@ cudaError_t run_few(const Maps& maps, Args a, int sms, cudaStream_t s)
     if (e != cudaSuccess) return e;
     constexpr int COLS = EPI == GATED ? kFewRows / 2 : kFewRows;
     const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
-    const int blocks = (a.rowsA + BN - 1) / BN, depth = a.num_kb * a.segments;
-    const int parts = few_parts(tiles * blocks, depth, sms), per = (depth + parts - 1) / parts;
+    const int blocks = plan.blocks, parts = plan.parts, per = plan.per;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
-    // fp32 results in pieces of 512 of depth (2 to 3 units lost in each), or two of any length
+    // fp32 results in pieces of 512 of depth (2 to 3 units lost in each), or two of up to 1024
     a.piece = per;
     if (a.out_f32) a.piece = L::DRAINED || (per + 1) / 2 < 8 ? 8 : (per + 1) / 2;
     const int held = per > a.piece ? 2 : 1;  // accumulators
@@ -1390,17 +1418,14 @@ cudaError_t run_few(const Maps& maps, Args a, int sms, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per, stages, cols);
 }
 
-// Tokens a tile holds for this many rows.
-int few_tokens(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
-
 template <int EPI, bool W_MN>
-cudaError_t run_few_rows(const Maps& maps, const Args& a, int sms, cudaStream_t s)
+cudaError_t run_few_rows(const Maps& maps, const Args& a, const FewPlan& plan, int sms, cudaStream_t s)
 {
-    switch (few_tokens(a.rowsA)) {
-        case 16: return run_few<EPI, 16, W_MN>(maps, a, sms, s);
-        case 32: return run_few<EPI, 32, W_MN>(maps, a, sms, s);
-        case 64: return run_few<EPI, 64, W_MN>(maps, a, sms, s);
-        default: return run_few<EPI, 128, W_MN>(maps, a, sms, s);
+    switch (plan.tokens) {
+        case 16: return run_few<EPI, 16, W_MN>(maps, a, plan, sms, s);
+        case 32: return run_few<EPI, 32, W_MN>(maps, a, plan, sms, s);
+        case 64: return run_few<EPI, 64, W_MN>(maps, a, plan, sms, s);
+        default: return run_few<EPI, 128, W_MN>(maps, a, plan, sms, s);
     }
 }
 
@@ -1415,9 +1440,12 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
 {
     Maps maps;
     const int n = m.segments * m.problems;
-    const bool few = m.M <= kFewMost && m.problems == 1 && !m.accumulate && !m.a[0].mn;
+    const int depth = (m.K + BK - 1) / BK * m.segments;
+    const FewPlan plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, m.out_f32, sms);
+    const bool few = m.problems == 1 && !m.accumulate && !m.a[0].mn &&
+                     (m.M <= kFewMost || (m.M <= kFewTry && plan.us < pair_us(m.M, m.N, depth, sms)));
     for (int i = 0; i < n; ++i)
-        if (!map_of(&maps.a[i], m.a[i], m.M, m.K, few ? few_tokens(m.M) : HALF) || !map_of(&maps.b[i], m.b[i], m.N, m.K, HALF))
+        if (!map_of(&maps.a[i], m.a[i], m.M, m.K, few ? plan.tokens : HALF) || !map_of(&maps.b[i], m.b[i], m.N, m.K, HALF))
             return cudaErrorInvalidValue;
     for (int i = n; i < kMmParts; ++i) maps.a[i] = maps.a[0], maps.b[i] = maps.b[0];
     Args a{};
@@ -1442,10 +1470,10 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     for (int i = 0; i < m.problems; ++i) out_vec = out_vec && pieces_of_16(m.out[i], m.ldo, m.N, es);
     a.vec = (out_vec ? VEC_OUT : 0) | (m.res && pieces_of_16(m.res, m.ldres, m.N, es) ? VEC_RES : 0) |
             (m.pre && pieces_of_16(m.pre, m.ldpre, m.N, 2) ? VEC_PRE : 0);
-    a.early = few && m.after_gated;
+    a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch was k_mm_few too)
     a.status = m.status;
     const bool amn = m.a[0].mn, bmn = m.b[0].mn;
-    if (few) return bmn ? run_few_rows<LINEAR, true>(maps, a, sms, s) : run_few_rows<LINEAR, false>(maps, a, sms, s);
+    if (few) return bmn ? run_few_rows<LINEAR, true>(maps, a, plan, sms, s) : run_few_rows<LINEAR, false>(maps, a, plan, sms, s);
     if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s);
     if (amn) return cudaErrorInvalidValue;
     if (bmn) return run_pair<LINEAR, false, true>(maps, a, s);
@@ -1456,8 +1484,9 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
 {
     Maps maps;
     const bool few = m.M <= kFewMost;
+    const FewPlan plan = few_plan(m.M, ((int64_t)m.F + kFewRows / 2 - 1) / (kFewRows / 2), (m.K + BK - 1) / BK, false, sms);
     const int w_rows = few ? kFewRows / 2 : HALF;
-    if (!make_map(&maps.a[0], m.x, m.M, m.K, few ? few_tokens(m.M) : HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, w_rows) ||
+    if (!make_map(&maps.a[0], m.x, m.M, m.K, few ? plan.tokens : HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, w_rows) ||
         !make_map(&maps.b[1], m.Wu, m.F, m.K, w_rows))
         return cudaErrorInvalidValue;
     maps.a[1] = maps.a[2] = maps.a[0];
@@ -1475,7 +1504,7 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
     a.h = m.h;
     a.ldo = m.F;
     a.status = m.status;
-    if (few) return run_few_rows<GATED, false>(maps, a, sms, s);
+    if (few) return run_few_rows<GATED, false>(maps, a, plan, sms, s);
     return run_pair<GATED, false, false>(maps, a, s);
 }
 
