@@ -1,6 +1,7 @@
 """GB300-native (sm_103a) TwELL activation-sparse feed-forward layer, and what
 a language model's training step needs around it: layer norm, the cross entropy
-of a linear head, gradient clipping.
+of a linear head, gradient clipping, the gated layer's dense training, linear
+layers, the optimiser's step.
 
 The compute path is the CUDA library ``libtwell.so`` (C ABI in
 ``include/twell.h``); ``twell`` is its thin ctypes binding (argument

@@ -39,7 +39,7 @@ constexpr int kBox = 4096;  // 32 rows x 128 bytes of one epilogue warp
 
 // GATED_BWD's results take the longest to form (two matrices in, two out, column sums): 16 warps of 64 columns, and a
 // ring one stage shorter for their boxes. With eight of 128 the epilogue took longer than a tile's products (8192 x 4096 x
-// 14336 807 us; with 16, and g and u asked for early, 700).
+// 14336 807 us; with 16, and g and u asked for early, 690 in pieces of 1024 of depth, 730 of 768).
 template <int EPI>
 struct Smem {
     static constexpr int STAGES = EPI == GATED_BWD ? 5 : 6;
@@ -56,11 +56,12 @@ struct Smem {
     static_assert(TOTAL <= 227 * 1024, "shared memory of one CTA");
 };
 
-// The tensor cores' fp32 sums drop what does not fit, towards zero, at each step of 16 of depth: over 1024
-// by 7 units of 2^-23 of the result, over 4096 by 31 to 70, over 16384 four times that. Results that leave in fp32
-// are therefore summed 1024 at a time and the pieces added up with rounding; for bf16 the loss is a hundredth of
-// the result's own rounding and the tensor cores sum the whole depth.
-constexpr int kPieceBlocks = 16;
+// The tensor cores' fp32 sums drop what does not fit, towards zero, at each step of 16 of depth: over 512 by 2 to 3
+// units of 2^-23 of the result, over 1024 by 7, over 4096 by 31 to 70, over 16384 four times that. Results that leave in
+// fp32 are therefore summed 768 at a time and the pieces added up with rounding (within 1e-6 of 64 bits, as plain fp32
+// sums are; with 1024 just not); for bf16 the loss is a hundredth of the result's own rounding and the tensor cores sum
+// the whole depth.
+constexpr int kPieceBlocks = 12;
 
 struct Maps {
     CUtensorMap a[kMmParts], b[kMmParts];
@@ -1358,8 +1359,8 @@ FewPlan few_plan(int rows, int64_t tiles, int depth, bool f32, int sms)
         p.parts = 1;
         while (p.parts < 8 && tiles * p.blocks * p.parts < sms && depth / (2 * p.parts) >= 4) p.parts *= 2;
         p.per = (depth + p.parts - 1) / p.parts;
-        // (fp32 results in pieces of at most 1024 of depth: with 128 tokens there are two accumulators for them)
-        if (p.tokens < 128 || !f32 || p.per <= 32) break;
+        // (fp32 results in pieces of at most kPieceBlocks: with 128 tokens there are two accumulators for them)
+        if (p.tokens < 128 || !f32 || p.per <= 2 * kPieceBlocks) break;
         p.tokens = 64;
     }
     const float ctas = (float)(tiles * p.blocks * p.parts), slots = 2.f * (float)sms;
@@ -1390,7 +1391,7 @@ cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cuda
     const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
     const int blocks = plan.blocks, parts = plan.parts, per = plan.per;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
-    // fp32 results in pieces of 512 of depth (2 to 3 units lost in each), or two of up to 1024
+    // fp32 results in pieces of 512 of depth, or two of up to kPieceBlocks
     a.piece = per;
     if (a.out_f32) a.piece = L::DRAINED || (per + 1) / 2 < 8 ? 8 : (per + 1) / 2;
     const int held = per > a.piece ? 2 : 1;  // accumulators
@@ -1429,6 +1430,13 @@ cudaError_t run_few_rows(const Maps& maps, const Args& a, const FewPlan& plan, i
     }
 }
 
+// Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
+int piece_of(int depth)
+{
+    const int pieces = (depth + kPieceBlocks - 1) / kPieceBlocks;
+    return (depth + pieces - 1) / pieces;
+}
+
 bool pieces_of_16(const void* p, int64_t ld, int n, int es)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * es % 16 == 0 && (int64_t)n * es % 16 == 0;
@@ -1454,7 +1462,7 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = m.segments;
     a.problems = m.problems;
-    a.piece = m.out_f32 ? kPieceBlocks : a.num_kb * a.segments;
+    a.piece = m.out_f32 ? piece_of(depth) : depth;
     a.bias = m.bias;
     a.act = m.act;
     a.res = m.res;
@@ -1521,7 +1529,7 @@ cudaError_t launch_mm_gated_bwd(const MmGatedBwd& m, int sms, cudaStream_t s)
     a.rowsB = m.F;
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = a.problems = 1;
-    a.piece = m.part ? kPieceBlocks : a.num_kb;
+    a.piece = m.part ? piece_of(a.num_kb) : a.num_kb;
     a.act = m.act;
     a.l1 = m.l1;
     a.g_in = m.g;

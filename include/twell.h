@@ -478,7 +478,7 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * fastest). M >= 0, N >= 1, K % 8 == 0; with w_kn N % 8 == 0. Limit of this build:
  * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res; other outputs must not
  * overlap inputs (the call rejects equal pointers).
- * Sums are fp32 (fp32 results are added up in rounded pieces of 1024 of depth),
+ * Sums are fp32 (fp32 results are added up in rounded pieces of at most 768 of depth),
  * outputs are rounded once.
  *
  * twell_linear_bwd: dy [M, N] bf16; pre as the forward kept it (NULL if act is
