@@ -873,7 +873,9 @@ struct FewSmem {
     static constexpr int TWO = BN <= 32 ? 5 : BN == 64 ? 4 : 3;
     static constexpr int THREE = BN == 16 ? 4 : BN <= 64 ? 3 : 2;
     // Accumulators. Up to 64 tokens: a second one for results in pieces, which the epilogue's threads add up in
-    // registers while the next piece is formed; with 128 (too many for registers) each piece has its own.
+    // registers while the next piece is formed; with 128 (too many for registers) the first one keeps the sum, and each
+    // later piece is formed in the second and added to it before the next may begin (128 x 50001 x 2048, fp32: 52 us;
+    // 70 in two blocks of 64 tokens, which read W twice).
     static constexpr bool DRAINED = BN <= 64;
     static_assert(TWO <= MOST && 2 * (total(TWO) + 1024) <= 228 * 1024 && 3 * (total(THREE) + 1024) <= 228 * 1024, "the SM's");
     static_assert(kFewRows * BN * 4 <= THREE * STAGE_BYTES, "the parts take the ring's place");
@@ -1056,6 +1058,7 @@ __global__ void __launch_bounds__(kFewThreads, 3)
     };
     const int pieces = (kb1 - kb0 + a.piece - 1) / a.piece;
     const bool drain = L::DRAINED && pieces > 1;
+    const bool merge = !L::DRAINED && pieces > 2;
     const int ahead = min(kb1 - kb0, stages);  // the ring's first round, which needs no wait
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -1119,9 +1122,16 @@ __global__ void __launch_bounds__(kFewThreads, 3)
                 }
                 tc_fence_after();
                 const int i = kb - kb0, piece = i / a.piece, in_piece = i - piece * a.piece;
-                const int acc = drain ? piece & 1 : piece;
+                const int acc = drain ? piece & 1 : min(piece, 1);
                 if (drain && in_piece == 0 && piece >= 2) {  // its last sums have been read
                     if (!mbar_wait(&tempty[acc], (uint32_t)((piece >> 1) & 1) ^ 1u, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                if (merge && in_piece == 0 && piece >= 2) {  // the piece before has been added to the sum
+                    if (!mbar_wait(&tempty[1], (uint32_t)piece & 1u, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -1136,6 +1146,7 @@ __global__ void __launch_bounds__(kFewThreads, 3)
                     umma_bf16(d_tmem, wdesc + W_KSTEP * k, xdesc + 2u * k, IDESC, (in_piece | k) != 0);
                 umma_commit(&empty[stage]);
                 if (drain && (in_piece == a.piece - 1 || kb == kb1 - 1)) umma_commit(&tfull[acc]);
+                if (merge && in_piece == a.piece - 1 && piece > 0 && piece < pieces - 1) umma_commit(&tfull[1]);
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
@@ -1165,6 +1176,24 @@ __global__ void __launch_bounds__(kFewThreads, 3)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&tempty[p & 1]);
             }
+        }
+    } else if (warp >= 2 && merge) {
+        for (int p = 1; p < pieces - 1; ++p) {  // (the last one is added below)
+            if (!__all_sync(0xffffffffu, mbar_wait(&tfull[1], (uint32_t)(p - 1) & 1u, abort_flag))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c0 = 0; c0 < BN; c0 += 32) {
+                uint32_t v[32], w[32];
+                tmem_ld32_wait(lanes_at + (uint32_t)c0, v);
+                tmem_ld32_wait(lanes_at + (uint32_t)(BN + c0), w);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(w[c]));
+                tmem_st32(lanes_at + (uint32_t)c0, v);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[1]);
         }
     }
     __syncwarp();
@@ -1221,7 +1250,7 @@ __global__ void __launch_bounds__(kFewThreads, 3)
                 float v[16];
 #pragma unroll
                 for (int c = 0; c < 16; ++c) v[c] = 0.f;
-                for (int p = 0; p < pieces; ++p) {
+                for (int p = 0; p < min(pieces, 2); ++p) {
                     uint32_t w[16];
                     tmem_ld16_wait(lanes_at + (uint32_t)(p * BN + c0), w);
 #pragma unroll
@@ -1349,20 +1378,15 @@ struct FewPlan {
     float us;                        // about
 };
 
-FewPlan few_plan(int rows, int64_t tiles, int depth, bool f32, int sms)
+FewPlan few_plan(int rows, int64_t tiles, int depth, int sms)
 {
     FewPlan p{};
     p.tokens = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-    while (true) {
-        p.blocks = (rows + p.tokens - 1) / p.tokens;
-        // parts of the depth: as few as keep about one CTA on each SM, and none shorter than four k-blocks
-        p.parts = 1;
-        while (p.parts < 8 && tiles * p.blocks * p.parts < sms && depth / (2 * p.parts) >= 4) p.parts *= 2;
-        p.per = (depth + p.parts - 1) / p.parts;
-        // (fp32 results in pieces of at most kPieceBlocks: with 128 tokens there are two accumulators for them)
-        if (p.tokens < 128 || !f32 || p.per <= 2 * kPieceBlocks) break;
-        p.tokens = 64;
-    }
+    p.blocks = (rows + p.tokens - 1) / p.tokens;
+    // parts of the depth: as few as keep about one CTA on each SM, and none shorter than four k-blocks
+    p.parts = 1;
+    while (p.parts < 8 && tiles * p.blocks * p.parts < sms && depth / (2 * p.parts) >= 4) p.parts *= 2;
+    p.per = (depth + p.parts - 1) / p.parts;
     const float ctas = (float)(tiles * p.blocks * p.parts), slots = 2.f * (float)sms;
     const float at_once = ctas < slots ? ctas : slots;
     // a k-block takes 0.2 us by itself, 0.55 where two CTAs share each SM (256 to 512 rows x 128 to 4096 x 512 to 14336)
@@ -1380,6 +1404,13 @@ float pair_us(int64_t rows, int64_t cols, int depth, int sms)
     return 6.6f + (parts == 4 ? 5.f : parts == 2 ? 2.5f : 0.f) + waves * (float)((depth + parts - 1) / parts) * 0.275f;
 }
 
+// Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
+int piece_of(int depth)
+{
+    const int pieces = (depth + kPieceBlocks - 1) / kPieceBlocks;
+    return (depth + pieces - 1) / pieces;
+}
+
 template <int EPI, int BN, bool W_MN>
 cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cudaStream_t s)
 {
@@ -1391,9 +1422,9 @@ cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cuda
     const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
     const int blocks = plan.blocks, parts = plan.parts, per = plan.per;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
-    // fp32 results in pieces of 512 of depth, or two of up to kPieceBlocks
+    // fp32 results in pieces of 512 of depth; of 128 tokens, where a piece waits for the one before, longer ones
     a.piece = per;
-    if (a.out_f32) a.piece = L::DRAINED || (per + 1) / 2 < 8 ? 8 : (per + 1) / 2;
+    if (a.out_f32) a.piece = L::DRAINED ? 8 : piece_of(per);
     const int held = per > a.piece ? 2 : 1;  // accumulators
     uint32_t cols = 32;
     while (cols < (uint32_t)(held * BN)) cols *= 2;
@@ -1430,13 +1461,6 @@ cudaError_t run_few_rows(const Maps& maps, const Args& a, const FewPlan& plan, i
     }
 }
 
-// Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
-int piece_of(int depth)
-{
-    const int pieces = (depth + kPieceBlocks - 1) / kPieceBlocks;
-    return (depth + pieces - 1) / pieces;
-}
-
 bool pieces_of_16(const void* p, int64_t ld, int n, int es)
 {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * es % 16 == 0 && (int64_t)n * es % 16 == 0;
@@ -1449,7 +1473,7 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     Maps maps;
     const int n = m.segments * m.problems;
     const int depth = (m.K + BK - 1) / BK * m.segments;
-    const FewPlan plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, m.out_f32, sms);
+    const FewPlan plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, sms);
     const bool few = m.problems == 1 && !m.accumulate && !m.a[0].mn &&
                      (m.M <= kFewMost || (m.M <= kFewTry && plan.us < pair_us(m.M, m.N, depth, sms)));
     for (int i = 0; i < n; ++i)
@@ -1492,7 +1516,7 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
 {
     Maps maps;
     const bool few = m.M <= kFewMost;
-    const FewPlan plan = few_plan(m.M, ((int64_t)m.F + kFewRows / 2 - 1) / (kFewRows / 2), (m.K + BK - 1) / BK, false, sms);
+    const FewPlan plan = few_plan(m.M, ((int64_t)m.F + kFewRows / 2 - 1) / (kFewRows / 2), (m.K + BK - 1) / BK, sms);
     const int w_rows = few ? kFewRows / 2 : HALF;
     if (!make_map(&maps.a[0], m.x, m.M, m.K, few ? plan.tokens : HALF) || !make_map(&maps.b[0], m.Wg, m.F, m.K, w_rows) ||
         !make_map(&maps.b[1], m.Wu, m.F, m.K, w_rows))

@@ -92,6 +92,24 @@ def test_strides_and_alignment(pad, offset, M, y_type):
         _forward(M, N, 200, False, "relu", y_type, True, True, True, pad=pad, offset=offset)
 
 
+@pytest.mark.parametrize("M,N,K,kn", [(65, 20001, 1544, False), (100, 20000, 2048, True), (128, 20001, 4096, False), (127, 1000, 14336, True),
+                                      (128, 136, 14400, False), (200, 2048, 8192, False), (1000, 640, 4104, False)])
+def test_fp32_results_of_any_depth(M, N, K, kn):
+    """fp32 results are summed in pieces of at most 48 steps of the tensor cores (K = 16 each). A step drops at most 2^-23
+    of the sum so far, which after s steps is sqrt(s / 48) of the piece's in the mean square: 2/3 of 48 units of 2^-23 of
+    a piece, and as much of the result, since the pieces are independent; and half a unit for each piece added."""
+    _forward(M, N, K, kn, "gelu", F32, True, True, True)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, W = _rand(g, M, K), _rand(g, *((K, N) if kn else (N, K)), scale=K ** -0.5)
+    y, again = (torch.empty(M, N, device="cuda") for _ in range(2))
+    st = _status()
+    for out in (y, again):
+        tw.twell_linear_fwd(x, W, kn, None, tw.ACT_NONE, None, None, out, st)
+    assert tw.twell_check(st) == 0 and torch.equal(y, again)
+    want = x.double() @ (W.double() if kn else W.double().T)
+    assert float((y.double() - want).norm() / want.norm()) <= (2 / 3 * 48 + K / 768) * 2.0 ** -23
+
+
 def test_residual_in_place():
     g = torch.Generator(device="cuda").manual_seed(3)
     for M in (1, 40, 300):
