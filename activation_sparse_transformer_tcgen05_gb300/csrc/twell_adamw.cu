@@ -38,7 +38,9 @@ constexpr int kBlocksPerSm = 4, kValueBlocksPerSm = 6;
 constexpr int kBlock = TWELL_ADAMW_BLOCK;         // elements that share a scale: one warp's, 8 a lane
 constexpr int kUnit = kBlock * (kThreads / 32);   // elements of one unit of work
 constexpr int kPer = kBlock / 32;
-constexpr int kTable = 256, kSmallTable = 32;     // tensors of one launch: two sizes of its parameters
+// Tensors of one launch: two sizes of its parameters (32,764 bytes at most), the larger one without scales and with them.
+// (500 tensors of 32-bit states, 4 M elements: 24.1 us, in two launches of 256 27.5.)
+constexpr int kSmallTable = 32, kTable = 512, kTable8 = 400;
 constexpr int kMost = 32768;
 constexpr int kMBits = 4, kVBits = 5;             // exponent bits of the codes
 
@@ -46,15 +48,27 @@ constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
 enum { P_F32 = 1, G_F32 = 2, VEC = 4 };  // VEC: everything lies on 16-byte boundaries (copies on 8)
 
+template <int CAP, bool SCALES>
+struct Scales {
+    float* ms[CAP];
+    float* vs[CAP];
+    __device__ __forceinline__ float* m_scale(int k) const { return ms[k]; }
+    __device__ __forceinline__ float* v_scale(int k) const { return vs[k]; }
+};
 template <int CAP>
-struct Table {
+struct Scales<CAP, false> {
+    __device__ __forceinline__ float* m_scale(int) const { return nullptr; }
+    __device__ __forceinline__ float* v_scale(int) const { return nullptr; }
+};
+
+template <int CAP, bool SCALES>
+struct Table : Scales<CAP, SCALES> {
     static constexpr int kCap = CAP;
+    static constexpr bool kScales = SCALES;
     void* p[CAP];
     const void* g[CAP];
     void* m[CAP];
     void* v[CAP];
-    float* ms[CAP];
-    float* vs[CAP];
     uint16_t* copy[CAP];
     int64_t numel[CAP];
     int32_t first[CAP + 1];  // first unit of each tensor
@@ -471,8 +485,9 @@ __device__ __forceinline__ void by_types(int flags, bool whole, F f)
 // STAGED: 8-bit states, some parameters in fp32. (Without any the ring's shared memory would only take the first-level
 // cache away: bf16 parameters 441 instead of 399 us.)
 template <int CAP, bool BITS8, bool STAGED>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_constant__ Table<CAP> t, const Hyper h)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_constant__ Table<CAP, BITS8> t, const Hyper h)
 {
+    static_assert(sizeof(t) + sizeof(h) <= 32764, "parameters of a launch");
     __shared__ Scalars shared;
     if (threadIdx.x == 0) {
         Scalars s;
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
         }
         by_types(t.flags[k], left == kBlock, [&](auto v, auto pf, auto gf) {
             step_block<decltype(v)::value, BITS8, STAGED, decltype(pf)::value, decltype(gf)::value>(
-                t.p[k], t.g[k], t.m[k], t.v[k], t.ms[k], t.vs[k], t.copy[k], i0, left, lane, h, s, moments, params,
+                t.p[k], t.g[k], t.m[k], t.v[k], t.m_scale(k), t.v_scale(k), t.copy[k], i0, left, lane, h, s, moments, params,
                 ring[STAGED ? warp : 0][at], scales);
         });
         at ^= 1;
@@ -541,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) k_adamw(const __grid_c
 
 // The values that 8-bit states stand for: m to p's tensor of the table, v to g's.
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kValueBlocksPerSm) k_adamw_values(const __grid_constant__ Table<CAP> t)
+__global__ void __launch_bounds__(kThreads, kValueBlocksPerSm) k_adamw_values(const __grid_constant__ Table<CAP, true> t)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int u0 = t.from(blockIdx.x), u1 = t.from(blockIdx.x + 1);
@@ -614,12 +629,12 @@ twell_status check_list(const twell_adamw_list* l)
 }
 
 // f(table, blocks) for the list's tensors, CAP of them a launch. p and g of entry i: of(i, &p, &g, &flags).
-template <int CAP, class Of, class F>
+template <int CAP, bool SCALES, class Of, class F>
 twell_status by_tables(const twell_adamw_list* l, int most, Of of, F f)
 {
     int next = 0;
     while (next < l->n) {
-        Table<CAP> t;
+        Table<CAP, SCALES> t;
         t.n = 0;
         int64_t units = 0;
         while (next < l->n && t.n < CAP) {
@@ -630,8 +645,10 @@ twell_status by_tables(const twell_adamw_list* l, int most, Of of, F f)
                 of(next, &t.p[i], &t.g[i], &t.copy[i], &t.flags[i]);
                 t.m[i] = l->m[next];
                 t.v[i] = l->v[next];
-                t.ms[i] = l->state_bits == 8 ? l->m_scale[next] : nullptr;
-                t.vs[i] = l->state_bits == 8 ? l->v_scale[next] : nullptr;
+                if constexpr (SCALES) {
+                    t.ms[i] = l->m_scale[next];
+                    t.vs[i] = l->v_scale[next];
+                }
                 t.numel[i] = n;
                 t.first[i] = (int32_t)units;
                 t.id[i] = next;
@@ -693,18 +710,19 @@ extern "C" twell_status twell_adamw(const twell_adamw_list* list, const float* l
     };
     bool any_f32 = false;
     for (int i = 0; i < list->n; ++i) any_f32 = any_f32 || (list->numel[i] > 0 && list->param_type[i] == TWELL_F32);
-    auto launch = [&](auto table, int blocks) {  // (by value: the parameters of the launch)
-        constexpr int CAP = decltype(table)::kCap;
-        if (!eight)
-            k_adamw<CAP, false, false><<<blocks, kThreads, 0, s>>>(table, h);
+    auto launch = [&](const auto& table, int blocks) {
+        using T = std::decay_t<decltype(table)>;
+        if constexpr (!T::kScales)
+            k_adamw<T::kCap, false, false><<<blocks, kThreads, 0, s>>>(table, h);
         else if (any_f32)
-            k_adamw<CAP, true, true><<<blocks, kThreads, 0, s>>>(table, h);
+            k_adamw<T::kCap, true, true><<<blocks, kThreads, 0, s>>>(table, h);
         else
-            k_adamw<CAP, true, false><<<blocks, kThreads, 0, s>>>(table, h);
+            k_adamw<T::kCap, true, false><<<blocks, kThreads, 0, s>>>(table, h);
     };
+    const int most = sms * kBlocksPerSm;
     if (list->n <= kSmallTable)
-        return by_tables<kSmallTable>(list, sms * kBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) { launch(t, blocks); });
-    return by_tables<kTable>(list, sms * kBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) { launch(t, blocks); });
+        return eight ? by_tables<kSmallTable, true>(list, most, of, launch) : by_tables<kSmallTable, false>(list, most, of, launch);
+    return eight ? by_tables<kTable8, true>(list, most, of, launch) : by_tables<kTable, false>(list, most, of, launch);
 }
 
 extern "C" twell_status twell_adamw_values(const twell_adamw_list* list, const twell_tensor_list* m_out,
@@ -730,11 +748,9 @@ extern "C" twell_status twell_adamw_values(const twell_adamw_list* list, const t
         *copy = nullptr;
         *flags = (uint8_t)((m_out->type[i] == TWELL_F32 ? P_F32 : 0) | (v_out->type[i] == TWELL_F32 ? G_F32 : 0));
     };
-    if (list->n <= kSmallTable)
-        return by_tables<kSmallTable>(list, sms * kValueBlocksPerSm, of, [&](const Table<kSmallTable>& t, int blocks) {
-            k_adamw_values<kSmallTable><<<blocks, kThreads, 0, s>>>(t);
-        });
-    return by_tables<kTable>(list, sms * kValueBlocksPerSm, of, [&](const Table<kTable>& t, int blocks) {
-        k_adamw_values<kTable><<<blocks, kThreads, 0, s>>>(t);
-    });
+    auto launch = [&](const auto& table, int blocks) {
+        k_adamw_values<std::decay_t<decltype(table)>::kCap><<<blocks, kThreads, 0, s>>>(table);
+    };
+    const int most = sms * kValueBlocksPerSm;
+    return list->n <= kSmallTable ? by_tables<kSmallTable, true>(list, most, of, launch) : by_tables<kTable8, true>(list, most, of, launch);
 }

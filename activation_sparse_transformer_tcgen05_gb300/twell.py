@@ -692,8 +692,8 @@ ADAMW_BLOCK = 256  # elements that share a scale of 8-bit states
 class TwellAdamWList:
     """Parameters with their gradients and optimiser states (contiguous device tensors) and the C struct naming them, for
     twell_adamw. m and v: fp32, or uint8 codes with m_scale and v_scale (fp32, one for every ADAMW_BLOCK elements).
-    copies: bf16 tensors that follow fp32 parameters (None, or None in places). Keeps the tensors alive; their memory
-    must stay where it is."""
+    copies: bf16 tensors that follow fp32 parameters (None, or None in places). No tensor may be in the lists twice
+    (tied weights are one parameter), gradients excepted. Keeps the tensors alive; their memory must stay where it is."""
 
     def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, copies=None):
         self.params, self.grads, self.m, self.v = list(params), list(grads), list(m), list(v)
@@ -721,6 +721,11 @@ class TwellAdamWList:
                 if p.dtype is not torch.float32:
                     raise ValueError(f"parameter {i} must be fp32 to have a copy")
                 _vec(self.copies[i], f"copy {i}", k, DTYPE_BF16)
+        # (a tensor that is there twice, such as tied weights, would be updated by two threads at once)
+        written = [t.data_ptr() for ts in (self.params, self.m, self.v, self.m_scale, self.v_scale, self.copies) for t in ts
+                   if t is not None and t.numel()]
+        if len(set(written)) != len(written) or not set(written).isdisjoint(g.data_ptr() for g in self.grads if g.numel()):
+            raise ValueError("a tensor that the step writes is in the lists more than once")
 
         def addresses(ts):
             return (ctypes.c_void_p * n)(*[None if t is None else t.data_ptr() for t in ts])

@@ -323,5 +323,9 @@ def test_lists_are_checked():
         tw.TwellAdamWList(pr.p, pr.g, [t.half() for t in pr.m], pr.v)
     with pytest.raises(ValueError):
         tw.TwellAdamWList(pr.p, pr.g[::-1], pr.m, pr.v)
+    for p, g, m, v in ((pr.p[:1] * 2, pr.g[:1] * 2, pr.m[:1] * 2, pr.v[:1] * 2), (pr.p, pr.g, pr.m, [pr.v[0], pr.m[1]]),
+                       (pr.p, [pr.g[0], pr.m[1]], pr.m, pr.v)):  # tied weights; a state as another; a state as a gradient
+        with pytest.raises(ValueError):
+            tw.TwellAdamWList(p, g, m, v)
     empty = tw.TwellAdamWList([], [], [], [])
     tw.twell_adamw(empty, pr.lr, pr.step, B1, B2, EPS, WD, None, 1.0, 0)
