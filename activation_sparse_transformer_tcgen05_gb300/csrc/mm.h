@@ -39,6 +39,10 @@ struct MmLinear {
 };
 cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s);
 
+// Two of them that do not need one another, in one launch or in two, whichever should be faster: A K-major in the first,
+// A and B as transposes in the second.
+cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, int sms, cudaStream_t s);
+
 // g = x Wg^T + bias, u = x Wu^T, h = act(g) u, all [M, F] bf16; g and u may be null (not kept).
 struct MmGated {
     int M, F, K;

@@ -7,8 +7,8 @@
 // With act = ReLU this is the layer that twell_ffn_fwd serves sparsely (h packed by the gate's
 // active units): here its weights are trained, and rows too dense to pack are served.
 // Forward: two launches, h formed in the first one's epilogue from both projections. Backward:
-// dg and du from dh's product, dx as one product over both of them, and the three weight
-// gradients side by side in one launch; h, g and u are what the forward kept, in bf16.
+// dg and du from dh's product, then dx as one product over both of them and the three weight
+// gradients, in one launch or two; h, g and u are what the forward kept, in bf16.
 #include "common.cuh"
 #include "launch.h"
 #include "mm.h"
@@ -152,8 +152,9 @@ extern "C" twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint1
     hid.status = status;
     e = launch_mm_gated_bwd(hid, sms, s);
     if (e == cudaSuccess && db) e = launch_block_sums(part, (M + kSumRows - 1) / kSumRows, F, db, status, s);
-    if (e == cudaSuccess && dx) {
-        MmLinear m{};
+    MmLinear in{}, w{};
+    if (dx) {
+        MmLinear& m = in;
         m.M = M;
         m.N = d;
         m.K = F;
@@ -166,10 +167,9 @@ extern "C" twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint1
         m.out[0] = dx;
         m.ldo = d;
         m.status = status;
-        e = launch_mm_linear(m, sms, s);
     }
-    if (e == cudaSuccess && grads) {
-        MmLinear m{};
+    if (grads) {
+        MmLinear& m = w;
         m.M = F;
         m.N = d;
         m.K = M;
@@ -185,7 +185,8 @@ extern "C" twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint1
         m.out_f32 = dw_type == TWELL_F32;
         m.accumulate = accumulate != 0;
         m.status = status;
-        e = launch_mm_linear(m, sms, s);
     }
+    if (e == cudaSuccess && (dx || grads))
+        e = dx && grads ? launch_mm_two(in, w, sms, s) : launch_mm_linear(dx ? in : w, sms, s);
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }

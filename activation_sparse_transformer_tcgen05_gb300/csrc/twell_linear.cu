@@ -221,8 +221,9 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
         }
         if (e == cudaSuccess && dbias) e = launch_block_sums(part, blocks, N, dbias, status, s);
     }
-    if (e == cudaSuccess && dx) {
-        MmLinear m{};
+    MmLinear in{}, w{};
+    if (dx) {
+        MmLinear& m = in;
         m.M = M;
         m.N = K;
         m.K = N;
@@ -232,10 +233,9 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
         m.out[0] = dx;
         m.ldo = lddx;
         m.status = status;
-        e = launch_mm_linear(m, sms, s);
     }
-    if (e == cudaSuccess && dW) {
-        MmLinear m{};
+    if (dW) {
+        MmLinear& m = w;
         m.M = w_kn ? K : N;
         m.N = w_kn ? N : K;
         m.K = M;
@@ -248,7 +248,7 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
         m.out_f32 = dw_type == TWELL_F32;
         m.accumulate = accumulate != 0;
         m.status = status;
-        e = launch_mm_linear(m, sms, s);
     }
+    if (e == cudaSuccess && (dx || dW)) e = dx && dW ? launch_mm_two(in, w, sms, s) : launch_mm_linear(dx ? in : w, sms, s);
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }

@@ -524,17 +524,83 @@ __device__ __forceinline__ void put_part(uint8_t* smem, int share, int my_part, 
     for (int c = 0; c < 8; ++c) to[c * HALF] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_constant__ Maps maps, const Args a, int parts_arg, int per)
+// The products of one launch. Two of them (JOBS = 2, LINEAR): a backward pass' dx and its weight gradients, which need the
+// same operands and nothing of one another. Each by itself seldom fills its last wave of tiles; together the short tiles
+// (the weight gradients', as deep as there are rows) fill up what the long ones leave: first the long ones, then the
+// short ones, `delay` rounds of them by the pairs without a long tile in the last round of those alone. (`delay` is what
+// a long tile takes in short ones. In two launches, and in one: linear backward 1000 x 1024 -> 1024 24 us, 14; 4096 x 4096 ->
+// 4096 174, 157; gated backward 2048 x 1000 x 2696 107, 93.)
+template <int JOBS>
+struct Jobs {
+    Maps maps[JOBS];
+    Args args[JOBS];
+    int delay;
+    float us[JOBS];  // about, of a tile (the host's)
+};
+
+__device__ __forceinline__ int tiles_of(const Args& a, int tile_n)
 {
-    const int parts = EPI == LINEAR ? parts_arg : 1;
+    return ((a.rowsA + PAIR_M - 1) / PAIR_M) * ((a.rowsB + tile_n - 1) / tile_n) * a.problems;
+}
+
+// A pair's tiles in their order; all roles of both CTAs walk along the same ones. What does not change lies in shared
+// memory (the epilogue has no registers left).
+struct Route {
+    int pair, pairs, count[2];
+    int start, free, head;  // of job 1: first tile, pairs without a tile in the last round of job 0, tiles for those alone
+};
+
+template <int JOBS, int TILE_N>
+__device__ __forceinline__ void set_route(Route& r, const Jobs<JOBS>& jobs, int pair, int pairs)
+{
+    r.pair = pair;
+    r.pairs = pairs;
+    r.count[0] = tiles_of(jobs.args[0], TILE_N);
+    if constexpr (JOBS > 1) {
+        r.count[1] = tiles_of(jobs.args[1], TILE_N);
+        const int busy = r.count[0] % pairs;
+        r.free = pairs - busy;
+        r.head = jobs.delay * r.free;
+        r.start = pair >= busy ? pair - busy : r.head + pair;
+    }
+}
+
+template <int JOBS>
+struct Walk {
+    const Route& r;
+    int job, tile;
+    __device__ __forceinline__ Walk(const Route& route) : r(route), job(0), tile(route.pair) { enter(); }
+    __device__ __forceinline__ bool more() const { return tile < r.count[JOBS > 1 ? job : 0]; }
+    __device__ __forceinline__ void next()
+    {
+        if (JOBS > 1 && job == 1 && tile < r.head) {
+            tile += r.free;
+            if (tile >= r.head) tile = r.head + r.pair;
+        } else {
+            tile += r.pairs;
+            enter();
+        }
+    }
+    __device__ __forceinline__ void enter()
+    {
+        if (JOBS > 1 && job == 0 && tile >= r.count[0]) {
+            job = 1;
+            tile = r.start;
+        }
+    }
+};
+
+// (of two jobs the first has K-major rows and B_MN, the second both as their transposes)
+template <int EPI, bool A_MN, bool B_MN, int JOBS>
+__global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_constant__ Jobs<JOBS> jobs, int parts_arg, int per)
+{
+    static_assert(JOBS == 1 || (EPI == LINEAR && !A_MN), "two jobs");
+    const int parts = EPI == LINEAR && JOBS == 1 ? parts_arg : 1;
     using L = Smem<EPI>;
     constexpr int kStages = L::STAGES;
-    constexpr uint32_t IDESC =
-        idesc_bf16_f32(PAIR_M, PAIR_N) | (A_MN ? kIdescAMn : 0u) | (B_MN ? kIdescBMn : 0u);
-    constexpr uint64_t A_KSTEP = A_MN ? (16u * 128u) >> 4 : 2u;  // descriptor units (16 B) per 16-deep K step
-    constexpr uint64_t B_KSTEP = B_MN ? (16u * 128u) >> 4 : 2u;
     constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;  // output columns of a tile
+    const Args& first = jobs.args[0];
+    int32_t* const status = first.status;
     extern __shared__ uint8_t smem_raw[];
     // Same offset in both CTAs: the pair's products address the peer's operands with the leader's descriptors.
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -546,6 +612,7 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     volatile int* skip = reinterpret_cast<volatile int*>(tmem_slot + 2);
+    __shared__ Route route;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_rank(), rank = crank & 1u, lead = crank & ~1u;  // rank in the pair, its even CTA
@@ -553,7 +620,9 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
     const uint16_t both_ctas = (uint16_t)(3u << lead);
     const bool leader = rank == 0;
     if (threadIdx.x == 0) {
-        *skip = (crank == 0 && has_error(a.status)) ? 1 : 0;
+        // (in parts: one tile for each cluster)
+        set_route<JOBS, TILE_N>(route, jobs, (int)blockIdx.x / (2 * parts), (int)gridDim.x / (2 * parts));
+        *skip = (crank == 0 && has_error(status)) ? 1 : 0;
         *abort_flag = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -575,24 +644,27 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
         tmem_relinquish_pair();
     }
     if (warp == 0 && lane == 0) {
-        for (int i = 0; i < a.segments * a.problems; ++i) {
-            tma_prefetch_map(&maps.a[i]);
-            tma_prefetch_map(&maps.b[i]);
-        }
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j)
+            for (int i = 0; i < jobs.args[j].segments * jobs.args[j].problems; ++i) {
+                tma_prefetch_map(&jobs.maps[j].a[i]);
+                tma_prefetch_map(&jobs.maps[j].b[i]);
+            }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    const int num_m = (a.rowsA + PAIR_M - 1) / PAIR_M;
-    const int num_n = (a.rowsB + TILE_N - 1) / TILE_N;
-    const int mn_tiles = num_m * num_n;
-    const int num_tiles = mn_tiles * a.problems;
-    const int whole = a.num_kb * a.segments;
-    const int k0 = parts > 1 ? min(my_part * per, whole) : 0, k1 = parts > 1 ? min(k0 + per, whole) : whole;
-    const int depth = k1 - k0;  // of this pair
-    const int pair = (int)blockIdx.x / (2 * parts), num_pairs = (int)gridDim.x / (2 * parts);  // (in parts: one tile each)
+    // this pair's k-blocks of a job's tiles
+    auto from = [&](const Args& a) { return parts > 1 ? min(my_part * per, a.num_kb * a.segments) : 0; };
+    auto to = [&](const Args& a) { return parts > 1 ? min(from(a) + per, a.num_kb * a.segments) : a.num_kb * a.segments; };
+    // a tile's product and coordinates
+    auto locate = [&](const Args& a, int tile, int* problem, int* mb, int* nb) {
+        const int num_m = (a.rowsA + PAIR_M - 1) / PAIR_M, num_n = (a.rowsB + TILE_N - 1) / TILE_N;
+        *problem = tile / (num_m * num_n);
+        pair_tile_coords(tile - *problem * (num_m * num_n), num_m, num_n, mb, nb);
+    };
     Box box{smem + L::BOX_OFF + (warp >= 2 ? warp - 2 : 0) * kBox, lane};
     int last_acc = 0;
 
@@ -604,10 +676,14 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
             uint32_t phase = 0;
             long long issued = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-                int mb, nb;
-                const int problem = tile / mn_tiles;
-                pair_tile_coords(tile - problem * mn_tiles, num_m, num_n, &mb, &nb);
+            for (Walk<JOBS> at(route); ok && at.more(); at.next()) {
+                const int job = JOBS > 1 ? at.job : 0;
+                const Args& a = jobs.args[job];
+                const Maps& maps = jobs.maps[job];
+                const bool a_mn = JOBS > 1 ? job == 1 : A_MN, b_mn = JOBS > 1 ? job == 1 || B_MN : B_MN;
+                int mb, nb, problem;
+                locate(a, at.tile, &problem, &mb, &nb);
+                const int k0 = from(a), k1 = to(a);
                 const int ma = mb * PAIR_M + (int)rank * HALF;
                 // GATED: 128 rows of W_gate in the even CTA, the same rows of W_up in the odd one
                 const int nbr = EPI == GATED ? nb * HALF : nb * PAIR_N + (int)rank * HALF;
@@ -623,13 +699,13 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                         uint8_t* sa = smem + stage * L::STAGE_BYTES;
                         if (leader) mbar_arrive_expect_tx(&full[stage], 2 * L::STAGE_BYTES);
                         const uint32_t fb = full_leader + 8u * (uint32_t)stage;
-                        if (A_MN) {
+                        if (a_mn) {
                             tma_load_2d_pair(sa, ta, ma, kb * BK, fb);
                             tma_load_2d_pair(sa + kMnBox * BK * 2, ta, ma + kMnBox, kb * BK, fb);
                         } else {
                             tma_load_2d_pair(sa, ta, kb * BK, ma, fb);
                         }
-                        if (B_MN) {
+                        if (b_mn) {
                             tma_load_2d_pair(sa + L::A_BYTES, tb, nbr, kb * BK, fb);
                             tma_load_2d_pair(sa + L::A_BYTES + kMnBox * BK * 2, tb, nbr + kMnBox, kb * BK, fb);
                         } else {
@@ -643,7 +719,7 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                     }
                 }
             }
-            if (!ok) fail(a.status, abort_flag);
+            if (!ok) fail(status, abort_flag);
             // The last load issued into each stage must land before the CTA exits: the leader sees it on its full
             // barrier, the peer on its empty barrier (the leader's products consumed it).
             for (int s = 0; s < kStages; ++s) {
@@ -659,7 +735,14 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
             int acc = 0;
             uint32_t acc_phase = 0;
             bool ok = true;
-            for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+            for (Walk<JOBS> at(route); ok && at.more(); at.next()) {
+                const int job = JOBS > 1 ? at.job : 0;
+                const Args& a = jobs.args[job];
+                const bool a_mn = JOBS > 1 ? job == 1 : A_MN, b_mn = JOBS > 1 ? job == 1 || B_MN : B_MN;
+                const uint32_t idesc = idesc_bf16_f32(PAIR_M, PAIR_N) | (a_mn ? kIdescAMn : 0u) | (b_mn ? kIdescBMn : 0u);
+                // descriptor units (16 B) per 16-deep K step
+                const uint64_t a_kstep = a_mn ? (16u * 128u) >> 4 : 2u, b_kstep = b_mn ? (16u * 128u) >> 4 : 2u;
+                const int depth = to(a) - from(a);
                 for (int kb0 = 0, kb1; ok && kb0 < depth; kb0 = kb1) {
                     kb1 = min(kb0 + a.piece, depth);
                     if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, abort_flag)) {
@@ -675,11 +758,11 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                         }
                         tc_fence_after();
                         const uint32_t sa = smem_u32(smem + stage * L::STAGE_BYTES);
-                        const uint64_t adesc = operand_desc(A_MN, sa);
-                        const uint64_t bdesc = operand_desc(B_MN, sa + L::A_BYTES);
+                        const uint64_t adesc = operand_desc(a_mn, sa);
+                        const uint64_t bdesc = operand_desc(b_mn, sa + L::A_BYTES);
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
-                            umma_bf16_pair(d_tmem, adesc + A_KSTEP * k, bdesc + B_KSTEP * k, IDESC, ((kb - kb0) | k) != 0);
+                            umma_bf16_pair(d_tmem, adesc + a_kstep * k, bdesc + b_kstep * k, idesc, ((kb - kb0) | k) != 0);
                         umma_commit_pair(&empty[stage], both_ctas);
                         if (++stage == kStages) {
                             stage = 0;
@@ -692,7 +775,7 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                     if (acc == 0) acc_phase ^= 1u;
                 }
             }
-            if (!ok) fail(a.status, abort_flag);
+            if (!ok) fail(status, abort_flag);
             umma_commit_pair(mma_done, (uint16_t)(1u << lead));  // every product issued above has finished once this arrives
             mbar_wait(mma_done, 0, nullptr);
         }
@@ -702,25 +785,26 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
         const int slice = (warp - 2) >> 2;   // its columns of the accumulator
         const uint32_t tempty_leader = cluster_addr(tempty, lead);
         const uint32_t lanes_at = tmem_base + ((uint32_t)(32 * q) << 16);
-        const bool pieces = EPI != GATED && depth > a.piece;
-        if (EPI == GATED_BWD && pair < num_tiles) {
-            int mb, nb;
-            pair_tile_coords(pair, num_m, num_n, &mb, &nb);
-            HalfBox{box.box, lane}.fetch(0, mb * PAIR_M + (int)rank * HALF + 32 * q, nb * TILE_N + L::COLS * slice, a);
+        Walk<JOBS> at(route);
+        if (EPI == GATED_BWD && at.more()) {
+            int mb, nb, problem;
+            locate(first, at.tile, &problem, &mb, &nb);
+            HalfBox{box.box, lane}.fetch(0, mb * PAIR_M + (int)rank * HALF + 32 * q, nb * TILE_N + L::COLS * slice, first);
             copies_commit();
         }
         int acc = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-            int mb, nb;
-            const int problem = tile / mn_tiles;
-            pair_tile_coords(tile - problem * mn_tiles, num_m, num_n, &mb, &nb);
+        auto finish = [&](const Args& a) {
+            const int depth = to(a) - from(a);
+            const bool pieces = EPI != GATED && depth > a.piece;
+            int mb, nb, problem;
+            locate(a, at.tile, &problem, &mb, &nb);
             const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
             const int col0 = nb * TILE_N + L::COLS * slice;
             const bool live = row0 < a.rowsA && col0 < a.rowsB;  // not all past the last row or column
             ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
-            if (!ok) break;
+            if (!ok) return;
             tc_fence_after();
             if constexpr (EPI != GATED) {
                 if (pieces) {
@@ -729,11 +813,11 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                     for (int k = 0; k < L::COLS; ++k) sum[k] = 0.f;
                     int done = 0;
                     while (true) {
-                        const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
+                        const uint32_t sums = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
                         done += a.piece;
-                        if (live) add_columns(at, sum);
+                        if (live) add_columns(sums, sum);
                         if (done >= depth) {
-                            if (live) set_columns(at, sum);
+                            if (live) set_columns(sums, sum);
                             break;
                         }
                         tc_fence_before();
@@ -745,36 +829,38 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    if (!ok) break;
+                    if (!ok) return;
                 }
             }
             if (EPI == LINEAR && parts > 1) {
                 // (the pair's products are done: its ring is free)
-                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N);
+                const uint32_t sums = lanes_at + (uint32_t)(acc * PAIR_N);
                 last_acc = acc;
                 const int share = PAIR_N / parts;
 #pragma unroll 1
                 for (int c0 = L::COLS * slice; c0 < L::COLS * (slice + 1); c0 += 32) {
                     if (c0 / share == my_part) continue;
                     float v[32];
-                    read_columns(at + (uint32_t)c0, v);
+                    read_columns(sums + (uint32_t)c0, v);
                     put_part(smem, share, my_part, 32 * q + lane, c0, v);
                 }
             } else if (live || EPI == GATED_BWD) {  // (there also to ask for what comes next)
-                const uint32_t at = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
+                const uint32_t sums = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
                 if constexpr (EPI == LINEAR)
-                    epi_linear([&](int c, float (&v)[64]) { read_columns(at + (uint32_t)c, v); }, L::COLS, row0, col0, problem, a,
+                    epi_linear([&](int c, float (&v)[64]) { read_columns(sums + (uint32_t)c, v); }, L::COLS, row0, col0, problem, a,
                                box);
                 else if constexpr (EPI == GATED)
-                    epi_gated(at, row0, col0, a, box);
+                    epi_gated(sums, row0, col0, a, box);
                 else {
                     int next_row0 = -1, next_col0 = 0;
-                    if (tile + num_pairs < num_tiles) {
-                        pair_tile_coords(tile + num_pairs, num_m, num_n, &mb, &nb);
+                    Walk<JOBS> then = at;
+                    then.next();
+                    if (then.more()) {
+                        locate(a, then.tile, &problem, &mb, &nb);
                         next_row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
                         next_col0 = nb * TILE_N + L::COLS * slice;
                     }
-                    epi_gated_bwd(at, row0, col0, next_row0, next_col0, a, HalfBox{box.box, lane});
+                    epi_gated_bwd(sums, row0, col0, next_row0, next_col0, a, HalfBox{box.box, lane});
                 }
             }
             tc_fence_before();
@@ -783,22 +869,28 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
             if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
+        };
+        for (; ok && at.more(); at.next()) {
+            if (JOBS == 1 || at.job == 0)  // (each with its own, so that they need no registers)
+                finish(jobs.args[0]);
+            else
+                finish(jobs.args[JOBS - 1]);
         }
-        if (!ok) fail(a.status, abort_flag);
+        if (!ok) fail(status, abort_flag);
         if (EPI == GATED_BWD) asm volatile("cp.async.wait_all;" ::: "memory");  // (copies may be left after a wait that ran out)
     }
 
-    if constexpr (EPI == LINEAR) {
+    if constexpr (EPI == LINEAR && JOBS == 1) {
         if (parts > 1) {
+            const Args& a = first;
             __syncwarp();
             tc_fence_before();
             cluster_sync();
             tc_fence_after();
             if (warp >= 2 && !has_error(a.status)) {  // (a wait that ran out has left a part undefined)
                 const int q = warp & 3, half = (warp - 2) >> 2;
-                int mb, nb;
-                const int problem = pair / mn_tiles;
-                pair_tile_coords(pair - problem * mn_tiles, num_m, num_n, &mb, &nb);
+                int mb, nb, problem;
+                locate(a, route.pair, &problem, &mb, &nb);
                 const int share = PAIR_N / parts, width = share / 2;  // 64 or 32 columns of a warp
                 const int first = my_part * share + half * width;
                 const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q, col0 = nb * PAIR_N + first;
@@ -1315,10 +1407,38 @@ bool map_of(CUtensorMap* m, const MmOperand& o, int rows, int K, int box_rows)
     return o.mn ? make_map_mn(m, o.p, rows, K, (int)o.ld) : make_map(m, o.p, rows, K, box_rows, (int)o.ld);
 }
 
-template <int EPI, bool A_MN, bool B_MN>
-cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
+// What a tile of 256 x 256 takes a pair among others, in us: 0.3 a k-block, and 1 between tiles. (Depths of 64 to 14336;
+// rows that do not lie on 128-byte boundaries: 0.41 a k-block.)
+float tile_us(const Args& a, bool rows128)
 {
-    auto kern = k_mm_pair<EPI, A_MN, B_MN>;
+    return 1.f + (rows128 ? 0.3f : 0.41f) * (float)a.num_kb * (float)a.segments;
+}
+
+// How two jobs' tiles share the pairs.
+struct Split {
+    int delay;   // rounds of the second's tiles for the pairs without a last tile of the first
+    float most;  // of the pair with the most
+    Split(const Args& one, const Args& two, float us1, float us2, int pairs)
+    {
+        auto tiles = [](const Args& a) {
+            return ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + PAIR_N - 1) / PAIR_N) * a.problems;
+        };
+        const int64_t t1 = tiles(one), t2 = tiles(two), busy = t1 % pairs, free = pairs - busy;
+        const int64_t enough = (t2 + free - 1) / free;
+        const float about = us1 / us2 + 0.5f;
+        const int64_t rounds = about < 1.f ? 1 : about > (float)enough ? enough : (int64_t)about;
+        delay = (int)rounds;
+        const int64_t later = t2 > rounds * free ? (t2 - rounds * free + pairs - 1) / pairs : 0;
+        const float with = (float)(t1 / pairs + (busy > 0)) * us1 + (float)later * us2;
+        const float without = (float)(t1 / pairs) * us1 + (float)(rounds + later) * us2;
+        most = with > without ? with : without;
+    }
+};
+
+template <int EPI, bool A_MN, bool B_MN, int JOBS>
+cudaError_t run_jobs(Jobs<JOBS>& jobs, cudaStream_t s)
+{
+    auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -1341,7 +1461,7 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (known[dev][0] <= 0) {
         for (int i = 2; i >= 0; --i) {  // (the first entry last: it says that all are known)
-            if (i > 0 && EPI != LINEAR) continue;
+            if (i > 0 && (EPI != LINEAR || JOBS > 1)) continue;
             int n = 0;
             attr[0].val.clusterDim.x = 2u << i;
             cfg.gridDim = dim3(2u << i, 1, 1);
@@ -1353,20 +1473,30 @@ cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
         }
     }
     constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;
-    const int64_t tiles =
-        ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + TILE_N - 1) / TILE_N) * a.problems;
+    int64_t tiles = 0;
+    for (const Args& a : jobs.args)
+        tiles += ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + TILE_N - 1) / TILE_N) * a.problems;
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
     // Few tiles: the depth in as many parts as run at once, if none is shorter than 12 k-blocks (joining takes about
     // 2.5 us for each part more, as long as 9 k-blocks); so no part is empty.
-    const int depth = a.num_kb * a.segments;
+    const int depth = jobs.args[0].num_kb * jobs.args[0].segments;
     int parts = 1;
     for (int i = 1; i <= 2; ++i)
-        if (EPI == LINEAR && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
+        if (EPI == LINEAR && JOBS == 1 && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
     const int per = (depth + parts - 1) / parts;
+    const int clusters = (int)(parts > 1 || tiles < known[dev][0] ? tiles : known[dev][0]);
+    if constexpr (JOBS > 1) jobs.delay = Split(jobs.args[0], jobs.args[1], jobs.us[0], jobs.us[1], clusters).delay;
     attr[0].val.clusterDim.x = 2u * (unsigned)parts;
-    cfg.gridDim = dim3(2u * (unsigned)parts * (unsigned)(parts > 1 || tiles < known[dev][0] ? tiles : known[dev][0]), 1, 1);
+    cfg.gridDim = dim3(2u * (unsigned)parts * (unsigned)clusters, 1, 1);
     count_launches(1);
-    return cudaLaunchKernelEx(&cfg, kern, maps, a, parts, per);
+    return cudaLaunchKernelEx(&cfg, kern, jobs, parts, per);
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
+{
+    Jobs<1> jobs{{maps}, {a}, 0, {0.f}};
+    return run_jobs<EPI, A_MN, B_MN, 1>(jobs, s);
 }
 
 // Few rows: up to this many always, up to kFewTry where an estimate says so.
@@ -1395,13 +1525,16 @@ FewPlan few_plan(int rows, int64_t tiles, int depth, int sms)
     return p;
 }
 
-// The same of the CTA pairs' kernel, whose k-blocks of 256 x 256 take 0.275 us: its parts are 2.5 us each (run_pair).
-float pair_us(int64_t rows, int64_t cols, int depth, int sms)
+// The same of the CTA pairs' kernel, whose parts are 2.5 us each (run_jobs).
+float pair_us(int64_t rows, int64_t cols, int problems, int depth, bool rows128, int sms)
 {
-    const int64_t tiles = (rows + PAIR_M - 1) / PAIR_M * ((cols + PAIR_N - 1) / PAIR_N), pairs = sms / 2;
+    const int64_t tiles = (rows + PAIR_M - 1) / PAIR_M * ((cols + PAIR_N - 1) / PAIR_N) * problems, pairs = sms / 2;
     const int parts = tiles <= 15 && depth >= 48 ? 4 : tiles <= 36 && depth >= 24 ? 2 : 1;
     const float waves = parts > 1 ? 1.f : (float)((tiles + pairs - 1) / pairs);
-    return 6.6f + (parts == 4 ? 5.f : parts == 2 ? 2.5f : 0.f) + waves * (float)((depth + parts - 1) / parts) * 0.275f;
+    Args a{};
+    a.num_kb = (depth + parts - 1) / parts;
+    a.segments = 1;
+    return 6.6f + (parts == 4 ? 5.f : parts == 2 ? 2.5f : 0.f) + waves * tile_us(a, rows128);
 }
 
 // Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
@@ -1468,25 +1601,23 @@ bool pieces_of_16(const void* p, int64_t ld, int n, int es)
 
 }  // namespace
 
-cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
+namespace {
+
+// What a launch of m needs, with boxes of `box` rows of A (few rows: the tokens of a tile).
+bool fill(const MmLinear& m, int box, Maps* maps, Args* args)
 {
-    Maps maps;
     const int n = m.segments * m.problems;
-    const int depth = (m.K + BK - 1) / BK * m.segments;
-    const FewPlan plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, sms);
-    const bool few = m.problems == 1 && !m.accumulate && !m.a[0].mn &&
-                     (m.M <= kFewMost || (m.M <= kFewTry && plan.us < pair_us(m.M, m.N, depth, sms)));
     for (int i = 0; i < n; ++i)
-        if (!map_of(&maps.a[i], m.a[i], m.M, m.K, few ? plan.tokens : HALF) || !map_of(&maps.b[i], m.b[i], m.N, m.K, HALF))
-            return cudaErrorInvalidValue;
-    for (int i = n; i < kMmParts; ++i) maps.a[i] = maps.a[0], maps.b[i] = maps.b[0];
-    Args a{};
+        if (!map_of(&maps->a[i], m.a[i], m.M, m.K, box) || !map_of(&maps->b[i], m.b[i], m.N, m.K, HALF)) return false;
+    for (int i = n; i < kMmParts; ++i) maps->a[i] = maps->a[0], maps->b[i] = maps->b[0];
+    Args& a = *args;
+    a = Args{};
     a.rowsA = m.M;
     a.rowsB = m.N;
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = m.segments;
     a.problems = m.problems;
-    a.piece = m.out_f32 ? piece_of(depth) : depth;
+    a.piece = m.out_f32 ? piece_of(a.num_kb * m.segments) : a.num_kb * m.segments;
     a.bias = m.bias;
     a.act = m.act;
     a.res = m.res;
@@ -1502,14 +1633,66 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     for (int i = 0; i < m.problems; ++i) out_vec = out_vec && pieces_of_16(m.out[i], m.ldo, m.N, es);
     a.vec = (out_vec ? VEC_OUT : 0) | (m.res && pieces_of_16(m.res, m.ldres, m.N, es) ? VEC_RES : 0) |
             (m.pre && pieces_of_16(m.pre, m.ldpre, m.N, 2) ? VEC_PRE : 0);
-    a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch was k_mm_few too)
     a.status = m.status;
+    return true;
+}
+
+// Whether all operands' rows lie on 128-byte boundaries.
+bool rows128(const MmLinear& m)
+{
+    for (int i = 0; i < m.segments * m.problems; ++i)
+        if (m.a[i].ld % 64 != 0 || m.b[i].ld % 64 != 0) return false;
+    return true;
+}
+
+// The kernel for m, and about its time.
+struct Choice {
+    FewPlan plan;
+    bool few;
+    float us;
+    Choice(const MmLinear& m, int sms)
+    {
+        const int depth = (m.K + BK - 1) / BK * m.segments;
+        plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, sms);
+        us = pair_us(m.M, m.N, m.problems, depth, rows128(m), sms);
+        few = m.problems == 1 && !m.accumulate && !m.a[0].mn && (m.M <= kFewMost || (m.M <= kFewTry && plan.us < us));
+        if (few) us = plan.us;
+    }
+};
+
+}  // namespace
+
+cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
+{
+    const Choice choice(m, sms);
+    const bool few = choice.few;
+    Maps maps;
+    Args a;
+    if (!fill(m, few ? choice.plan.tokens : HALF, &maps, &a)) return cudaErrorInvalidValue;
+    a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch was k_mm_few too)
     const bool amn = m.a[0].mn, bmn = m.b[0].mn;
-    if (few) return bmn ? run_few_rows<LINEAR, true>(maps, a, plan, sms, s) : run_few_rows<LINEAR, false>(maps, a, plan, sms, s);
+    if (few)
+        return bmn ? run_few_rows<LINEAR, true>(maps, a, choice.plan, sms, s)
+                   : run_few_rows<LINEAR, false>(maps, a, choice.plan, sms, s);
     if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s);
     if (amn) return cudaErrorInvalidValue;
     if (bmn) return run_pair<LINEAR, false, true>(maps, a, s);
     return run_pair<LINEAR, false, false>(maps, a, s);
+}
+
+cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, int sms, cudaStream_t s)
+{
+    if (one.a[0].mn || !two.a[0].mn || !two.b[0].mn || one.status != two.status) return cudaErrorInvalidValue;
+    Jobs<2> jobs;
+    if (!fill(one, HALF, &jobs.maps[0], &jobs.args[0]) || !fill(two, HALF, &jobs.maps[1], &jobs.args[1])) return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i) jobs.us[i] = tile_us(jobs.args[i], rows128(i ? two : one));
+    const Split split(jobs.args[0], jobs.args[1], jobs.us[0], jobs.us[1], sms / 2);
+    // (tiles that run far apart in depth read more from memory, so that a gain of 2 to 4 % by this estimate was a loss of 1
+    // to 3, 8192 x 4096 x 14336 and -> 16384; one of 8 % was a gain of 1.5, 2048 x 4096 x 14336)
+    if (6.6f + split.most < 0.95f * (Choice(one, sms).us + Choice(two, sms).us))
+        return one.b[0].mn ? run_jobs<LINEAR, false, true, 2>(jobs, s) : run_jobs<LINEAR, false, false, 2>(jobs, s);
+    const cudaError_t e = launch_mm_linear(one, sms, s);
+    return e == cudaSuccess ? launch_mm_linear(two, sms, s) : e;
 }
 
 cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)

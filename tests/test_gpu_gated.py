@@ -132,6 +132,16 @@ def test_backward(M, d, F, dw_type):
     layer.check_backward(dy, 0.0, dw_type)
 
 
+@pytest.mark.parametrize("M,d,F", [(260, 2048, 2056), (777, 2048, 2816), (2100, 1000, 2696), (4100, 1544, 1032)])
+@pytest.mark.parametrize("dw_type,accumulate", [(BF, False), (F32, True)], ids=["bf16", "f32_added"])
+def test_backward_of_all_products_in_one_launch(M, d, F, dw_type, accumulate):
+    layer = Layer(M, d, F, "silu")
+    layer.forward(True)
+    dy = _bf(layer.gen, M, d)
+    layer.backward(dy, 0.01, dw_type, accumulate=accumulate)
+    layer.check_backward(dy, 0.01, dw_type, accumulate=accumulate)
+
+
 def test_backward_adds_to_gradients():
     layer = Layer(200, 136, 264, "relu")
     layer.forward(True)

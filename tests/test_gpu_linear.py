@@ -195,6 +195,14 @@ def test_backward_of_weights_by_depth(M, N, K, act, dw_type):
     _backward(M, N, K, True, act, dw_type)
 
 
+@pytest.mark.parametrize("M,N,K", [(300, 1024, 1024), (1000, 4096, 1032), (2000, 2304, 2312), (4100, 1000, 3992)])
+@pytest.mark.parametrize("kn", [False, True])
+@pytest.mark.parametrize("dw_type,accumulate", [(BF, False), (F32, True)], ids=["bf16", "f32_added"])
+def test_backward_of_two_products_in_one_launch(M, N, K, kn, dw_type, accumulate):
+    """One or several rounds of tiles in either product, in the last of which some pairs have none."""
+    _backward(M, N, K, kn, "relu", dw_type, accumulate)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_backward_activations(act):
     _backward(257, 264, 200, False, act)
