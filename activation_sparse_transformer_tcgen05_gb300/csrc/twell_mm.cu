@@ -1380,6 +1380,138 @@ __global__ void __launch_bounds__(kFewThreads, 3)
     }
 }
 
+// ------------------------------------------------------------- one to four tokens --
+//
+// Products of W's rows (K-major) with up to four tokens' rows, on the fp32 units: bound by memory like the kernel above, but
+// nothing has to be set up, and nothing joined. A warp (SPLIT of them where there are few rows) has a row of W, GATED the
+// same row of both; x comes from the first-level cache, past which W goes.
+constexpr int kMvThreads = 256, kMvWarps = kMvThreads / 32;
+
+__device__ __forceinline__ uint4 ld_once(const uint16_t* p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+struct MvArgs {
+    const uint16_t *x, *w0, *w1;  // w1: GATED's W_up
+    int64_t ldx, ldw;
+    int K, tokens;
+};
+
+template <int TOK>
+__device__ __forceinline__ void mv_piece(const uint4& w, const MvArgs& m, int piece, float (&sum)[TOK])
+{
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int t = 0; t < TOK; ++t) {
+        if (TOK == 4 && t == 3 && m.tokens < 4) break;
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(m.x + t * m.ldx) + piece);
+        const uint32_t xx[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sum[t] = fmaf(bf16_lo(ww[e]), bf16_lo(xx[e]), sum[t]);
+            sum[t] = fmaf(bf16_hi(ww[e]), bf16_hi(xx[e]), sum[t]);
+        }
+    }
+}
+
+// The tokens' results of output column n, one in each of the first TOK lanes.
+template <int EPI>
+__device__ __forceinline__ void mv_finish(float v, float u, int n, int t, const Args& a)
+{
+    const size_t row = (size_t)t;
+    if (a.bias) v += a.bias[n];
+    float y[2] = {v, 0.f};
+    if constexpr (EPI == GATED) {
+        if (a.g) {
+            a.g[row * a.ldo + n] = f32_to_bf16_bits(v);
+            a.u[row * a.ldo + n] = f32_to_bf16_bits(u);
+        }
+        by_activation(a.act, [&](auto tag) { activate_all<decltype(tag)::value>(y); });
+        a.h[row * a.ldo + n] = f32_to_bf16_bits(y[0] * u);
+    } else {
+        if (a.pre) a.pre[row * a.ldpre + n] = f32_to_bf16_bits(v);
+        if (a.act != TWELL_ACT_NONE) by_activation(a.act, [&](auto tag) { activate_all<decltype(tag)::value>(y); });
+        if (a.res)
+            y[0] += a.out_f32 ? static_cast<const float*>(a.res)[row * a.ldres + n]
+                              : bf16_to_f32(static_cast<const uint16_t*>(a.res)[row * a.ldres + n]);
+        if (a.out_f32)
+            static_cast<float*>(a.out[0])[row * a.ldo + n] = y[0];
+        else
+            static_cast<uint16_t*>(a.out[0])[row * a.ldo + n] = f32_to_bf16_bits(y[0]);
+    }
+}
+
+template <int EPI, int TOK, int SPLIT>
+__global__ void __launch_bounds__(kMvThreads) k_mv(const MvArgs m, const Args a)
+{
+    constexpr int W = EPI == GATED ? 2 : 1;
+    constexpr int AT_ONCE = 8 / W;  // pieces of a row under way in a lane
+    __shared__ float shared[W * TOK][kMvWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n = (int)blockIdx.x * (kMvWarps / SPLIT) + warp / SPLIT;
+    if (EPI == GATED) launch_next();
+    float sum[W][TOK];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) sum[i][t] = 0.f;
+    if (n < a.rowsB) {
+        const int pieces = m.K / 8;
+        const uint16_t* w0 = m.w0 + (size_t)n * m.ldw;
+        const uint16_t* w1 = EPI == GATED ? m.w1 + (size_t)n * m.ldw : nullptr;
+        for (int p = warp % SPLIT * 32 + lane; p < pieces; p += AT_ONCE * 32 * SPLIT) {
+            uint4 q[W][AT_ONCE];
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const int at = p + j * 32 * SPLIT;
+                if (at < pieces) {
+                    q[0][j] = ld_once(w0 + (size_t)at * 8);
+                    if constexpr (EPI == GATED) q[1][j] = ld_once(w1 + (size_t)at * 8);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < AT_ONCE; ++j) {
+                const int at = p + j * 32 * SPLIT;
+                if (at < pieces) {
+#pragma unroll
+                    for (int i = 0; i < W; ++i) mv_piece<TOK>(q[i][j], m, at, sum[i]);
+                }
+            }
+        }
+    }
+    float v = 0.f, u = 0.f;  // lane t: token t's
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int t = 0; t < TOK; ++t) {
+            float s = sum[i][t];
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+            if (SPLIT > 1) {
+                if (lane == 0) shared[i * TOK + t][warp] = s;
+            } else if (lane == t) {
+                (i ? u : v) = s;
+            }
+        }
+    if constexpr (SPLIT > 1) {
+        __syncthreads();
+        if (warp % SPLIT != 0) return;
+        if (lane < TOK) {
+#pragma unroll
+            for (int k = 0; k < SPLIT; ++k) {
+                v += shared[lane][warp + k];
+                if (EPI == GATED) u += shared[(W - 1) * TOK + lane][warp + k];
+            }
+        }
+    }
+    if (lane < TOK && lane < a.rowsA && n < a.rowsB && !has_error(a.status)) mv_finish<EPI>(v, u, n, lane, a);
+}
+
 __global__ void __launch_bounds__(512) k_block_sums(const float* __restrict__ part, int blocks, int n,
                                                     float* __restrict__ db, const int32_t* __restrict__ status)
 {
@@ -1537,6 +1669,43 @@ float pair_us(int64_t rows, int64_t cols, int problems, int depth, bool rows128,
     return 6.6f + (parts == 4 ? 5.f : parts == 2 ? 2.5f : 0.f) + waves * tile_us(a, rows128);
 }
 
+// Whether k_mv takes `tokens` rows and `weights` weights: one token always (4096 x 4096 8.7 us, k_mm_few 11.4; 256 x 8192 3.2,
+// 12.1; 50001 x 2048 32.8, 34.5). x's rows are read from the cache as often as W's, so more of them count: two tokens as long
+// as that is hidden (4096 x 4096 10.3, 11.5; 16384 x 4096 26.6, 26.5; 50001 x 2048 36.1, 34.8), three or four where W is small
+// (256 x 8192 4.0, 12.1; 1024 x 1024 4.2, 6.7; 4096 x 4096 17.9, 11.5).
+bool mv_takes(int tokens, int64_t weights)
+{
+    return tokens == 1 || (tokens == 2 && weights <= 1 << 26) || (tokens <= 4 && weights <= 1 << 22);
+}
+
+template <int EPI, int TOK>
+cudaError_t run_mv_tokens(const MvArgs& m, const Args& a, int sms, cudaStream_t s)
+{
+    // as many warps on a row as give every SM about 24
+    int split = 1;
+    while (split < 8 && (int64_t)a.rowsB * split < (int64_t)sms * 24 && m.K >= 512 * split) split *= 2;
+    const int rows = kMvWarps / split;
+    const unsigned blocks = (unsigned)(((int64_t)a.rowsB + rows - 1) / rows);
+    count_launches(1);
+    switch (split) {
+        case 1: k_mv<EPI, TOK, 1><<<blocks, kMvThreads, 0, s>>>(m, a); break;
+        case 2: k_mv<EPI, TOK, 2><<<blocks, kMvThreads, 0, s>>>(m, a); break;
+        case 4: k_mv<EPI, TOK, 4><<<blocks, kMvThreads, 0, s>>>(m, a); break;
+        default: k_mv<EPI, TOK, 8><<<blocks, kMvThreads, 0, s>>>(m, a); break;
+    }
+    return cudaGetLastError();
+}
+
+template <int EPI>
+cudaError_t run_mv(const MvArgs& m, const Args& a, int sms, cudaStream_t s)
+{
+    switch (a.rowsA) {
+        case 1: return run_mv_tokens<EPI, 1>(m, a, sms, s);
+        case 2: return run_mv_tokens<EPI, 2>(m, a, sms, s);
+        default: return run_mv_tokens<EPI, 4>(m, a, sms, s);
+    }
+}
+
 // Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
 int piece_of(int depth)
 {
@@ -1669,8 +1838,10 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     Maps maps;
     Args a;
     if (!fill(m, few ? choice.plan.tokens : HALF, &maps, &a)) return cudaErrorInvalidValue;
-    a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch was k_mm_few too)
+    a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch lets this one start)
     const bool amn = m.a[0].mn, bmn = m.b[0].mn;
+    if (few && !bmn && m.segments == 1 && mv_takes(m.M, (int64_t)m.N * m.K))
+        return run_mv<LINEAR>(MvArgs{m.a[0].p, m.b[0].p, nullptr, m.a[0].ld, m.b[0].ld, m.K, m.M}, a, sms, s);
     if (few)
         return bmn ? run_few_rows<LINEAR, true>(maps, a, choice.plan, sms, s)
                    : run_few_rows<LINEAR, false>(maps, a, choice.plan, sms, s);
@@ -1719,6 +1890,7 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
     a.h = m.h;
     a.ldo = m.F;
     a.status = m.status;
+    if (mv_takes(m.M, 2ll * m.F * m.K)) return run_mv<GATED>(MvArgs{m.x, m.Wg, m.Wu, m.K, m.K, m.K, m.M}, a, sms, s);
     if (few) return run_few_rows<GATED, false>(maps, a, plan, sms, s);
     return run_pair<GATED, false, false>(maps, a, s);
 }

@@ -110,6 +110,15 @@ def test_forward(M, d, F, save):
     layer.check_forward(res)
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("d,F", [(8, 8), (264, 40), (520, 5000), (2056, 8200)])
+def test_single_tokens(M, d, F):
+    layer = Layer(M, d, F, "silu", M % 2 == 0)
+    res = _bf(layer.gen, M, d)
+    layer.forward(M != 3, res)
+    layer.check_forward(res)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M", [5, 150])
 @pytest.mark.parametrize("bias", [False, True])

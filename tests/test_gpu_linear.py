@@ -110,6 +110,14 @@ def test_fp32_results_of_any_depth(M, N, K, kn):
     assert float((y.double() - want).norm() / want.norm()) <= (2 / 3 * 48 + K / 768) * 2.0 ** -23
 
 
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("N,K", [(1, 8), (3, 264), (1000, 520), (130, 8200), (5001, 1288), (8192, 8192)])
+@pytest.mark.parametrize("y_type", [BF, F32], ids=["bf16", "f32"])
+def test_single_tokens(M, N, K, y_type):
+    _forward(M, N, K, False, "gelu", y_type, True, True, True)
+    _forward(M, N, K, False, "none", y_type, False, False, False, pad=3, offset=1)
+
+
 def test_residual_in_place():
     g = torch.Generator(device="cuda").manual_seed(3)
     for M in (1, 40, 300):
