@@ -5,7 +5,22 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace twell {
+
+// Whether an output is an input or another output (null ones are neither).
+inline bool shared(std::initializer_list<const void*> out, std::initializer_list<const void*> in)
+{
+    for (const void* const* o = out.begin(); o != out.end(); ++o) {
+        if (!*o) continue;
+        for (const void* i : in)
+            if (i == *o) return true;
+        for (const void* const* p = o + 1; p != out.end(); ++p)
+            if (*p == *o) return true;
+    }
+    return false;
+}
 
 // A bf16 operand: `rows` x K, either K-major ([rows, K], ld >= K) or with mn set as its
 // transpose ([K, rows], ld >= rows). ld a multiple of 8, p 16-byte aligned.

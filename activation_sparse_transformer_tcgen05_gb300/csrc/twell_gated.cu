@@ -50,9 +50,8 @@ extern "C" twell_status twell_dense_gated_ffn_fwd(const uint16_t* x, const uint1
                           (const void*)g, (const void*)u, (const void*)h, (const void*)y})
         if (!aligned16(p)) return TWELL_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(status)) & 3u) return TWELL_ERR_INVALID_ARG;
-    if (h == x || y == x || h == y || y == h || (g && (g == u || g == h || u == h || g == x || u == x || y == g || y == u)) ||
-        (res && res == h))
-        return TWELL_ERR_INVALID_ARG;
+    // (g, u and h are written before res is read)
+    if (shared({g, u, h, y}, {x, W_gate, W_up, b, W_down}) || shared({g, u, h}, {res})) return TWELL_ERR_INVALID_ARG;
     const int sms = sms_current();
     if (sms <= 0) return TWELL_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -121,12 +120,7 @@ extern "C" twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint1
         return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
     }
     if (!W_down || !g || !u || !dy || (dx && (!W_gate || !W_up)) || (grads && (!x || !h))) return TWELL_ERR_INVALID_ARG;
-    for (const void* in : {(const void*)x, (const void*)W_gate, (const void*)W_up, (const void*)W_down, (const void*)g,
-                           (const void*)u, (const void*)h, (const void*)dy}) {
-        if (in && (in == dx || in == dW_gate || in == dW_up || in == dW_down)) return TWELL_ERR_INVALID_ARG;
-    }
-    if (grads && (dW_gate == dW_up || dW_gate == dW_down || dW_up == dW_down || dx == dW_gate || dx == dW_up || dx == dW_down))
-        return TWELL_ERR_INVALID_ARG;
+    if (shared({dx, dW_gate, dW_up, dW_down, db, ws}, {x, W_gate, W_up, W_down, g, u, h, dy})) return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_dense_gated_bwd_workspace_bytes(M, d, F)) return TWELL_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return TWELL_ERR_INVALID_ARG;
     const int sms = sms_current();

@@ -138,7 +138,9 @@ extern "C" twell_status twell_linear_fwd(const uint16_t* x, int64_t ldx, const u
         !aligned(bias, 4) || !aligned(status, 4))
         return TWELL_ERR_INVALID_ARG;
     if ((res && (ldres < N || !aligned(res, es))) || (pre && (ldpre < N || !aligned(pre, 2)))) return TWELL_ERR_INVALID_ARG;
-    if (y == x || y == W || pre == x || pre == W || (pre && (y == pre || res == pre))) return TWELL_ERR_INVALID_ARG;
+    if (shared({y, pre}, {x, W, bias}) || (pre && res == pre)) return TWELL_ERR_INVALID_ARG;
+    // (in place: rows of y that lie elsewhere than those of res would replace some that are not read yet)
+    if (y == res && ldy != ldres && M > 1) return TWELL_ERR_INVALID_ARG;
     const int sms = sms_current();
     if (sms <= 0) return TWELL_ERR_CUDA;
     MmLinear m{};
@@ -188,8 +190,7 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
         (dx && (lddx < K || !aligned(dx, 2))))
         return TWELL_ERR_INVALID_ARG;
     if (act != TWELL_ACT_NONE && (!pre || ldpre < N || !aligned(pre, 2))) return TWELL_ERR_INVALID_ARG;
-    if ((dx && (dx == dy || dx == x || dx == W || dx == pre)) || (dW && (dW == dy || dW == x || dW == W || dW == pre || dW == dx)))
-        return TWELL_ERR_INVALID_ARG;
+    if (shared({dx, dW, dbias, ws}, {dy, x, W, pre})) return TWELL_ERR_INVALID_ARG;
     if (!ws || ws_bytes < twell_linear_bwd_workspace_bytes(M, N, K)) return TWELL_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return TWELL_ERR_INVALID_ARG;
     const int sms = sms_current();

@@ -476,8 +476,9 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * Row strides (ld*) in elements. x: a multiple of 8, <= 2^30, 16-byte aligned; y, res, pre,
  * dy, dx: any that is at least the width, of any alignment (16-byte boundaries are
  * fastest). M >= 0, N >= 1, K % 8 == 0; with w_kn N % 8 == 0. Limit of this build:
- * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res; other outputs must not
- * overlap inputs (the call rejects equal pointers).
+ * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res, with the same row stride;
+ * otherwise outputs and ws must not overlap inputs or one another (the calls reject
+ * equal pointers, and y = res with another stride).
  * Sums are fp32 (fp32 results are added up in rounded pieces of at most 768 of depth),
  * outputs are rounded once.
  *
@@ -514,6 +515,8 @@ twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
  * [M, F] bf16; res may be NULL, or y itself. The forward writes h, and g and u unless
  * both are NULL (only a backward reads them); h is formed from the unrounded g and u,
  * y from h as stored. Everything is densely packed; d, F multiples of 8, M >= 0.
+ * Apart from res, outputs and ws must not overlap inputs or one another (the calls
+ * reject equal pointers).
  * Limit of this build: M, d, F <= 2^30 (TWELL_ERR_UNSUPPORTED).
  * Backward: dg and du enter the products rounded to bf16, db sums dg in fp32. dW_*
  * bf16 or fp32 (dw_type), with accumulate != 0 (fp32 only) added to what is there; the
