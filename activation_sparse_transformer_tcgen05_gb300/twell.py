@@ -493,6 +493,13 @@ def _vec(t: torch.Tensor | None, name: str, n: int, dtype: int):
     return t.data_ptr()
 
 
+def _shapes(**tensors):
+    """(tensor or None, rows, columns) of each name."""
+    for name, (t, rows, cols) in tensors.items():
+        if t is not None and t.shape != (rows, cols):
+            raise ValueError(f"{name} must be a [{rows}, {cols}] matrix, got {list(t.shape)}")
+
+
 def twell_layernorm_fwd(x, res, w, b, eps: float, sum_out, y, mean, rstd, stream=None):
     """y = LN(x + res) w + b; sum_out = x + res (res and sum_out: both or neither). w, b, mean, rstd may be None."""
     if x.dim() != 2 or y.dim() != 2:
@@ -653,11 +660,19 @@ def twell_linear_bwd(dy, x, W, w_kn: bool, act: int, pre, dx, dW, accumulate: bo
         _ptr(status, "status", bytes_per_elem=4), _stream(stream)), "twell_linear_bwd")
 
 
+def _gated_sizes(x, W_gate, W_up, W_down):
+    if x.dim() != 2:
+        raise ValueError(f"x must be a matrix, got {list(x.shape)}")
+    (M, d), F = x.shape, W_up.shape[0]
+    _shapes(W_up=(W_up, F, d), W_gate=(W_gate, F, d), W_down=(W_down, F, d))
+    return M, d, F
+
+
 def twell_dense_gated_ffn_fwd(x, W_gate, W_up, b, W_down, act: int, res, g, u, h, y, status, stream=None):
-    """The gated layer densely: h = act(x W_gate^T + b) * (x W_up^T), y = h W_down + res. g and u: the two projections, kept for
-    the backward (or both None); b and res may be None, res may be y."""
-    M, d = x.shape
-    F = W_up.shape[0]
+    """The gated layer densely: h = act(x W_gate^T + b) * (x W_up^T), y = h W_down + res. The three W are [F, d], W_down too.
+    g and u: the two projections, kept for the backward (or both None); b and res may be None, res may be y."""
+    M, d, F = _gated_sizes(x, W_gate, W_up, W_down)
+    _shapes(res=(res, M, d), g=(g, M, F), u=(u, M, F), h=(h, M, F), y=(y, M, d))
     _check(load_library().twell_dense_gated_ffn_fwd(
         _vec(x, "x", M * d, DTYPE_BF16), _vec(W_gate, "W_gate", F * d, DTYPE_BF16), _vec(W_up, "W_up", F * d, DTYPE_BF16),
         _vec(b, "b", F, DTYPE_F32), _vec(W_down, "W_down", F * d, DTYPE_BF16), act, _vec(res, "res", M * d, DTYPE_BF16), M, d, F,
@@ -674,8 +689,9 @@ def twell_dense_gated_ffn_bwd(x, W_gate, W_up, W_down, act: int, g, u, h, dy, l1
                               accumulate: bool, db, ws, status, stream=None):
     """Backward of twell_dense_gated_ffn_fwd with l1 sum |h| added to the loss. dx and db may be None, and the three dW (bf16 or
     fp32; accumulate adds to fp32 ones) together."""
-    M, d = x.shape
-    F = W_up.shape[0]
+    M, d, F = _gated_sizes(x, W_gate, W_up, W_down)
+    _shapes(g=(g, M, F), u=(u, M, F), h=(h, M, F), dy=(dy, M, d), dx=(dx, M, d), dW_gate=(dW_gate, F, d), dW_up=(dW_up, F, d),
+            dW_down=(dW_down, F, d))
     tw = _dtype(dW_gate, "dW_gate") if dW_gate is not None else DTYPE_BF16
     _check(load_library().twell_dense_gated_ffn_bwd(
         _vec(x, "x", M * d, DTYPE_BF16), _vec(W_gate, "W_gate", F * d, DTYPE_BF16), _vec(W_up, "W_up", F * d, DTYPE_BF16),
