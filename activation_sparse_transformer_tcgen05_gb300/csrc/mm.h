@@ -55,8 +55,9 @@ struct MmLinear {
 cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s);
 
 // Two of them that do not need one another, in one launch or in two, whichever should be faster: A K-major in the first,
-// A and B as transposes in the second.
-cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, int sms, cudaStream_t s);
+// A and B as transposes in the second. Or one of them alone (with_one, with_two): its sums are taken in the order that they
+// have beside the other, so that its bits do not depend on it; of the other only sizes and strides are looked at.
+cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, bool with_one, bool with_two, int sms, cudaStream_t s);
 
 // g = x Wg^T + bias, u = x Wu^T, h = act(g) u, all [M, F] bf16; g and u may be null (not kept).
 struct MmGated {

@@ -147,40 +147,33 @@ extern "C" twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint1
     e = launch_mm_gated_bwd(hid, sms, s);
     if (e == cudaSuccess && db) e = launch_block_sums(part, (M + kSumRows - 1) / kSumRows, F, db, status, s);
     MmLinear in{}, w{};
-    if (dx) {
-        MmLinear& m = in;
-        m.M = M;
-        m.N = d;
-        m.K = F;
-        m.segments = 2;
-        m.problems = 1;
-        m.a[0] = {dg, F, false};
-        m.a[1] = {du, F, false};
-        m.b[0] = {W_gate, d, true};
-        m.b[1] = {W_up, d, true};
-        m.out[0] = dx;
-        m.ldo = d;
-        m.status = status;
-    }
-    if (grads) {
-        MmLinear& m = w;
-        m.M = F;
-        m.N = d;
-        m.K = M;
-        m.segments = 1;
-        m.problems = 3;
-        m.a[0] = {dg, F, true};
-        m.a[1] = {du, F, true};
-        m.a[2] = {h, F, true};
-        m.b[0] = m.b[1] = {x, d, true};
-        m.b[2] = {dy, d, true};
-        for (int i = 0; i < 3; ++i) m.out[i] = dW[i];
-        m.ldo = d;
-        m.out_f32 = dw_type == TWELL_F32;
-        m.accumulate = accumulate != 0;
-        m.status = status;
-    }
-    if (e == cudaSuccess && (dx || grads))
-        e = dx && grads ? launch_mm_two(in, w, sms, s) : launch_mm_linear(dx ? in : w, sms, s);
+    in.M = M;
+    in.N = d;
+    in.K = F;
+    in.segments = 2;
+    in.problems = 1;
+    in.a[0] = {dg, F, false};
+    in.a[1] = {du, F, false};
+    in.b[0] = {W_gate, d, true};
+    in.b[1] = {W_up, d, true};
+    in.out[0] = dx;
+    in.ldo = d;
+    in.status = status;
+    w.M = F;
+    w.N = d;
+    w.K = M;
+    w.segments = 1;
+    w.problems = 3;
+    w.a[0] = {dg, F, true};
+    w.a[1] = {du, F, true};
+    w.a[2] = {h, F, true};
+    w.b[0] = w.b[1] = {x, d, true};
+    w.b[2] = {dy, d, true};
+    for (int i = 0; i < 3; ++i) w.out[i] = dW[i];
+    w.ldo = d;
+    w.out_f32 = dw_type == TWELL_F32;
+    w.accumulate = accumulate != 0;
+    w.status = status;
+    if (e == cudaSuccess) e = launch_mm_two(in, w, dx != nullptr, grads != 0, sms, s);
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }

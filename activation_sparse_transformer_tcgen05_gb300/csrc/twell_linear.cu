@@ -223,33 +223,27 @@ extern "C" twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const
         if (e == cudaSuccess && dbias) e = launch_block_sums(part, blocks, N, dbias, status, s);
     }
     MmLinear in{}, w{};
-    if (dx) {
-        MmLinear& m = in;
-        m.M = M;
-        m.N = K;
-        m.K = N;
-        m.segments = m.problems = 1;
-        m.a[0] = dpre;
-        m.b[0] = {W, w_kn ? N : K, w_kn == 0};  // [K, N]: K-major for this product
-        m.out[0] = dx;
-        m.ldo = lddx;
-        m.status = status;
-    }
-    if (dW) {
-        MmLinear& m = w;
-        m.M = w_kn ? K : N;
-        m.N = w_kn ? N : K;
-        m.K = M;
-        m.segments = m.problems = 1;
-        const MmOperand rows{dpre.p, dpre.ld, true}, cols{x, ldx, true};
-        m.a[0] = w_kn ? cols : rows;
-        m.b[0] = w_kn ? rows : cols;
-        m.out[0] = dW;
-        m.ldo = m.N;
-        m.out_f32 = dw_type == TWELL_F32;
-        m.accumulate = accumulate != 0;
-        m.status = status;
-    }
-    if (e == cudaSuccess && (dx || dW)) e = dx && dW ? launch_mm_two(in, w, sms, s) : launch_mm_linear(dx ? in : w, sms, s);
+    in.M = M;
+    in.N = K;
+    in.K = N;
+    in.segments = in.problems = 1;
+    in.a[0] = dpre;
+    in.b[0] = {W, w_kn ? N : K, w_kn == 0};  // [K, N]: K-major for this product
+    in.out[0] = dx;
+    in.ldo = lddx;
+    in.status = status;
+    const MmOperand rows{dpre.p, dpre.ld, true}, cols{x, ldx, true};
+    w.M = w_kn ? K : N;
+    w.N = w_kn ? N : K;
+    w.K = M;
+    w.segments = w.problems = 1;
+    w.a[0] = w_kn ? cols : rows;
+    w.b[0] = w_kn ? rows : cols;
+    w.out[0] = dW;
+    w.ldo = w.N;
+    w.out_f32 = dw_type == TWELL_F32;
+    w.accumulate = accumulate != 0;
+    w.status = status;
+    if (e == cudaSuccess) e = launch_mm_two(in, w, dx != nullptr, dW != nullptr, sms, s);
     return e == cudaSuccess ? TWELL_OK : TWELL_ERR_CUDA;
 }

@@ -1567,8 +1567,9 @@ struct Split {
     }
 };
 
+// whole: a tile's depth in one part, however few tiles there are.
 template <int EPI, bool A_MN, bool B_MN, int JOBS>
-cudaError_t run_jobs(Jobs<JOBS>& jobs, cudaStream_t s)
+cudaError_t run_jobs(Jobs<JOBS>& jobs, bool whole, cudaStream_t s)
 {
     auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
@@ -1614,7 +1615,7 @@ cudaError_t run_jobs(Jobs<JOBS>& jobs, cudaStream_t s)
     const int depth = jobs.args[0].num_kb * jobs.args[0].segments;
     int parts = 1;
     for (int i = 1; i <= 2; ++i)
-        if (EPI == LINEAR && JOBS == 1 && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
+        if (EPI == LINEAR && JOBS == 1 && !whole && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
     const int per = (depth + parts - 1) / parts;
     const int clusters = (int)(parts > 1 || tiles < known[dev][0] ? tiles : known[dev][0]);
     if constexpr (JOBS > 1) jobs.delay = Split(jobs.args[0], jobs.args[1], jobs.us[0], jobs.us[1], clusters).delay;
@@ -1625,10 +1626,19 @@ cudaError_t run_jobs(Jobs<JOBS>& jobs, cudaStream_t s)
 }
 
 template <int EPI, bool A_MN, bool B_MN>
-cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s)
+cudaError_t run_pair(const Maps& maps, const Args& a, cudaStream_t s, bool whole = false)
 {
     Jobs<1> jobs{{maps}, {a}, 0, {0.f}};
-    return run_jobs<EPI, A_MN, B_MN, 1>(jobs, s);
+    return run_jobs<EPI, A_MN, B_MN, 1>(jobs, whole, s);
+}
+
+cudaError_t run_linear(const MmLinear& m, const Maps& maps, const Args& a, cudaStream_t s, bool whole)
+{
+    const bool amn = m.a[0].mn, bmn = m.b[0].mn;
+    if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s, whole);
+    if (amn) return cudaErrorInvalidValue;
+    if (bmn) return run_pair<LINEAR, false, true>(maps, a, s, whole);
+    return run_pair<LINEAR, false, false>(maps, a, s, whole);
 }
 
 // Few rows: up to this many always, up to kFewTry where an estimate says so.
@@ -1839,31 +1849,48 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
     Args a;
     if (!fill(m, few ? choice.plan.tokens : HALF, &maps, &a)) return cudaErrorInvalidValue;
     a.early = few && m.M <= kFewMost && m.after_gated;  // (then that launch lets this one start)
-    const bool amn = m.a[0].mn, bmn = m.b[0].mn;
+    const bool bmn = m.b[0].mn;
     if (few && !bmn && m.segments == 1 && mv_takes(m.M, (int64_t)m.N * m.K))
         return run_mv<LINEAR>(MvArgs{m.a[0].p, m.b[0].p, nullptr, m.a[0].ld, m.b[0].ld, m.K, m.M}, a, sms, s);
     if (few)
         return bmn ? run_few_rows<LINEAR, true>(maps, a, choice.plan, sms, s)
                    : run_few_rows<LINEAR, false>(maps, a, choice.plan, sms, s);
-    if (amn && bmn) return run_pair<LINEAR, true, true>(maps, a, s);
-    if (amn) return cudaErrorInvalidValue;
-    if (bmn) return run_pair<LINEAR, false, true>(maps, a, s);
-    return run_pair<LINEAR, false, false>(maps, a, s);
+    return run_linear(m, maps, a, s, false);
 }
 
-cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, int sms, cudaStream_t s)
+cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, bool with_one, bool with_two, int sms, cudaStream_t s)
 {
     if (one.a[0].mn || !two.a[0].mn || !two.b[0].mn || one.status != two.status) return cudaErrorInvalidValue;
-    Jobs<2> jobs;
-    if (!fill(one, HALF, &jobs.maps[0], &jobs.args[0]) || !fill(two, HALF, &jobs.maps[1], &jobs.args[1])) return cudaErrorInvalidValue;
-    for (int i = 0; i < 2; ++i) jobs.us[i] = tile_us(jobs.args[i], rows128(i ? two : one));
-    const Split split(jobs.args[0], jobs.args[1], jobs.us[0], jobs.us[1], sms / 2);
+    Args args[2];
+    for (int i = 0; i < 2; ++i) {
+        const MmLinear& m = i ? two : one;
+        args[i].rowsA = m.M, args[i].rowsB = m.N, args[i].problems = m.problems, args[i].segments = m.segments;
+        args[i].num_kb = (m.K + BK - 1) / BK;
+    }
+    const float us[2] = {tile_us(args[0], rows128(one)), tile_us(args[1], rows128(two))};
+    const Split split(args[0], args[1], us[0], us[1], sms / 2);
     // (tiles that run far apart in depth read more from memory, so that a gain of 2 to 4 % by this estimate was a loss of 1
     // to 3, 8192 x 4096 x 14336 and -> 16384; one of 8 % was a gain of 1.5, 2048 x 4096 x 14336)
-    if (6.6f + split.most < 0.95f * (Choice(one, sms).us + Choice(two, sms).us))
-        return one.b[0].mn ? run_jobs<LINEAR, false, true, 2>(jobs, s) : run_jobs<LINEAR, false, false, 2>(jobs, s);
-    const cudaError_t e = launch_mm_linear(one, sms, s);
-    return e == cudaSuccess ? launch_mm_linear(two, sms, s) : e;
+    const bool together = 6.6f + split.most < 0.95f * (Choice(one, sms).us + Choice(two, sms).us);
+    if (together && with_one && with_two) {
+        Jobs<2> jobs;
+        if (!fill(one, HALF, &jobs.maps[0], &jobs.args[0]) || !fill(two, HALF, &jobs.maps[1], &jobs.args[1])) return cudaErrorInvalidValue;
+        for (int i = 0; i < 2; ++i) jobs.us[i] = us[i];
+        return one.b[0].mn ? run_jobs<LINEAR, false, true, 2>(jobs, true, s) : run_jobs<LINEAR, false, false, 2>(jobs, true, s);
+    }
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+        if (!(i ? with_two : with_one)) continue;
+        const MmLinear& m = i ? two : one;
+        if (!together) {
+            e = launch_mm_linear(m, sms, s);
+            continue;
+        }
+        Maps maps;
+        Args a;
+        e = fill(m, HALF, &maps, &a) ? run_linear(m, maps, a, s, true) : cudaErrorInvalidValue;
+    }
+    return e;
 }
 
 cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)

@@ -485,7 +485,8 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * twell_linear_bwd: dy [M, N] bf16; pre as the forward kept it (NULL if act is
  * TWELL_ACT_NONE). dx [M, K] bf16; dW in W's layout, bf16 or fp32 (dw_type), with
  * accumulate != 0 (fp32 only) added to what is there; dbias [N] fp32. Each of the
- * three may be NULL, not all. With an activation dpre enters the products rounded
+ * three may be NULL, not all; a gradient's bits do not depend on which others are
+ * asked for. With an activation dpre enters the products rounded
  * to bf16, like any operand of the tensor cores; dbias sums it in fp32.
  *   ws: at least twell_linear_bwd_workspace_bytes(M, N, K) bytes, 256-byte aligned.
  * M = 0: dW and dbias are 0 (dW unchanged with accumulate).
