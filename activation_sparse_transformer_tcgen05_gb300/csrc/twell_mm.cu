@@ -1935,7 +1935,7 @@ cudaError_t launch_mm_gated_bwd(const MmGatedBwd& m, int sms, cudaStream_t s)
     a.rowsB = m.F;
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = a.problems = 1;
-    a.piece = m.part ? piece_of(a.num_kb) : a.num_kb;
+    a.piece = piece_of(a.num_kb);  // without db too: dx and the weight gradients have the same bits
     a.act = m.act;
     a.l1 = m.l1;
     a.g_in = m.g;

@@ -521,7 +521,8 @@ twell_status twell_linear_bwd(const uint16_t* dy, int64_t lddy, const uint16_t* 
  * Limit of this build: M, d, F <= 2^30 (TWELL_ERR_UNSUPPORTED).
  * Backward: dg and du enter the products rounded to bf16, db sums dg in fp32. dW_*
  * bf16 or fp32 (dw_type), with accumulate != 0 (fp32 only) added to what is there; the
- * three may all be NULL, and so may dx and db, but not everything.
+ * three may all be NULL, and so may dx and db, but not everything; a gradient's bits
+ * do not depend on which others are asked for.
  *   ws: at least twell_dense_gated_bwd_workspace_bytes(M, d, F) bytes, 256-byte aligned.
  * M = 0: dW_* and db are 0 (dW_* unchanged with accumulate). Large batches run on CTA
  * pairs (TWELL_ERR_CUDA if a cluster of two cannot be launched).
