@@ -59,9 +59,9 @@ struct Smem {
 // The tensor cores' fp32 sums drop what does not fit, towards zero, at each step of 16 of depth: over 512 by 2 to 3
 // units of 2^-23 of the result, over 1024 by 7, over 4096 by 31 to 70, over 16384 four times that. Results that leave in
 // fp32 are therefore summed 768 at a time and the pieces added up with rounding (within 1e-6 of 64 bits, as plain fp32
-// sums are; with 1024 just not); for bf16 the loss is a hundredth of the result's own rounding and the tensor cores sum
-// the whole depth.
-constexpr int kPieceBlocks = 12;
+// sums are; with 1024 just not); results that leave in bf16, 16384 at a time: the loss is then 280 units of 2^-23 at most, a
+// hundredth of their own rounding, whatever the depth (of a weight gradient the number of rows).
+constexpr int kPieceBlocks = 12, kPieceBlocksBf16 = 256;
 
 struct Maps {
     CUtensorMap a[kMmParts], b[kMmParts];
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
         bool ok = true;
         auto finish = [&](const Args& a) {
             const int depth = to(a) - from(a);
-            const bool pieces = EPI != GATED && depth > a.piece;
+            const bool pieces = depth > a.piece;
             int mb, nb, problem;
             locate(a, at.tile, &problem, &mb, &nb);
             const int row0 = mb * PAIR_M + (int)rank * HALF + 32 * q;
@@ -806,31 +806,38 @@ __global__ void __launch_bounds__(Smem<EPI>::THREADS, 1) k_mm_pair(const __grid_
             ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
             if (!ok) return;
             tc_fence_after();
-            if constexpr (EPI != GATED) {
-                if (pieces) {
-                    float sum[L::COLS];
+            if (pieces) {
+                constexpr int W = EPI == GATED ? 2 : 1;  // (g and u)
+                float sum[W][L::COLS];
 #pragma unroll
-                    for (int k = 0; k < L::COLS; ++k) sum[k] = 0.f;
-                    int done = 0;
-                    while (true) {
-                        const uint32_t sums = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
-                        done += a.piece;
-                        if (live) add_columns(sums, sum);
-                        if (done >= depth) {
-                            if (live) set_columns(sums, sum);
-                            break;
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
-                        acc ^= 1;
-                        if (acc == 0) acc_phase ^= 1u;
-                        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
-                        if (!ok) break;
-                        tc_fence_after();
+                for (int w = 0; w < W; ++w)
+#pragma unroll
+                    for (int k = 0; k < L::COLS; ++k) sum[w][k] = 0.f;
+                int done = 0;
+                while (true) {
+                    const uint32_t sums = lanes_at + (uint32_t)(acc * PAIR_N + L::COLS * slice);
+                    done += a.piece;
+                    if (live) {
+#pragma unroll
+                        for (int w = 0; w < W; ++w) add_columns(sums + (uint32_t)(w * HALF), sum[w]);
                     }
-                    if (!ok) return;
+                    if (done >= depth) {
+                        if (live) {
+#pragma unroll
+                            for (int w = 0; w < W; ++w) set_columns(sums + (uint32_t)(w * HALF), sum[w]);
+                        }
+                        break;
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + 8u * (uint32_t)acc);
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
+                    ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
+                if (!ok) return;
             }
             if (EPI == LINEAR && parts > 1) {
                 // (the pair's products are done: its ring is free)
@@ -1716,10 +1723,11 @@ cudaError_t run_mv(const MvArgs& m, const Args& a, int sms, cudaStream_t s)
     }
 }
 
-// Length of the pieces of `depth` k-blocks: as few as kPieceBlocks allows, as even as they can be.
-int piece_of(int depth)
+// Length of the pieces of `depth` k-blocks: as few as the results' type allows, as even as they can be.
+int piece_of(int depth, bool f32)
 {
-    const int pieces = (depth + kPieceBlocks - 1) / kPieceBlocks;
+    const int most = f32 ? kPieceBlocks : kPieceBlocksBf16;
+    const int pieces = (depth + most - 1) / most;
     return (depth + pieces - 1) / pieces;
 }
 
@@ -1735,8 +1743,7 @@ cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cuda
     const int blocks = plan.blocks, parts = plan.parts, per = plan.per;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
     // fp32 results in pieces of 512 of depth; of 128 tokens, where a piece waits for the one before, longer ones
-    a.piece = per;
-    if (a.out_f32) a.piece = L::DRAINED ? 8 : piece_of(per);
+    a.piece = a.out_f32 && L::DRAINED ? 8 : piece_of(per, a.out_f32);
     const int held = per > a.piece ? 2 : 1;  // accumulators
     uint32_t cols = 32;
     while (cols < (uint32_t)(held * BN)) cols *= 2;
@@ -1796,7 +1803,7 @@ bool fill(const MmLinear& m, int box, Maps* maps, Args* args)
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = m.segments;
     a.problems = m.problems;
-    a.piece = m.out_f32 ? piece_of(a.num_kb * m.segments) : a.num_kb * m.segments;
+    a.piece = piece_of(a.num_kb * m.segments, m.out_f32);
     a.bias = m.bias;
     a.act = m.act;
     a.res = m.res;
@@ -1909,7 +1916,7 @@ cudaError_t launch_mm_gated(const MmGated& m, int sms, cudaStream_t s)
     a.rowsB = m.F;
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = a.problems = 1;
-    a.piece = a.num_kb;
+    a.piece = piece_of(a.num_kb, false);
     a.bias = m.bias;
     a.act = m.act;
     a.g = m.g;
@@ -1935,7 +1942,7 @@ cudaError_t launch_mm_gated_bwd(const MmGatedBwd& m, int sms, cudaStream_t s)
     a.rowsB = m.F;
     a.num_kb = (m.K + BK - 1) / BK;
     a.segments = a.problems = 1;
-    a.piece = piece_of(a.num_kb);  // without db too: dx and the weight gradients have the same bits
+    a.piece = piece_of(a.num_kb, true);  // without db too: dx and the weight gradients have the same bits
     a.act = m.act;
     a.l1 = m.l1;
     a.g_in = m.g;

@@ -479,7 +479,8 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * M, N, K <= 2^30 (TWELL_ERR_UNSUPPORTED). y may be res, with the same row stride;
  * otherwise outputs and ws must not overlap inputs or one another (the calls reject
  * equal pointers, and y = res with another stride).
- * Sums are fp32 (fp32 results are added up in rounded pieces of at most 768 of depth),
+ * Sums are fp32, the tensor cores', which drop what does not fit towards zero, over at
+ * most 768 of depth for fp32 results and 16384 for bf16 ones, joined with rounding;
  * outputs are rounded once.
  *
  * twell_linear_bwd: dy [M, N] bf16; pre as the forward kept it (NULL if act is
