@@ -5,11 +5,15 @@
 //   gelu       z P(z), P the normal distribution function; derivative P(z) + z e^(-z^2 / 2) / sqrt(2 pi)
 //   gelu_tanh  z (1 + tanh i) / 2 = z s(2 i), i = sqrt(2 / pi) (z + 0.044715 z^3)
 // All in fp32. The exponential and the quotient are the fast ones: within 4e-7 of
-// the value for |z| < 6, where s matters, a hundredth of a bf16 rounding. P's tail is
-// Hastings' rational approximation (Abramowitz and Stegun, 7.1.26), within 8e-8: a
-// polynomial in 1 / (1 + p |z| / sqrt 2) times the e^(-z^2 / 2) that the derivative
-// needs anyway. (With erff, and eight warps, the epilogue of the backward's first product
-// was longer than the product itself: 777 x 1000 x 2696 37 us, now 24.)
+// the value for |z| < 6, where s matters, a hundredth of a bf16 rounding. P's tail is a
+// polynomial t (c1 + ... + c6 t^5) in t = 1 / (1 + 0.29 |z|) times the e^(-z^2 / 2) that
+// the derivative needs anyway. The coefficients are a fit (iteratively reweighted least
+// squares) to the tail times e^(z^2 / 2) on |z| < 14, under both bounds at once: within
+// 6e-8, and within 1.2e-4 of the tail itself, a thirtieth of a bf16 rounding. (The five
+// terms of Abramowitz and Stegun 7.1.26 are within 8e-8, but 0.4 % off the tail at z = -6
+// and 2 % at -10; five terms under both bounds, 5e-7. With erff, and eight warps, the
+// epilogue of the backward's first product was longer than the product itself: 777 x 1000 x
+// 2696 37 us, now 24.)
 #pragma once
 
 #include "common.cuh"
@@ -42,11 +46,12 @@ __device__ __forceinline__ float2 activate(float2 z, float2* da = nullptr)
         return __fmul2_rn(z, s);
     } else if constexpr (ACT == TWELL_ACT_GELU) {
         const float2 e = exp2_pair(__fmul2_rn(__fmul2_rn(z, z), pair(-0.72134752f)));  // e^(-z^2 / 2)
-        const float2 t = reciprocal_pair(__ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), pair(0.23164189f), pair(1.f)));
-        float2 q = __ffma2_rn(t, pair(0.530702714f), pair(-0.726576013f));  // half of Hastings' coefficients
-        q = __ffma2_rn(t, q, pair(0.710706871f));
-        q = __ffma2_rn(t, q, pair(-0.142248368f));
-        q = __fmul2_rn(__fmul2_rn(__ffma2_rn(t, q, pair(0.127414796f)), t), e);
+        const float2 t = reciprocal_pair(__ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), pair(0.29f), pair(1.f)));
+        float2 q = __ffma2_rn(t, pair(-0.0891031250f), pair(0.285923600f));
+        q = __ffma2_rn(t, q, pair(-0.0946542323f));
+        q = __ffma2_rn(t, q, pair(0.180511311f));
+        q = __ffma2_rn(t, q, pair(0.100418434f));
+        q = __fmul2_rn(__fmul2_rn(__ffma2_rn(t, q, pair(0.116904020f)), t), e);
         const float2 o = __ffma2_rn(q, pair(-1.f), pair(1.f));
         const float2 p = make_float2(z.x < 0.f ? q.x : o.x, z.y < 0.f ? q.y : o.y);
         if (da) *da = __ffma2_rn(__fmul2_rn(z, pair(0.39894228f)), e, p);
