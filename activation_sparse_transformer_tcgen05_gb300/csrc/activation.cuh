@@ -58,7 +58,8 @@ __device__ __forceinline__ float2 activate(float2 z, float2* da = nullptr)
         return __fmul2_rn(z, p);
     } else if constexpr (ACT == TWELL_ACT_GELU_TANH) {
         const float k = 1.59576912f;  // 2 sqrt(2 / pi)
-        const float2 z2 = __fmul2_rn(z, z);
+        // (below the squares that pass fp32's range: times the 0 of s (1 - s) those would be NaN in the derivative)
+        const float2 sq = __fmul2_rn(z, z), z2 = make_float2(fminf(sq.x, 1e30f), fminf(sq.y, 1e30f));
         const float2 i = __fmul2_rn(__ffma2_rn(z2, pair(-1.44269504f * k * 0.044715f), pair(-1.44269504f * k)), z);
         const float2 s = reciprocal_pair(__fadd2_rn(exp2_pair(i), pair(1.f))), zs = __fmul2_rn(z, s);
         if (da)
