@@ -1574,32 +1574,32 @@ struct Split {
     }
 };
 
-// whole: a tile's depth in one part, however few tiles there are.
+// Clusters of 2, 4 and 8 CTAs of a kernel of pairs that can be resident at once on the current device (0: none, or not
+// needed), as the driver says.
+struct AtOnce {
+    int n[3];
+};
 template <int EPI, bool A_MN, bool B_MN, int JOBS>
-cudaError_t run_jobs(Jobs<JOBS>& jobs, bool whole, cudaStream_t s)
+cudaError_t clusters_at_once(AtOnce* out)
 {
-    auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
-    if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(Smem<EPI>::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = Smem<EPI>::TOTAL;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    // clusters of 2, 4 and 8 CTAs that can be resident at once
-    static int known[64][3] = {{0}};
+    static AtOnce known[64] = {{{0}}};
     int dev = 0;
-    e = cudaGetDevice(&dev);
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (known[dev][0] <= 0) {
+    if (known[dev].n[0] <= 0) {
+        auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.blockDim = dim3(Smem<EPI>::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = Smem<EPI>::TOTAL;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
         for (int i = 2; i >= 0; --i) {  // (the first entry last: it says that all are known)
             if (i > 0 && (EPI != LINEAR || JOBS > 1)) continue;
             int n = 0;
@@ -1609,22 +1609,52 @@ cudaError_t run_jobs(Jobs<JOBS>& jobs, bool whole, cudaStream_t s)
             if (e != cudaSuccess && i == 0) return e;
             if (e != cudaSuccess) (void)cudaGetLastError();
             if (n <= 0 && i == 0) return cudaErrorNotSupported;
-            known[dev][i] = e == cudaSuccess ? n : 0;
+            known[dev].n[i] = e == cudaSuccess ? n : 0;
         }
     }
+    *out = known[dev];
+    return cudaSuccess;
+}
+
+// Parts of a tile's depth: where there are few tiles, as many as run at once, if none is shorter than 12 k-blocks (joining
+// takes about 2.5 us for each part more, as long as 9 k-blocks); so no part is empty.
+int parts_of(int64_t tiles, int depth, const AtOnce& at_once)
+{
+    int parts = 1;
+    for (int i = 1; i <= 2; ++i)
+        if (tiles <= at_once.n[i] && depth >= (12 << i)) parts = 1 << i;
+    return parts;
+}
+
+// whole: a tile's depth in one part, however few tiles there are.
+template <int EPI, bool A_MN, bool B_MN, int JOBS>
+cudaError_t run_jobs(Jobs<JOBS>& jobs, bool whole, cudaStream_t s)
+{
+    auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
+    AtOnce at_once;
+    cudaError_t e = clusters_at_once<EPI, A_MN, B_MN, JOBS>(&at_once);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(Smem<EPI>::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = Smem<EPI>::TOTAL;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     constexpr int TILE_N = EPI == GATED ? HALF : PAIR_N;
     int64_t tiles = 0;
     for (const Args& a : jobs.args)
         tiles += ((int64_t)a.rowsA + PAIR_M - 1) / PAIR_M * (((int64_t)a.rowsB + TILE_N - 1) / TILE_N) * a.problems;
     if (tiles > INT32_MAX / 2) return cudaErrorInvalidValue;
-    // Few tiles: the depth in as many parts as run at once, if none is shorter than 12 k-blocks (joining takes about
-    // 2.5 us for each part more, as long as 9 k-blocks); so no part is empty.
     const int depth = jobs.args[0].num_kb * jobs.args[0].segments;
-    int parts = 1;
-    for (int i = 1; i <= 2; ++i)
-        if (EPI == LINEAR && JOBS == 1 && !whole && tiles <= known[dev][i] && depth >= (12 << i)) parts = 1 << i;
+    const int parts = EPI == LINEAR && JOBS == 1 && !whole ? parts_of(tiles, depth, at_once) : 1;
     const int per = (depth + parts - 1) / parts;
-    const int clusters = (int)(parts > 1 || tiles < known[dev][0] ? tiles : known[dev][0]);
+    const int clusters = (int)(parts > 1 || tiles < at_once.n[0] ? tiles : at_once.n[0]);
     if constexpr (JOBS > 1) jobs.delay = Split(jobs.args[0], jobs.args[1], jobs.us[0], jobs.us[1], clusters).delay;
     attr[0].val.clusterDim.x = 2u * (unsigned)parts;
     cfg.gridDim = dim3(2u * (unsigned)parts * (unsigned)clusters, 1, 1);
@@ -1674,11 +1704,11 @@ FewPlan few_plan(int rows, int64_t tiles, int depth, int sms)
     return p;
 }
 
-// The same of the CTA pairs' kernel, whose parts are 2.5 us each (run_jobs).
-float pair_us(int64_t rows, int64_t cols, int problems, int depth, bool rows128, int sms)
+// The same of the CTA pairs' kernel, whose parts are 2.5 us each (parts_of).
+float pair_us(int64_t rows, int64_t cols, int problems, int depth, bool rows128, const AtOnce& at_once)
 {
-    const int64_t tiles = (rows + PAIR_M - 1) / PAIR_M * ((cols + PAIR_N - 1) / PAIR_N) * problems, pairs = sms / 2;
-    const int parts = tiles <= 15 && depth >= 48 ? 4 : tiles <= 36 && depth >= 24 ? 2 : 1;
+    const int64_t tiles = (rows + PAIR_M - 1) / PAIR_M * ((cols + PAIR_N - 1) / PAIR_N) * problems, pairs = at_once.n[0];
+    const int parts = parts_of(tiles, depth, at_once);
     const float waves = parts > 1 ? 1.f : (float)((tiles + pairs - 1) / pairs);
     Args a{};
     a.num_kb = (depth + parts - 1) / parts;
@@ -1836,11 +1866,11 @@ struct Choice {
     FewPlan plan;
     bool few;
     float us;
-    Choice(const MmLinear& m, int sms)
+    Choice(const MmLinear& m, int sms, const AtOnce& at_once)
     {
         const int depth = (m.K + BK - 1) / BK * m.segments;
         plan = few_plan(m.M, ((int64_t)m.N + kFewRows - 1) / kFewRows, depth, sms);
-        us = pair_us(m.M, m.N, m.problems, depth, rows128(m), sms);
+        us = pair_us(m.M, m.N, m.problems, depth, rows128(m), at_once);
         few = m.problems == 1 && !m.accumulate && !m.a[0].mn && (m.M <= kFewMost || (m.M <= kFewTry && plan.us < us));
         if (few) us = plan.us;
     }
@@ -1850,7 +1880,10 @@ struct Choice {
 
 cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
 {
-    const Choice choice(m, sms);
+    AtOnce at_once;
+    const cudaError_t e = clusters_at_once<LINEAR, false, false, 1>(&at_once);
+    if (e != cudaSuccess) return e;
+    const Choice choice(m, sms, at_once);
     const bool few = choice.few;
     Maps maps;
     Args a;
@@ -1868,6 +1901,9 @@ cudaError_t launch_mm_linear(const MmLinear& m, int sms, cudaStream_t s)
 cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, bool with_one, bool with_two, int sms, cudaStream_t s)
 {
     if (one.a[0].mn || !two.a[0].mn || !two.b[0].mn || one.status != two.status) return cudaErrorInvalidValue;
+    AtOnce at_once;
+    cudaError_t e = clusters_at_once<LINEAR, false, false, 1>(&at_once);
+    if (e != cudaSuccess) return e;
     Args args[2];
     for (int i = 0; i < 2; ++i) {
         const MmLinear& m = i ? two : one;
@@ -1875,17 +1911,16 @@ cudaError_t launch_mm_two(const MmLinear& one, const MmLinear& two, bool with_on
         args[i].num_kb = (m.K + BK - 1) / BK;
     }
     const float us[2] = {tile_us(args[0], rows128(one)), tile_us(args[1], rows128(two))};
-    const Split split(args[0], args[1], us[0], us[1], sms / 2);
+    const Split split(args[0], args[1], us[0], us[1], at_once.n[0]);
     // (tiles that run far apart in depth read more from memory, so that a gain of 2 to 4 % by this estimate was a loss of 1
     // to 3, 8192 x 4096 x 14336 and -> 16384; one of 8 % was a gain of 1.5, 2048 x 4096 x 14336)
-    const bool together = 6.6f + split.most < 0.95f * (Choice(one, sms).us + Choice(two, sms).us);
+    const bool together = 6.6f + split.most < 0.95f * (Choice(one, sms, at_once).us + Choice(two, sms, at_once).us);
     if (together && with_one && with_two) {
         Jobs<2> jobs;
         if (!fill(one, HALF, &jobs.maps[0], &jobs.args[0]) || !fill(two, HALF, &jobs.maps[1], &jobs.args[1])) return cudaErrorInvalidValue;
         for (int i = 0; i < 2; ++i) jobs.us[i] = us[i];
         return one.b[0].mn ? run_jobs<LINEAR, false, true, 2>(jobs, true, s) : run_jobs<LINEAR, false, false, 2>(jobs, true, s);
     }
-    cudaError_t e = cudaSuccess;
     for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
         if (!(i ? with_two : with_one)) continue;
         const MmLinear& m = i ? two : one;
