@@ -39,7 +39,7 @@ constexpr int kBox = 4096;  // 32 rows x 128 bytes of one epilogue warp
 
 // GATED_BWD's results take the longest to form (two matrices in, two out, column sums): 16 warps of 64 columns, and a
 // ring one stage shorter for their boxes. With eight of 128 the epilogue took longer than a tile's products (8192 x 4096 x
-// 14336 807 us; with 16, and g and u asked for early, 690 in pieces of 1024 of depth, 730 of 768).
+// 14336 807 us; with 16, and g and u asked for early, 690 in pieces of 1024 of depth, 709 of 768, 748 of 512).
 template <int EPI>
 struct Smem {
     static constexpr int STAGES = EPI == GATED_BWD ? 5 : 6;
@@ -58,10 +58,14 @@ struct Smem {
 
 // The tensor cores' fp32 sums drop what does not fit, towards zero, at each step of 16 of depth: over 512 by 2 to 3
 // units of 2^-23 of the result, over 1024 by 7, over 4096 by 31 to 70, over 16384 four times that. Results that leave in
-// fp32 are therefore summed 768 at a time and the pieces added up with rounding (within 1e-6 of 64 bits, as plain fp32
-// sums are; with 1024 just not); results that leave in bf16, 16384 at a time: the loss is then 280 units of 2^-23 at most, a
-// hundredth of their own rounding, whatever the depth (of a weight gradient the number of rows).
-constexpr int kPieceBlocks = 12, kPieceBlocksBf16 = 256;
+// fp32, and the dh that db is summed from, are therefore summed 512 at a time and the pieces added up with rounding: 4.8e-7
+// off 64 bits in norm at any depth, where fp32 matrix products by torch are 2.5e-7 (depth 1000), 6.1e-7 (4096) and 9.6e-7
+// (8192) off. Both sides of the length: 768, 7.2e-7; 256, 2.5e-7. Linear backward 8192 x 4096 -> 16384 with fp32 dW 1266 us at 768, 1289
+// at 512, 1341 at 256; gated backward 8192 x 4096 x 14336 with bf16 dW 3144, 3189 and 3273. Up to 128 rows (k_mm_few), whose
+// time goes into W, 256 at a time costs 0 to 1 us (61 x 50001 x 2048 39.5 us at 768, 39.8 at 256; 128 rows 53.5 and 54.3).
+// Results that leave in bf16, 16384 at a time: the loss is then 280 units of 2^-23 at most, a hundredth of their own
+// rounding, whatever the depth (of a weight gradient the number of rows).
+constexpr int kPieceBlocks = 8, kFewPieceBlocks = 4, kPieceBlocksBf16 = 256;
 
 struct Maps {
     CUtensorMap a[kMmParts], b[kMmParts];
@@ -973,7 +977,7 @@ struct FewSmem {
     static constexpr int THREE = BN == 16 ? 4 : BN <= 64 ? 3 : 2;
     // Accumulators. Up to 64 tokens: a second one for results in pieces, which the epilogue's threads add up in
     // registers while the next piece is formed; with 128 (too many for registers) the first one keeps the sum, and each
-    // later piece is formed in the second and added to it before the next may begin (128 x 50001 x 2048, fp32: 52 us;
+    // later piece is formed in the second and added to it before the next may begin (128 x 50001 x 2048, fp32: 54 us;
     // 70 in two blocks of 64 tokens, which read W twice).
     static constexpr bool DRAINED = BN <= 64;
     static_assert(TWO <= MOST && 2 * (total(TWO) + 1024) <= 228 * 1024 && 3 * (total(THREE) + 1024) <= 228 * 1024, "the SM's");
@@ -1772,8 +1776,7 @@ cudaError_t run_few(const Maps& maps, Args a, const FewPlan& plan, int sms, cuda
     const int64_t tiles = ((int64_t)a.rowsB + COLS - 1) / COLS;
     const int blocks = plan.blocks, parts = plan.parts, per = plan.per;
     if (tiles * parts > INT32_MAX) return cudaErrorInvalidValue;
-    // fp32 results in pieces of 512 of depth; of 128 tokens, where a piece waits for the one before, longer ones
-    a.piece = a.out_f32 && L::DRAINED ? 8 : piece_of(per, a.out_f32);
+    a.piece = a.out_f32 ? kFewPieceBlocks : piece_of(per, false);
     const int held = per > a.piece ? 2 : 1;  // accumulators
     uint32_t cols = 32;
     while (cols < (uint32_t)(held * BN)) cols *= 2;

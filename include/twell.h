@@ -480,7 +480,7 @@ twell_status twell_grad_clip(const twell_tensor_list* list, float max_norm, floa
  * otherwise outputs and ws must not overlap inputs or one another (the calls reject
  * equal pointers, and y = res with another stride).
  * Sums are fp32, the tensor cores', which drop what does not fit towards zero, over at
- * most 768 of depth for fp32 results and 16384 for bf16 ones, joined with rounding;
+ * most 512 of depth for fp32 results and 16384 for bf16 ones, joined with rounding;
  * outputs are rounded once.
  *
  * twell_linear_bwd: dy [M, N] bf16; pre as the forward kept it (NULL if act is
