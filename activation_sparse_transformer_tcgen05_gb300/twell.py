@@ -649,7 +649,7 @@ def twell_linear_bwd(dy, x, W, w_kn: bool, act: int, pre, dx, dW, accumulate: bo
         raise ValueError(f"W must be {'[K, N]' if w_kn else '[N, K]'} with x's width K = {K}, got {list(W.shape)}")
     if dW is not None and dW.shape != W.shape:
         raise ValueError(f"dW must have W's shape {list(W.shape)}, got {list(dW.shape)}")
-    tw = _dtype(dW, "dW") if dW is not None else DTYPE_BF16
+    tw = _dtype(dW, "dW") if dW is not None else DTYPE_F32  # (fp32 may be added to, whether there is one or not)
     pg, ldg = _rows(dy, "dy", M, N, DTYPE_BF16)
     px, ldx = _rows(x, "x", M, K, DTYPE_BF16)
     pp, ldp = _rows(pre, "pre", M, N, DTYPE_BF16)
@@ -692,7 +692,7 @@ def twell_dense_gated_ffn_bwd(x, W_gate, W_up, W_down, act: int, g, u, h, dy, l1
     M, d, F = _gated_sizes(x, W_gate, W_up, W_down)
     _shapes(g=(g, M, F), u=(u, M, F), h=(h, M, F), dy=(dy, M, d), dx=(dx, M, d), dW_gate=(dW_gate, F, d), dW_up=(dW_up, F, d),
             dW_down=(dW_down, F, d))
-    tw = _dtype(dW_gate, "dW_gate") if dW_gate is not None else DTYPE_BF16
+    tw = _dtype(dW_gate, "dW_gate") if dW_gate is not None else DTYPE_F32
     _check(load_library().twell_dense_gated_ffn_bwd(
         _vec(x, "x", M * d, DTYPE_BF16), _vec(W_gate, "W_gate", F * d, DTYPE_BF16), _vec(W_up, "W_up", F * d, DTYPE_BF16),
         _vec(W_down, "W_down", F * d, DTYPE_BF16), act, _vec(g, "g", M * F, DTYPE_BF16), _vec(u, "u", M * F, DTYPE_BF16),
