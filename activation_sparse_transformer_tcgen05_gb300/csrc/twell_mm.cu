@@ -30,6 +30,8 @@
 #include "launch.h"
 #include "mm.h"
 
+#include <atomic>
+
 namespace twell {
 namespace {
 
@@ -1586,12 +1588,14 @@ struct AtOnce {
 template <int EPI, bool A_MN, bool B_MN, int JOBS>
 cudaError_t clusters_at_once(AtOnce* out)
 {
-    static AtOnce known[64] = {{{0}}};
+    // (one word for a device, so that threads whose first calls meet see all three numbers or none)
+    static std::atomic<uint64_t> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (known[dev].n[0] <= 0) {
+    uint64_t all = known[dev].load(std::memory_order_relaxed);
+    if (all == 0) {
         auto kern = k_mm_pair<EPI, A_MN, B_MN, JOBS>;
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<EPI>::TOTAL);
         if (e != cudaSuccess) return e;
@@ -1604,7 +1608,7 @@ cudaError_t clusters_at_once(AtOnce* out)
         cfg.dynamicSmemBytes = Smem<EPI>::TOTAL;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        for (int i = 2; i >= 0; --i) {  // (the first entry last: it says that all are known)
+        for (int i = 0; i < 3; ++i) {
             if (i > 0 && (EPI != LINEAR || JOBS > 1)) continue;
             int n = 0;
             attr[0].val.clusterDim.x = 2u << i;
@@ -1613,10 +1617,11 @@ cudaError_t clusters_at_once(AtOnce* out)
             if (e != cudaSuccess && i == 0) return e;
             if (e != cudaSuccess) (void)cudaGetLastError();
             if (n <= 0 && i == 0) return cudaErrorNotSupported;
-            known[dev].n[i] = e == cudaSuccess ? n : 0;
+            if (e == cudaSuccess) all |= (uint64_t)(n & 0xffff) << (16 * i);
         }
+        known[dev].store(all, std::memory_order_relaxed);
     }
-    *out = known[dev];
+    for (int i = 0; i < 3; ++i) out->n[i] = (int)(all >> (16 * i) & 0xffff);
     return cudaSuccess;
 }
 
