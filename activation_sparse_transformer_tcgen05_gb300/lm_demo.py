@@ -231,7 +231,8 @@ class TorchAdam:
 
 
 class TwellAdamW:
-    """The norm by twell_grad_clip, everything else in one twell_adamw: clipping, states of 32 or 8 bits, bf16 copies."""
+    """The norm by twell_grad_clip, everything else in one twell_adamw: clipping, states of 32 or 8 bits, bf16 copies.
+    A norm that is not finite drops the step."""
 
     def __init__(self, model, lr: float, max_norm: float, bits: int = 32, weight_decay: float = 0.0, seed: int = 0):
         self.model, self.max_norm, self.weight_decay, self.seed = model, max_norm, weight_decay, seed

@@ -761,7 +761,8 @@ class TwellAdamWList:
 def twell_adamw(tensors: TwellAdamWList, lr, step, beta1: float, beta2: float, eps: float, weight_decay: float, norm,
                 max_norm: float, seed: int, stream=None):
     """One AdamW step in place. lr (fp32 [1]) and step (int32 [1], 1 for the first) are read on the device; norm (fp32 [1],
-    or None): the gradients count scaled so that it is at most max_norm."""
+    or None): the gradients count scaled so that it is at most max_norm. A norm that is not finite drops the step: nothing
+    changes, and norm is the only sign of it."""
     if step.dtype is not torch.int32:
         raise ValueError(f"step must be int32, got {step.dtype}")
     _check(load_library().twell_adamw(tensors.ref, _vec(lr, "lr", 1, DTYPE_F32), _ptr(step, "step", numel=1), beta1, beta2, eps,

@@ -548,7 +548,10 @@ twell_status twell_dense_gated_ffn_bwd(const uint16_t* x, const uint16_t* W_gate
  * lr [1] fp32 and step [1] int32 (t, 1 for the first step) are read on the device, so
  * that a captured call follows them; norm [1] fp32 as twell_grad_clip writes it (with
  * an infinite bound), or NULL: c = 1. Gradients are read only. With a norm that is not
- * finite, or a step below 1, the call changes nothing. beta1, beta2 in [0, 1), eps >= 2^-126, weight_decay >= 0.
+ * finite, or a step below 1, the call changes nothing, and *norm, which the caller
+ * holds, is the only sign of it. That drops the step of finite gradients whose norm
+ * passes fp32's range (2^128) too; twell_grad_clip with a finite bound scales those,
+ * after which norm = NULL takes the step. beta1, beta2 in [0, 1), eps >= 2^-126, weight_decay >= 0.
  * The list is a host struct of host arrays (read during the call): n tensors, device
  * addresses, element counts (>= 0). param and grad bf16 or fp32 (twell_dtype codes);
  * copy (the array or any entry may be NULL): a bf16 copy of an fp32 param. Tensors are
