@@ -62,9 +62,10 @@ struct Smem {
 // units of 2^-23 of the result, over 1024 by 7, over 4096 by 31 to 70, over 16384 four times that. Results that leave in
 // fp32, and the dh that db is summed from, are therefore summed 512 at a time and the pieces added up with rounding: 4.8e-7
 // off 64 bits in norm at any depth, where fp32 matrix products by torch are 2.5e-7 (depth 1000), 6.1e-7 (4096) and 9.6e-7
-// (8192) off. Both sides of the length: 768, 7.2e-7; 256, 2.5e-7. Linear backward 8192 x 4096 -> 16384 with fp32 dW 1266 us at 768, 1289
-// at 512, 1341 at 256; gated backward 8192 x 4096 x 14336 with bf16 dW 3144, 3189 and 3273. Up to 128 rows (k_mm_few), whose
-// time goes into W, 256 at a time costs 0 to 1 us (61 x 50001 x 2048 39.5 us at 768, 39.8 at 256; 128 rows 53.5 and 54.3).
+// (8192) off. Both sides of the length: 768, 7.2e-7; 256, 2.5e-7. Linear backward 8192 x 4096 -> 16384 with fp32 dW 1266 us
+// at 768, 1289 at 512, 1341 at 256; gated backward 8192 x 4096 x 14336 with bf16 dW 3144, 3189 and 3273. Few rows (k_mm_few),
+// whose time goes into W, 256 at a time, which costs 0 to 1 us (61 x 50001 x 2048 39.5 us at 768, 39.8 at 256; 128 rows
+// 53.5 and 54.3).
 // Results that leave in bf16, 16384 at a time: the loss is then 280 units of 2^-23 at most, a hundredth of their own
 // rounding, whatever the depth (of a weight gradient the number of rows).
 constexpr int kPieceBlocks = 8, kFewPieceBlocks = 4, kPieceBlocksBf16 = 256;
